@@ -1,0 +1,657 @@
+// Attention of new tokens over the 4-bit key/value cache, GB300 (sm_103a):
+// the kernel for few query rows (decode, verification of drafts) and the one
+// that joins divided items.  Contract: hs_kv4_attention in hs.h.
+//
+// Mathematics.  With k_j = s_jg c_jd + b_jg (g the channel's group of 64),
+//   q . k_j = sum_g s_jg (q . c_j)_g + b_jg (sum of q over g),
+// so the matrix product runs on the codes themselves, and a key's scales act
+// on one number per row.  The values' scales fold into the probabilities,
+//   o_d = sum_j (p_j s_jg) c_jd + sum_j p_j b_jg,
+// the first sum a matrix product on codes, the second one number per (row,
+// group).  A code becomes an fp16 operand by masking alone: the four bits of
+// nibble 0 (of each half of a word) are the subnormal c * 2^-24 and those of
+// nibble 1 c * 2^-20, exact, five logic instructions for eight codes; the
+// powers of two go into q (per channel) and the output.  Query rows are scaled
+// by a power of two so that their largest channel is near 1: bf16 values then
+// lose nothing as fp16.
+#include "hs_kv4_sched.cuh"
+
+namespace hs {
+
+constexpr int kKvMaxCtas = 456;   // three CTAs on each of 152 SMs
+constexpr int kKvWsRows = 2 * 152 * 64;  // rows of partial sums of the widest launch
+constexpr float kLazy = 8.f;      // a row's maximum may lag by a factor 2^8 before the sums are rescaled
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D += A * B, one 16 x 8 x 16 product of fp16 operands in fp32.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float bf16_f32(uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); }
+
+template <int D, int RT, int KW>
+struct DecodeCfg {
+    static constexpr int kNg = D / 64;
+    static constexpr int kTiles = 2;                  // 64-key tiles of a ring stage
+    static constexpr int kStages = 3;
+    static constexpr int kStageBytes = kTiles * kv_record_bytes(kKvTile, D);
+    static constexpr int kWarps = RT * KW;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kCtas = RT > 1 ? 1 : D == 64 ? 3 : 2;  // resident on an SM
+    static constexpr int kO = 32 * kNg;               // accumulators of a thread
+    static constexpr int kMergeBytes = RT * (KW / 2) * (kO + 4) * 128;
+    static constexpr int kRows = 16 * RT;
+    static int smem(int n_seqs) {
+        return kStages * kStageBytes + kMergeBytes + 256 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16;
+    }
+};
+
+// What warp 0 knows of the ring's next stage.
+struct KvLoad {
+    KvWalk w;            // behind that stage
+    int tiles, head;     // of it (0 tiles: the run is done)
+};
+
+// Warp (rt, kw): rows 16 rt .. 16 rt + 15 of the item's row tile, the 16-key
+// steps kw, kw + KW, ... of every ring stage.  Warp 0 also keeps the ring full:
+// a stage is up to two 64-key tiles of one item, copied as whole page records
+// by one bulk copy a page; the pages of the stage after the next are looked up
+// while the earlier ones are on their way.  In the fragments of a
+// step, column n of key block j stands for key 8 j + n / 2 + 4 (n % 2), and
+// the k index runs over the channels in the order in which the nibbles of a
+// word come apart; both orders are free as long as the two operands agree.
+template <int D, int RT, int KW>
+__global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, RT, KW>::kCtas)) kv4_decode_kernel(const KvAttnArgs a) {
+    using C = DecodeCfg<D, RT, KW>;
+    constexpr int NG = C::kNg;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;
+    float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes + C::kMergeBytes);
+    uint64_t* empty = full + C::kStages;
+    uint32_t* absent = reinterpret_cast<uint32_t*>(empty + C::kStages);  // per stage: 16-key steps that are not there
+    long long* cum = reinterpret_cast<long long*>(full + 32);
+    int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
+    int* ls = qs + a.n_seqs + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, C::kWarps);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    kv_schedule(a, qs, ls, cum);
+    __shared__ KvLoad load;
+    // The place in the line, kept in shared memory (a copy a warp, every lane
+    // writing the same): it is looked at once an item, and registers are short.
+    __shared__ KvWalk walks[C::kWarps];
+    KvWalk& w = walks[warp];
+    w = kv_begin(a, qs, ls, cum);
+    __syncwarp();
+    const int P = 1 << a.g.page_log2;
+
+    const int per_tile = kKvTile >> a.g.page_log2;
+
+    // ---- the ring's loads (warp 0)
+    uint32_t loads = 0;
+    int page = -1;  // lane l: page l of the next stage
+    auto look_up = [&]() {
+        KvWalk v = load.w;
+        const int tiles = v.left > 0 ? min(C::kTiles, (int)min(v.left, (long long)(v.units - v.tile))) : 0;
+        if (tiles) {
+            const int p = (v.lo + v.tile) * per_tile + lane;
+            const bool in = lane < tiles * per_tile && v.hi >= v.lo && p < (v.len + P - 1) >> a.g.page_log2;
+            page = in ? a.table[(size_t)v.seq * a.width + p] : -1;
+            if (lane == 0) load.head = v.head;
+            v.left -= tiles;
+            v.tile += tiles;
+            if (v.tile == v.units && v.left > 0) kv_next_item(a, qs, ls, v);
+        }
+        __syncwarp();
+        if (lane == 0) {
+            load.w = v;
+            load.tiles = tiles;
+        }
+        __syncwarp();
+    };
+    auto refill = [&]() -> bool {
+        const int tiles = load.tiles;
+        if (!tiles) return true;
+        const int st = loads % C::kStages;
+        if (loads >= C::kStages && !mbar_wait(empty + st, (loads / C::kStages + 1) & 1)) return false;
+        const bool here = page >= 0 && page < a.g.n_pages;
+        const unsigned mask = __ballot_sync(~0u, here);
+        if (lane == 0) {
+            uint32_t gone = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * C::kTiles; ++i)
+                if (!((mask >> (i * 16 >> a.g.page_log2)) & 1u)) gone |= 1u << i;
+            absent[st] = gone;
+            mbar_arrive_expect_tx(full + st, (uint32_t)__popc(mask) * (uint32_t)a.g.rec);
+        }
+        __syncwarp();
+        if (here)
+            bulk_g2s(ring + st * C::kStageBytes + lane * a.g.rec, kv_record(a.g, page, load.head), (uint32_t)a.g.rec,
+                     full + st, policy_evict_first());
+        ++loads;
+        look_up();
+        return true;
+    };
+    if (warp == 0) {
+        if (lane == 0) load.w = w;
+        __syncwarp();
+        look_up();
+        for (int i = 0; i < C::kStages; ++i) refill();  // nothing to wait for yet
+    }
+
+    // ---- the items
+    const int rt = warp / KW, kw = warp % KW, g = lane >> 2, t = lane & 3;  // fragment row or column, and pair
+    const int half_b = (D / 2) << a.g.page_log2, pairs_b = (NG * 4) << a.g.page_log2;
+    uint32_t it = 0;
+    int4 meta = make_int4(0, 0, 0, 0);
+    while (w.left > 0) {
+        const int cnt = (int)min(w.left, (long long)(w.units - w.tile));
+        const int ctx = w.len - w.n;
+        // this thread's two rows: query rows and the last key each sees; the first one is back_keys before it
+        uint32_t Q[4 * NG][4];
+        float sc[2], sq[NG][2];
+        int lim[2];
+        int min_lim = INT_MAX, max_lim = -1;  // over the warp's rows that exist
+        const int back_keys = a.window ? a.window - 1 : 0x3fffffff;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int row = rt * 16 + g + 8 * x, tok = w.r * a.tq + row / a.group;
+            const bool valid = row < a.tq * a.group && tok < w.n;
+            lim[x] = ctx + tok;
+            if (valid) min_lim = min(min_lim, lim[x]), max_lim = max(max_lim, lim[x]);
+            uint4 v[NG][2];
+            float top = 0.f;
+            const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row % a.group) * a.q_sh;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                float sum = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float f = bf16_f32(u[e >> 1], e & 1);
+                        top = fmaxf(top, fabsf(f));
+                        sum += f;
+                    }
+                }
+                sum += __shfl_xor_sync(~0u, sum, 1);
+                sq[i][x] = sum + __shfl_xor_sync(~0u, sum, 2);
+            }
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            // f = 2^-e with 2^e <= top < 2^(e+1); rows of zeros and of infinities keep f = 1
+            int e = (int)((__float_as_uint(top) >> 23) & 255u);
+            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float f8 = f * 256.f, f4 = f * 16.f;  // the even nibbles stand for c * 2^-24, the odd ones for c * 2^-20
+            sc[x] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 65536.f;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                sq[i][x] *= f * (1.f / 65536.f);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {  // nibbles (2j, 2j + 4) and (2j + 1, 2j + 5)
+                        Q[(i * 2 + h) * 2 + j][x] = pack_half2(bf16_f32(u[j], 0) * f8, bf16_f32(u[j + 2], 0) * f8);
+                        Q[(i * 2 + h) * 2 + j][2 + x] = pack_half2(bf16_f32(u[j], 1) * f4, bf16_f32(u[j + 2], 1) * f4);
+                    }
+                }
+            }
+        }
+        max_lim = warp_max_s32(max_lim);
+        min_lim = -warp_max_s32(-min_lim);
+        const int min_from = max_lim < 0 ? 0 : min_lim - back_keys, max_from = max_lim - back_keys;
+
+        float O[NG][8][4];
+        float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, bs[NG][2];
+        uint32_t eb = 0;          // exponent field of the largest value scale so far
+        float ke = 2097152.f;     // 2^(21 - eb): probability * scale * ke stays below 2^15
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            bs[i][0] = bs[i][1] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) O[i][n][e] = 0.f;
+        }
+
+        int tile_key = (w.lo + w.tile) * kKvTile;
+        for (int k = 0; k < cnt; k += C::kTiles, ++it, tile_key += C::kTiles * kKvTile) {
+            if (warp == 0 && it && !refill()) return;  // the stage of the iteration before
+            const int st = it % C::kStages;
+            const int steps = min(C::kTiles, cnt - k) * 4;
+            if (!mbar_wait(full + st, (it / C::kStages) & 1)) return;
+            const uint32_t gone = absent[st];
+            const uint8_t* stage = ring + st * C::kStageBytes;
+#pragma unroll 1
+            for (int step = kw; step < steps; step += KW) {
+                const int key0 = tile_key + step * 16;
+                if ((gone >> step) & 1u || key0 > max_lim || key0 + 15 < min_from) continue;
+                const bool masked = key0 + 15 > min_lim || key0 < max_from;
+                const int in_tile = step * 16, off = in_tile & (P - 1);
+                const uint8_t* rec = stage + (in_tile >> a.g.page_log2) * a.g.rec;
+
+                float S[NG][2][4];
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) S[i][j][0] = S[i][j][1] = S[i][j][2] = S[i][j][3] = 0.f;
+                uint2 kc[2][NG];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+                        kc[j][i] = *reinterpret_cast<const uint2*>(rec + (off + 8 * j + (g >> 1) + 4 * (g & 1)) * (D / 2) + i * 32 + t * 8);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            const uint32_t c = h ? kc[j][i].y : kc[j][i].x, c8 = c >> 8;
+                            mma_16816(S[i][j], Q[(i * 2 + h) * 2], c & 0x000f000fu, c & 0x00f000f0u);
+                            mma_16816(S[i][j], Q[(i * 2 + h) * 2 + 1], c8 & 0x000f000fu, c8 & 0x00f000f0u);
+                        }
+                // the pairs of this thread's four keys; what lies behind the last key may be anything
+                uint32_t kp[4][NG];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint8_t* pk = rec + 2 * half_b + (off + 4 * c + t) * (NG * 4);
+                    const bool there = !masked || key0 + 4 * c + t < w.len;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        kp[c][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
+                    }
+                }
+                float s[2][4];  // [row][key]
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float2 p[NG];
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) p[i] = half2_to_float2(kp[c][i]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            v = i ? fmaf(p[i].x, S[i][c >> 1][2 * x + (c & 1)], v) : p[i].x * S[i][c >> 1][2 * x + (c & 1)];
+                            v = fmaf(p[i].y, sq[i][x], v);
+                        }
+                        if (masked) {
+                            const int key = key0 + 4 * c + t;
+                            if (key > lim[x] || key < lim[x] - back_keys) v = -INFINITY;
+                        }
+                        s[x][c] = v;
+                        mx[x] = fmaxf(mx[x], v);
+                    }
+                }
+                uint32_t top = 0, vp[4][NG];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint8_t* pk = rec + 2 * half_b + pairs_b + (off + 4 * c + t) * (NG * 4);
+                    const bool there = !masked || key0 + 4 * c + t < w.len;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) vp[c][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) top = max(top, vp[c][i] & 0x7fffu);
+                top = warp_max_u32(top) >> 10;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 1));
+                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 2)) * sc[x];
+                }
+                if (__any_sync(~0u, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy) || top > eb) {
+                    const uint32_t neb = max(eb, top);
+                    const float back = __uint_as_float((127u + eb - neb) << 23);
+                    eb = neb;
+                    ke = __uint_as_float((148u - neb) << 23);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float nm = fmaxf(m[x], mx[x]), f = ex2(m[x] - nm);
+                        m[x] = nm;
+                        l[x] *= f;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            bs[i][x] *= f;
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                O[i][n][2 * x] *= f * back;
+                                O[i][n][2 * x + 1] *= f * back;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[x][c] = ex2(fmaf(s[x][c], sc[x], -m[x]));
+                        l[x] += s[x][c];
+                    }
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    uint32_t A[4];
+#pragma unroll
+                    for (int c = 0; c < 4; c += 2) {
+                        const float2 p0 = half2_to_float2(vp[c][i]), p1 = half2_to_float2(vp[c + 1][i]);
+                        const float s0 = p0.x * ke, s1 = p1.x * ke;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float e0 = s[x][c], e1 = s[x][c + 1];
+                            float b0 = e0 * p0.y, b1 = e1 * p1.y, v0 = e0 * s0, v1 = e1 * s1;
+                            if (masked) {  // a key that the row does not see may hold a NaN
+                                if (e0 == 0.f) b0 = v0 = 0.f;
+                                if (e1 == 0.f) b1 = v1 = 0.f;
+                            }
+                            bs[i][x] += b0 + b1;
+                            A[c + x] = pack_half2(v0, v1);
+                        }
+                    }
+                    const uint8_t* pv = rec + half_b + (off + t) * (D / 2) + i * 32 + g * 4;
+                    uint32_t c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e] = *reinterpret_cast<const uint32_t*>(pv + 4 * e * (D / 2));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x = __byte_perm(c[0], c[1], h ? 0x7632 : 0x5410);
+                        uint32_t y = __byte_perm(c[2], c[3], h ? 0x7632 : 0x5410);
+                        mma_16816(O[i][4 * h], A, x & 0x000f000fu, y & 0x000f000fu);
+                        mma_16816(O[i][4 * h + 1], A, x & 0x00f000f0u, y & 0x00f000f0u);
+                        x >>= 8;
+                        y >>= 8;
+                        mma_16816(O[i][4 * h + 2], A, x & 0x000f000fu, y & 0x000f000fu);
+                        mma_16816(O[i][4 * h + 3], A, x & 0x00f000f0u, y & 0x00f000f0u);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st);
+        }
+
+        // ---- the piece's sums: over the four threads of a row, then over the key warps
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            l[x] += __shfl_xor_sync(~0u, l[x], 1);
+            l[x] += __shfl_xor_sync(~0u, l[x], 2);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                bs[i][x] += __shfl_xor_sync(~0u, bs[i][x], 1);
+                bs[i][x] += __shfl_xor_sync(~0u, bs[i][x], 2);
+            }
+        }
+        const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / ke
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    O[i][n][e] = fmaf(O[i][n][e], n & 1 ? even * 0.0625f : even, bs[i][e >> 1]);
+#pragma unroll
+        for (int half = KW / 2; half; half >>= 1) {
+            if (kw >= half && kw < 2 * half) {
+                float* b = merge + (rt * (KW / 2) + kw - half) * (C::kO + 4) * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) b[((i * 8 + n) * 4 + e) * 32] = O[i][n][e];
+                b[C::kO * 32] = m[0], b[(C::kO + 1) * 32] = m[1];
+                b[(C::kO + 2) * 32] = l[0], b[(C::kO + 3) * 32] = l[1];
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
+            if (kw < half) {
+                const float* b = merge + (rt * (KW / 2) + kw) * (C::kO + 4) * 32 + lane;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float om = b[(C::kO + x) * 32], nm = fmaxf(m[x], om);
+                    const float f0 = ex2(m[x] - nm), f1 = ex2(om - nm);
+                    m[x] = nm;
+                    l[x] = l[x] * f0 + b[(C::kO + 2 + x) * 32] * f1;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+#pragma unroll
+                            for (int e = 2 * x; e < 2 * x + 2; ++e)
+                                O[i][n][e] = O[i][n][e] * f0 + b[((i * 8 + n) * 4 + e) * 32] * f1;
+                            if (n % 4 == 3) asm volatile("" ::: "memory");  // no more loads in flight than registers hold
+                        }
+                }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
+        }
+
+        const bool whole = w.tile == 0 && cnt == w.units;
+        if (!whole && w.tile == 0) {  // the item goes on in the next CTAs
+            const long long total = cum[a.n_seqs];
+            const int active = kv_active(a, total);
+            const long long end = kv_cut(total, blockIdx.x + 1, active) - cnt + w.units;
+            meta = make_int4((int)((end * active - 1) / total) - (int)blockIdx.x + 1, w.seq, w.head, w.r);
+        }
+        if (kw == 0) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = rt * 16 + g + 8 * x, tok = w.r * a.tq + row / a.group;
+                if (row >= a.tq * a.group || tok >= w.n) continue;
+                if (whole) {
+                    const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
+                    uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row % a.group) * a.o_sh;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                u[e] = (uint32_t)f32_to_bf16_bits(O[i][2 * e][2 * x + h] * inv) |
+                                       ((uint32_t)f32_to_bf16_bits(O[i][2 * e + 1][2 * x + h] * inv) << 16);
+                            *reinterpret_cast<uint4*>(dst + i * 64 + t * 16 + h * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                } else {
+                    const size_t slot = 2 * blockIdx.x + (w.tile == 0 ? 1 : 0);
+                    float* dst = a.part_o + (slot * a.rows + row) * D;
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<float4*>(dst + i * 64 + t * 16 + h * 8 + e * 4) =
+                                    make_float4(O[i][4 * e][2 * x + h], O[i][4 * e + 1][2 * x + h],
+                                                O[i][4 * e + 2][2 * x + h], O[i][4 * e + 3][2 * x + h]);
+                    if (t == 0) a.part_ml[slot * a.rows + row] = make_float2(m[x], l[x]);
+                }
+            }
+        }
+        KvWalk next = w;
+        next.left -= cnt;
+        if (next.left > 0) kv_next_item(a, qs, ls, next);
+        __syncwarp();
+        w = next;
+        __syncwarp();
+    }
+    if (tid == 0) a.meta[blockIdx.x] = meta;
+}
+
+// Joins the pieces of an item that several CTAs worked on: block (c, y) the
+// rows y, y + gridDim.y, ... of the item that began in CTA c and did not end
+// there.  The pieces are added in the order of the keys.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const KvAttnArgs a) {
+    constexpr int kLanes = D / 4, kSets = 128 / kLanes;
+    __shared__ float wt[kKvMaxCtas];
+    __shared__ float red[4], l_s[kSets];
+    __shared__ float4 acc_s[kSets][kLanes];
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x, tid = threadIdx.x;
+    const int4 meta = a.meta[c];
+    if (!meta.x) return;
+    const int row0 = min(max(a.q_start[meta.y], 0), a.n_tokens);
+    const int n = min(max(a.q_start[meta.y + 1], 0), a.n_tokens) - row0;
+    auto slot = [&](int i) { return (size_t)(i ? 2 * (c + i) : 2 * c + 1); };
+    for (int row = blockIdx.y; row < a.tq * a.group; row += gridDim.y) {
+        const int tok = meta.w * a.tq + row / a.group;
+        if (tok >= n) break;
+        float m = -1e30f;
+        for (int i = tid; i < meta.x; i += 128) m = fmaxf(m, a.part_ml[slot(i) * a.rows + row].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if ((tid & 31) == 0) red[tid >> 5] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        for (int i = tid; i < meta.x; i += 128) wt[i] = ex2(a.part_ml[slot(i) * a.rows + row].x - m);
+        __syncthreads();
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int set = tid / kLanes, d4 = tid % kLanes;
+#pragma unroll 8
+        for (int i = set; i < meta.x; i += kSets) {
+            const float f = wt[i];
+            const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * a.rows + row) * D)[d4];
+            l += f * a.part_ml[slot(i) * a.rows + row].y;
+            acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+        }
+        acc_s[set][d4] = acc;
+        if (d4 == 0) l_s[set] = l;
+        __syncthreads();
+        if (tid < kLanes) {
+            float sum = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) {
+                const float4 v = acc_s[i][tid];
+                sum += l_s[i];
+                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+            }
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
+            uint2 u;
+            u.x = (uint32_t)f32_to_bf16_bits(acc.x * inv) | ((uint32_t)f32_to_bf16_bits(acc.y * inv) << 16);
+            u.y = (uint32_t)f32_to_bf16_bits(acc.z * inv) | ((uint32_t)f32_to_bf16_bits(acc.w * inv) << 16);
+            *reinterpret_cast<uint2*>(a.out + (long long)(row0 + tok) * a.o_st +
+                                      (long long)(meta.z * a.group + row % a.group) * a.o_sh + tid * 4) = u;
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int RT, int KW>
+int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
+    using C = DecodeCfg<D, RT, KW>;
+    const int smem = C::smem(a.n_seqs);
+    const int st = hs_host::set_smem_attr((const void*)kv4_decode_kernel<D, RT, KW>, C::smem(kKvMaxSeqs));
+    if (st != HS_OK) return st;
+    a.rows = C::kRows;
+    a.tq = C::kRows / a.group;
+    a.min_units = 2;
+    const int ctas = std::min(152, sms) * C::kCtas;
+    static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
+    if (hs_host::launch_pdl(kv4_decode_kernel<D, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
+        return HS_ERR_CUDA;
+    if (hs_host::launch_pdl(kv4_combine_kernel<D>, dim3(ctas, 16), dim3(128), 0, s, a) != cudaSuccess) return HS_ERR_CUDA;
+    return HS_OK;
+}
+
+}  // namespace hs
+
+using namespace hs_host;
+
+// Partial sums, (maximum, sum) pairs and item records of the widest launch.
+static size_t kv4_ws_bytes(int dim) {
+    const size_t rows = hs::kKvWsRows;
+    return round_up(rows * dim * 4, 256) + round_up(rows * 8, 256) + hs::kKvMaxCtas * 16;
+}
+
+extern "C" size_t hs_kv4_attention_workspace_size(const hs_kv4_cache* c, int n_seqs, int n_q_heads) {
+    if (!c || !kv4_shape_ok(c) || n_seqs < 1 || n_seqs > hs::kKvMaxSeqs || n_q_heads < c->n_kv_heads ||
+        n_q_heads % c->n_kv_heads || n_q_heads / c->n_kv_heads > 64)
+        return 0;
+    return kv4_ws_bytes(c->head_dim);
+}
+
+extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, long long q_st, long long q_sh,
+                                const int* q_start, const int* seq_len, const int* table, int table_width, int n_seqs,
+                                int n_tokens, int n_q_heads, int max_new, float scale, int window, uint16_t* out,
+                                long long o_st, long long o_sh, void* ws, size_t ws_bytes, hs_stream_t stream) {
+    const int st = kv4_check(cache);
+    if (st != HS_OK) return st;
+    if (!q || !q_start || !seq_len || !table || !out || table_width < 1 || n_seqs < 1 || n_tokens < 0 || max_new < 0 ||
+        window < 0 || !(scale > 0.f) || scale > 1e30f)
+        return HS_ERR_INVALID_ARG;
+    if (n_q_heads < cache->n_kv_heads || n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 64 ||
+        n_seqs > hs::kKvMaxSeqs || (long long)table_width * cache->page_tokens >= (1ll << 31))
+        return HS_ERR_UNSUPPORTED_SHAPE;
+    if (!al16(q) || !al16(out) || (q_st | q_sh | o_st | o_sh) & 7 || !al4(q_start) || !al4(seq_len) || !al4(table))
+        return HS_ERR_MISALIGNED;
+    if (!ws || ws_bytes < kv4_ws_bytes(cache->head_dim)) return HS_ERR_WORKSPACE;
+    if (!al16(ws)) return HS_ERR_MISALIGNED;
+    if (!n_tokens) return HS_OK;
+    const int sms = sm_count();
+    if (!sms) return HS_ERR_CUDA;
+    const int dim = cache->head_dim;
+    const size_t rows = hs::kKvWsRows;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    hs::KvAttnArgs a = {};
+    a.g = kv4_geom(cache);
+    a.q = q, a.q_st = q_st, a.q_sh = q_sh;
+    a.out = out, a.o_st = o_st, a.o_sh = o_sh;
+    a.q_start = q_start, a.seq_len = seq_len, a.table = table;
+    a.width = table_width, a.n_seqs = n_seqs, a.n_tokens = n_tokens;
+    a.group = n_q_heads / cache->n_kv_heads;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.part_o = reinterpret_cast<float*>(w);
+    a.part_ml = reinterpret_cast<float2*>(w + round_up(rows * dim * 4, 256));
+    a.meta = reinterpret_cast<int4*>(w + round_up(rows * dim * 4, 256) + round_up(rows * 8, 256));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // Row tiles of 16, 32 or 64: the smallest that holds a request's rows.
+    const long long need = std::max((long long)max_new, 1ll) * a.group;
+    int r;
+    if (dim == 64)
+        r = need <= 16 ? hs::launch_decode<64, 1, 4>(a, sms, s)
+                       : need <= 32 ? hs::launch_decode<64, 2, 4>(a, sms, s) : hs::launch_decode<64, 4, 2>(a, sms, s);
+    else
+        r = need <= 16 ? hs::launch_decode<128, 1, 4>(a, sms, s)
+                       : need <= 32 ? hs::launch_decode<128, 2, 4>(a, sms, s) : hs::launch_decode<128, 4, 2>(a, sms, s);
+    return r != HS_OK ? r : launch_err();
+}
+
+// Reads and clears this translation unit's device error word.
+unsigned hs_kv4_take_status() {
+    unsigned v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, hs::g_status, sizeof(v)) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(hs::g_status, &zero, sizeof(zero));
+    return v;
+}

@@ -1,0 +1,199 @@
+// Division of the attention's work among the CTAs of one launch, shared by
+// the kernels of hs_kv4_attention.
+//
+// An item is (request, kv head, row tile): the row tile holds TQ of the
+// request's new tokens for all G query heads of the kv head.  Its work is the
+// run of 64-key tiles that some row of it sees.  All items' tiles, in the
+// order (request, kv head, row tile, key tile), form one line that is cut into
+// equal pieces, one a CTA: long and short requests, prompts and single tokens
+// load the SMs alike, and the host needs none of the lengths.  An item that a
+// cut divides leaves partial results that the combine kernel joins.
+#pragma once
+
+#include "hs_kv4.cuh"
+
+namespace hs {
+
+constexpr int kKvTile = 64;  // keys of a tile; pages of 16 to 64 tokens divide it
+
+struct KvAttnArgs {
+    KvGeom g;
+    const uint16_t* q;
+    long long q_st, q_sh;
+    uint16_t* out;
+    long long o_st, o_sh;
+    const int* q_start;
+    const int* seq_len;
+    const int* table;
+    int width, n_seqs, n_tokens, group, window, rows, tq, min_units;
+    float scale_log2;    // scale * log2(e)
+    float* part_o;       // [2 * CTAs][rows][dim] partial sums
+    float2* part_ml;     // [2 * CTAs][rows] (maximum, sum)
+    int4* meta;          // [CTAs]: the item whose first piece ends this CTA's run: pieces (0: none), request, head, row tile
+};
+
+struct KvSpan {
+    int lo, hi;  // first and last 64-key tile of an item (hi < lo: no key, counted as one tile)
+};
+
+// Key tiles of row tile r of a request with n new tokens and length len.
+__device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int n, int len, int r) {
+    const int ctx = len - n, t0 = r * a.tq, t1 = min(n, t0 + a.tq) - 1;
+    const int last = min(ctx + t1, len - 1);
+    const int first = a.window ? max(0, ctx + t0 - a.window + 1) : 0;
+    KvSpan s;
+    if (last < 0 || first > last) {
+        s.lo = 0, s.hi = -1;
+    } else {
+        s.lo = first / kKvTile, s.hi = last / kKvTile;
+    }
+    return s;
+}
+__device__ __forceinline__ int kv_span_units(const KvSpan& s) { return max(1, s.hi - s.lo + 1); }
+
+// Where a CTA's run of units stands.
+struct KvWalk {
+    long long left;          // units of the CTA's run still to do (this one included)
+    int seq, head, r, tile;  // tile: unit within the item
+    int n, len, row0;        // of the request: new tokens, length, first row of q
+    int units;               // of the item
+    int lo, hi;
+    bool first;              // the run began inside this item
+};
+
+// The lengths the schedule goes by: a length is cut to the table's width, and
+// a count of new tokens that q_start does not ascend by is 0.
+__device__ __forceinline__ void kv_request(const KvAttnArgs& a, const int* qs, const int* ls, int i, int& n, int& len) {
+    n = max(qs[i + 1] - qs[i], 0);
+    len = (int)min((long long)max(ls[i], 0), (long long)a.width << a.g.page_log2);
+}
+
+// Fills cum[0..n_seqs] (units before each request), qs[0..n_seqs] and
+// ls[0..n_seqs) in shared memory, by all threads of the CTA.
+__device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* ls, long long* cum) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+    for (int i = tid; i <= a.n_seqs; i += nt) {
+        qs[i] = min(max(a.q_start[i], 0), a.n_tokens);  // no row outside q, whatever the device holds
+        if (i < a.n_seqs) ls[i] = a.seq_len[i];
+    }
+    __syncthreads();
+    bool many = false;  // some request has more than one row tile
+    for (int i = tid; i < a.n_seqs; i += nt) {
+        int n, len;
+        kv_request(a, qs, ls, i, n, len);
+        if (n <= a.tq)
+            cum[i + 1] = n ? (long long)a.g.heads * kv_span_units(kv_span(a, n, len, 0)) : 0;
+        else
+            many = true;
+    }
+    if (__syncthreads_or(many)) {
+        for (int i = warp; i < a.n_seqs; i += nw) {
+            int n, len;
+            kv_request(a, qs, ls, i, n, len);
+            if (n <= a.tq) continue;
+            const int tiles = (n + a.tq - 1) / a.tq;
+            int s = 0;
+            for (int r = lane; r < tiles; r += 32) s += kv_span_units(kv_span(a, n, len, r));
+            s = (int)warp_add_u32((uint32_t)s);
+            if (lane == 0) cum[i + 1] = (long long)a.g.heads * s;
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        long long base = 0;
+        for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
+            const int i = i0 + lane;
+            long long v = i < a.n_seqs ? cum[i + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(~0u, v, o);
+                if (lane >= o) v += t;
+            }
+            if (i < a.n_seqs) cum[i + 1] = base + v;
+            base += __shfl_sync(~0u, v, 31);
+        }
+        if (lane == 0) cum[0] = 0;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void kv_set_item(const KvAttnArgs& a, KvWalk& w) {
+    const KvSpan s = kv_span(a, w.n, w.len, w.r);
+    w.lo = s.lo, w.hi = s.hi, w.units = kv_span_units(s);
+}
+
+// CTAs that share the line; the first unit of CTA c is total * c / active.
+__device__ __forceinline__ int kv_active(const KvAttnArgs& a, long long total) {
+    return (int)min((long long)gridDim.x, (total + a.min_units - 1) / a.min_units);
+}
+__device__ __forceinline__ long long kv_cut(long long total, int c, int active) { return total * c / active; }
+
+// Start of this CTA's run (called by whole warps; every lane gets the same).
+__device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const long long* cum) {
+    KvWalk w;
+    const long long total = cum[a.n_seqs];
+    const int active = kv_active(a, total);
+    w.left = 0;
+    if (!total || (int)blockIdx.x >= active) return w;
+    const long long u0 = kv_cut(total, blockIdx.x, active);
+    w.left = kv_cut(total, blockIdx.x + 1, active) - u0;
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {  // the last request with cum <= u0: it has units
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= u0) lo = mid;
+        else hi = mid;
+    }
+    w.seq = lo;
+    kv_request(a, qs, ls, lo, w.n, w.len);
+    w.row0 = qs[lo];
+    const long long per_head = (cum[lo + 1] - cum[lo]) / a.g.heads;
+    long long rest = u0 - cum[lo];
+    w.head = (int)(rest / per_head);
+    rest -= (long long)w.head * per_head;
+    const int tiles = (w.n + a.tq - 1) / a.tq;
+    w.r = 0;
+    if (tiles > 1) {
+        const int lane = threadIdx.x & 31;
+        for (int r0 = 0; r0 < tiles; r0 += 32) {
+            const int mine = r0 + lane < tiles ? kv_span_units(kv_span(a, w.n, w.len, r0 + lane)) : 0;
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(~0u, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned past = __ballot_sync(~0u, mine && incl > rest);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                rest -= __shfl_sync(~0u, incl - mine, l);
+                w.r = r0 + l;
+                break;
+            }
+            rest -= __shfl_sync(~0u, incl, 31);
+        }
+    }
+    w.tile = (int)rest;
+    w.first = true;
+    kv_set_item(a, w);
+    return w;
+}
+
+// To the next item (the current one's units are done).
+__device__ __forceinline__ void kv_next_item(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w) {
+    w.first = false;
+    w.tile = 0;
+    if (++w.r * a.tq >= w.n) {
+        w.r = 0;
+        if (++w.head == a.g.heads) {
+            w.head = 0;
+            do {
+                ++w.seq;
+                kv_request(a, qs, ls, w.seq, w.n, w.len);
+            } while (!w.n);
+            w.row0 = qs[w.seq];
+        }
+    }
+    kv_set_item(a, w);
+}
+
+}  // namespace hs

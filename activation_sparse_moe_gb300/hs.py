@@ -57,6 +57,11 @@ class hs_prefill_debug(C.Structure):
                 ("live_mask", C.c_void_p), ("tile_live", C.c_void_p)]
 
 
+class hs_kv4_cache(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("n_pages", C.c_int), ("page_tokens", C.c_int), ("n_kv_heads", C.c_int),
+                ("head_dim", C.c_int)]
+
+
 _lib = None
 
 _SIGS = {
@@ -81,6 +86,18 @@ _SIGS = {
     "hs_moe_prefill_workspace_size": (C.c_size_t, [C.POINTER(hs_moe_layer), C.c_int]),
     "hs_moe_prefill": (C.c_int, [C.POINTER(hs_moe_layer), C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
                                  C.c_uint, C.POINTER(hs_prefill_debug), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hs_kv4_pool_bytes": (C.c_size_t, [C.POINTER(hs_kv4_cache)]),
+    "hs_kv4_plan": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
+                              C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                              C.c_void_p, C.c_void_p, C.c_void_p]),
+    "hs_kv4_append": (C.c_int, [C.POINTER(hs_kv4_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
+                                C.c_longlong, C.c_longlong, C.c_void_p, C.c_int, C.c_void_p]),
+    "hs_kv4_read": (C.c_int, [C.POINTER(hs_kv4_cache), C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                              C.c_void_p, C.c_void_p]),
+    "hs_kv4_attention_workspace_size": (C.c_size_t, [C.POINTER(hs_kv4_cache), C.c_int, C.c_int]),
+    "hs_kv4_attention": (C.c_int, [C.POINTER(hs_kv4_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float,
+                                   C.c_int, C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 
@@ -252,3 +269,54 @@ def hs_moe_prefill(layer: Layer, x_bf16, logits, tokens, y_bf16, y_f32=None, fla
     _check("hs_moe_prefill", lib().hs_moe_prefill(
         layer.ref, _p(x_bf16), _p(logits), tokens, _p(y_bf16), _p(y_f32), flags, dbg, _p(workspace), nb,
         _stream(stream)))
+
+
+def make_kv4_cache(pool, n_pages, page_tokens, n_kv_heads, head_dim) -> hs_kv4_cache:
+    """Descriptor of a 4-bit key/value cache; pool is a device tensor (or
+    address, or None where only sizes are asked for) that the caller keeps."""
+    return hs_kv4_cache(_p(pool), n_pages, page_tokens, n_kv_heads, head_dim)
+
+
+def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
+    return lib().hs_kv4_pool_bytes(C.byref(cache))
+
+
+def hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, table_width, ring, counters_in,
+                max_tokens, table_out, seq_len, q_start, slot, position, counters_out, short, stream=None):
+    _check("hs_kv4_plan", lib().hs_kv4_plan(
+        _p(cached_len), _p(new_len), n_seqs, page_tokens, n_pages, _p(table_in), table_width, _p(ring),
+        _p(counters_in), max_tokens, _p(table_out), _p(seq_len), _p(q_start), _p(slot), _p(position),
+        _p(counters_out), _p(short), _stream(stream)))
+
+
+def _rows(t, fn: str):
+    """Pointer and (token, head) strides of a [tokens][heads][channels] tensor."""
+    if t.stride(2) != 1:
+        raise HsError(fn, HS_ERR_INVALID_ARG)
+    return _p(t), t.stride(0), t.stride(1)
+
+
+def hs_kv4_append(cache: hs_kv4_cache, k, v, slots, n_tokens, stream=None):
+    """k, v: bf16 [tokens][kv heads][head_dim], any token and head strides."""
+    _check("hs_kv4_append", lib().hs_kv4_append(C.byref(cache), *_rows(k, "hs_kv4_append"),
+                                                *_rows(v, "hs_kv4_append"), _p(slots), n_tokens, _stream(stream)))
+
+
+def hs_kv4_read(cache: hs_kv4_cache, slots, n_tokens, k_bf16=None, v_bf16=None, k_f32=None, v_f32=None, stream=None):
+    _check("hs_kv4_read", lib().hs_kv4_read(C.byref(cache), _p(slots), n_tokens, _p(k_bf16), _p(v_bf16), _p(k_f32),
+                                            _p(v_f32), _stream(stream)))
+
+
+def hs_kv4_attention_workspace_size(cache: hs_kv4_cache, n_seqs, n_q_heads) -> int:
+    return lib().hs_kv4_attention_workspace_size(C.byref(cache), n_seqs, n_q_heads)
+
+
+def hs_kv4_attention(cache: hs_kv4_cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out,
+                     workspace=None, workspace_bytes=None, stream=None):
+    """q, out: bf16 [tokens][query heads][head_dim], any token and head
+    strides; table: int32 [n_seqs][table_width] contiguous."""
+    nb = workspace_bytes if workspace_bytes is not None else (workspace.numel() * workspace.element_size()
+                                                              if workspace is not None else 0)
+    _check("hs_kv4_attention", lib().hs_kv4_attention(
+        C.byref(cache), *_rows(q, "hs_kv4_attention"), _p(q_start), _p(seq_len), _p(table), table.shape[1], n_seqs,
+        q.shape[0], q.shape[1], max_new, scale, window, *_rows(out, "hs_kv4_attention"), _p(workspace), nb, _stream(stream)))

@@ -347,6 +347,114 @@ int hs_moe_prefill(const hs_moe_layer* layer, const uint16_t* x_bf16_dev, const 
                    const hs_prefill_debug* debug, void* workspace_dev, size_t workspace_bytes,
                    hs_stream_t stream);
 
+/* ------------------------------------------------- 4-bit key/value cache
+ * The cache of one attention layer (the model the page serves has attention
+ * layers between its MoE layers; the page gives them no section), held in the
+ * library's 4-bit affine format with groups of 64 channels, in pages that
+ * requests own through block tables.  Four calls run it without the host
+ * knowing any length: hs_kv4_plan once a step, then for every layer
+ * hs_kv4_append and hs_kv4_attention; hs_kv4_read gives cached rows back.
+ *
+ * Pool layout: [n_pages][n_kv_heads][record], one record a (page, kv head):
+ *   K codes [page_tokens][head_dim/2], V codes [page_tokens][head_dim/2],
+ *   K pairs [page_tokens][head_dim/64], V pairs [page_tokens][head_dim/64]
+ * codes two a byte (even channel in the low nibble), pairs (scale, bias) fp16
+ * with scale >= 0; a channel stands for scale * code + bias.
+ * A token's slot is page * page_tokens + offset (int64); -1 means none. */
+typedef struct {
+    void* pool;        /* device, 16-byte aligned, hs_kv4_pool_bytes bytes */
+    int   n_pages;     /* >= 1 */
+    int   page_tokens; /* 16, 32 or 64 */
+    int   n_kv_heads;  /* 1..256 */
+    int   head_dim;    /* 64 or 128 */
+} hs_kv4_cache;
+
+/* Bytes of the pool; 0 for sizes outside the ranges above.  (pool is not read.) */
+size_t hs_kv4_pool_bytes(const hs_kv4_cache* cache);
+
+/* Block tables, slot map, positions and row starts of one step, from the
+ * requests' lengths, all on the device.  Request i holds cached_len[i] tokens
+ * (negative counts as 0) in the first ceil(cached_len/page_tokens) entries of
+ * its row of table_in, and gets new_len[i] more; new_len[i] < 0 means that it
+ * has ended.  Free pages stand in a ring: entries counters_in[0] up to, not
+ * including, counters_in[1] (both modulo n_pages) of ring.  New pages are
+ * taken from its front in the order of the requests; the pages of ended
+ * requests go to its end, in request and table order, and are not taken again
+ * by the same call.
+ *   cached_len_dev, new_len_dev [n_seqs];  table_in_dev [n_seqs][table_width]
+ *   ring_dev [n_pages] in and out;  counters_in_dev [2] int64
+ *   table_out_dev  [n_seqs][table_width], -1 past a request's pages; it may be
+ *                  table_in_dev, whose entries past a request's cached pages
+ *                  are then left as they are except for the new pages and the
+ *                  rows of ended requests
+ *   seq_len_dev    [n_seqs] cached + new (0 for an ended request)
+ *   q_start_dev    [n_seqs + 1] first new token of each request, and the total
+ *   slot_dev       [max_tokens] slots of the new tokens, -1 past the total
+ *   position_dev   [max_tokens] their positions, -1 past the total; or NULL
+ *   counters_out_dev [2]; must not be counters_in_dev
+ *   short_dev      [1]: 0, or the number of pages missing (in the ring, or past
+ *                  table_width) plus tokens over max_tokens.  Then the step is
+ *                  refused as a whole: no request gets a page or a token
+ *                  (q_start all 0, slots -1, seq_len = cached_len); ended
+ *                  requests still give their pages back.
+ * n_seqs 1..4096; n_seqs * table_width, max_tokens and n_pages below 2^30,
+ * table_width * page_tokens below 2^31. */
+int hs_kv4_plan(const int* cached_len_dev, const int* new_len_dev, int n_seqs, int page_tokens, int n_pages,
+                const int* table_in_dev, int table_width, int* ring_dev, const long long* counters_in_dev,
+                int max_tokens, int* table_out_dev, int* seq_len_dev, int* q_start_dev, long long* slot_dev,
+                int* position_dev, long long* counters_out_dev, int* short_dev, hs_stream_t stream);
+
+/* Writes the keys and values of n_tokens tokens into their slots.  For each
+ * group of 64 channels: scale = fp16((max - min) / 15), bias = fp16(min),
+ * code = clamp(rint((x - bias) / scale), 0, 15) (0 where scale = 0), each step
+ * in fp32, round to nearest even, as hs_requant_down_rowscale.  A group that
+ * holds an infinity or a NaN, or whose scale or bias passes the fp16 range,
+ * reads back as NaN.  A slot outside the pool (such as -1) is skipped.  Two
+ * tokens with the same slot leave one of the two in it, group by group.
+ *   k_bf16_dev, v_bf16_dev  bf16, token t and head h at t * stride_token +
+ *     h * stride_head elements (K and V each their own strides), channels
+ *     contiguous; 16-byte aligned, strides multiples of 8
+ *   slot_dev [n_tokens]
+ * n_tokens 0..2^20. */
+int hs_kv4_append(const hs_kv4_cache* cache, const uint16_t* k_bf16_dev, long long k_stride_token,
+                  long long k_stride_head, const uint16_t* v_bf16_dev, long long v_stride_token,
+                  long long v_stride_head, const long long* slot_dev, int n_tokens, hs_stream_t stream);
+
+/* Reads n_tokens slots back: scale * code + bias in fp32, as bf16 (round to
+ * nearest even) in k/v_bf16_dev or as fp32 in k/v_f32_dev, each
+ * [n_tokens][n_kv_heads][head_dim] contiguous, 16-byte aligned; each may be
+ * NULL, not all.  A slot outside the pool reads as zeros. */
+int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_tokens, uint16_t* k_bf16_dev,
+                uint16_t* v_bf16_dev, float* k_f32_dev, float* v_f32_dev, hs_stream_t stream);
+
+/* Causal attention of each request's new tokens over its cached tokens (the
+ * new ones appended before).  Request i's new tokens are rows q_start[i] to
+ * q_start[i+1] of q and sit at the end of its seq_len[i] tokens; the row at
+ * position p looks at the keys j <= p, and with window > 0 only at
+ * j > p - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * Query head h reads kv head h / (n_q_heads / n_kv_heads).  A row that sees no
+ * key gives zeros.  Table entries outside the pool (such as -1) count as
+ * tokens that are not there.  Rows past q_start[n_seqs] are not written.
+ *   q_bf16_dev, out_bf16_dev  bf16, n_tokens rows, strides as in hs_kv4_append
+ *   q_start_dev [n_seqs + 1] ascending, seq_len_dev [n_seqs]
+ *   table_dev   [n_seqs][table_width]; a length past table_width pages is cut
+ *   max_new     the largest number of new tokens of a request, or more: it
+ *               chooses the kernel, not the result
+ *   scale       > 0 and finite;  window >= 0 (0: none)
+ * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it.
+ * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and
+ * values (chunks) with fp16 queries scaled by a power of two, fp32 sums,
+ * probabilities rounded to fp16 for the second product.
+ * Deterministic.  Calls sharing one workspace must not overlap on the GPU.
+ * The workspace needs no clearing. */
+size_t hs_kv4_attention_workspace_size(const hs_kv4_cache* cache, int n_seqs, int n_q_heads);
+int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q_bf16_dev, long long q_stride_token,
+                     long long q_stride_head, const int* q_start_dev, const int* seq_len_dev, const int* table_dev,
+                     int table_width, int n_seqs, int n_tokens, int n_q_heads, int max_new, float scale,
+                     int window, uint16_t* out_bf16_dev, long long out_stride_token, long long out_stride_head,
+                     void* workspace_dev, size_t workspace_bytes, hs_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
