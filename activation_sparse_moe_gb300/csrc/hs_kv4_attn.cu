@@ -14,6 +14,8 @@
 // powers of two go into q (per channel) and the output.  Query rows are scaled
 // by a power of two so that their largest channel is near 1: bf16 values then
 // lose nothing as fp16.
+#include <type_traits>
+
 #include "hs_kv4_sched.cuh"
 
 namespace hs {
@@ -36,6 +38,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 matrix of 16-bit numbers, lane 4 r + c holding columns 2c and 2c + 1
+// of row r, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&h);
@@ -43,7 +53,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 __device__ __forceinline__ float bf16_f32(uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); }
 
-template <int D, int RT, int KW>
+// NQ: query rows of a warp, in eights; RT: warps along the rows; KW: warps along the keys.
+template <int D, int NQ, int RT, int KW>
 struct DecodeCfg {
     static constexpr int kNg = D / 64;
     static constexpr int kTiles = 2;                  // 64-key tiles of a ring stage
@@ -51,10 +62,11 @@ struct DecodeCfg {
     static constexpr int kStageBytes = kTiles * kv_record_bytes(kKvTile, D);
     static constexpr int kWarps = RT * KW;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kCtas = RT > 1 ? 1 : D == 64 ? 3 : 2;  // resident on an SM
-    static constexpr int kO = 32 * kNg;               // accumulators of a thread
-    static constexpr int kMergeBytes = RT * (KW / 2) * (kO + 4) * 128;
-    static constexpr int kRows = 16 * RT;
+    static constexpr int kCtas = RT > 1 ? 1 : NQ == 1 || D == 64 ? 3 : 2;  // resident on an SM
+    static constexpr int kO = 16 * NQ * kNg;          // accumulators of a thread
+    static constexpr int kMerge = kO + 4 * NQ;        // and its maxima and sums
+    static constexpr int kMergeBytes = RT * (KW / 2) * kMerge * 128;
+    static constexpr int kRows = 8 * NQ * RT;
     static int smem(int n_seqs) {
         return kStages * kStageBytes + kMergeBytes + 256 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16;
     }
@@ -66,17 +78,23 @@ struct KvLoad {
     int tiles, head;     // of it (0 tiles: the run is done)
 };
 
-// Warp (rt, kw): rows 16 rt .. 16 rt + 15 of the item's row tile, the 16-key
-// steps kw, kw + KW, ... of every ring stage.  Warp 0 also keeps the ring full:
-// a stage is up to two 64-key tiles of one item, copied as whole page records
-// by one bulk copy a page; the pages of the stage after the next are looked up
-// while the earlier ones are on their way.  In the fragments of a
-// step, column n of key block j stands for key 8 j + n / 2 + 4 (n % 2), and
-// the k index runs over the channels in the order in which the nibbles of a
-// word come apart; both orders are free as long as the two operands agree.
-template <int D, int RT, int KW>
-__global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, RT, KW>::kCtas)) kv4_decode_kernel(const KvAttnArgs a) {
-    using C = DecodeCfg<D, RT, KW>;
+// Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 16-key steps
+// kw, kw + KW, ... of every ring stage.  Warp 0 also keeps the ring full: a
+// stage is up to two 64-key tiles of one item, copied as whole page records by
+// one bulk copy a page; the pages of the stage after the next are looked up
+// while the earlier ones are on their way.
+//
+// Both products have the cache on the left: scores (16 keys x 8 rows) = K q^T
+// and outputs (channels x 8 rows) = V^T p^T, so that a word of codes taken
+// apart once serves all rows, and eight rows do not pay for sixteen.  The
+// scores' fragment becomes the second product's right operand by one 8 x 8
+// transposition.  Row r (0..7) of a key block stands for key r / 2 + 4 (r % 2):
+// the four lanes of a group then read neighbouring rows of V.  The k index of
+// the first product runs over the channels in the order in which the nibbles
+// of a word come apart.
+template <int D, int NQ, int RT, int KW>
+__global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas)) kv4_decode_kernel(const KvAttnArgs a) {
+    using C = DecodeCfg<D, NQ, RT, KW>;
     constexpr int NG = C::kNg;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
@@ -170,76 +188,234 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, RT, KW>::kCtas)) k
     while (w.left > 0) {
         const int cnt = (int)min(w.left, (long long)(w.units - w.tile));
         const int ctx = w.len - w.n;
-        // this thread's two rows: query rows and the last key each sees; the first one is back_keys before it
-        uint32_t Q[4 * NG][4];
-        float sc[2], sq[NG][2];
-        int lim[2];
-        int min_lim = INT_MAX, max_lim = -1;  // over the warp's rows that exist
-        const int back_keys = a.window ? a.window - 1 : 0x3fffffff;
+        // the keys that the warp's rows see: all of [max_from, min_lim], none outside [min_from, max_lim]
+        const int row0 = rt * 8 * NQ, back_keys = a.window ? a.window - 1 : 0x3fffffff;
+        const int tok0 = w.r * a.tq + row0 / a.group;
+        const int tok1 = min(w.r * a.tq + min(row0 + 8 * NQ - 1, a.tq * a.group - 1) / a.group, w.n - 1);
+        const bool some = row0 < a.tq * a.group && tok0 < w.n;
+        const int min_lim = ctx + tok0, max_lim = some ? ctx + tok1 : -1;
+        const int min_from = some ? min_lim - back_keys : 0, max_from = max_lim - back_keys;
+
+        // Query rows as the right operand of the first product (lane: row g, 16
+        // channels of each group), all scaled by one power of two that brings
+        // the largest channel near 1 (bf16 values down to 2^-28 of it stay exact).
+        uint32_t Q[4 * NG][NQ][2];
+        float sq[NG][NQ][2], sc;
+        {
+            uint4 v[NQ][NG][2];
+            uint32_t top = 0;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int row = rt * 16 + g + 8 * x, tok = w.r * a.tq + row / a.group;
-            const bool valid = row < a.tq * a.group && tok < w.n;
-            lim[x] = ctx + tok;
-            if (valid) min_lim = min(min_lim, lim[x]), max_lim = max(max_lim, lim[x]);
-            uint4 v[NG][2];
-            float top = 0.f;
-            const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row % a.group) * a.q_sh;
+            for (int n = 0; n < NQ; ++n) {
+                const int row = row0 + n * 8 + g, tok = w.r * a.tq + row / a.group;
+                const bool valid = row < a.tq * a.group && tok < w.n;
+                const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row % a.group) * a.q_sh;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                float sum = 0.f;
+                for (int i = 0; i < NG; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
-                    const uint32_t u[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float f = bf16_f32(u[e >> 1], e & 1);
-                        top = fmaxf(top, fabsf(f));
-                        sum += f;
+                    for (int h = 0; h < 2; ++h) {
+                        v[n][i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
+                        top = max(max(top, v[n][i][h].x & 0x7fff7fffu), max(v[n][i][h].y & 0x7fff7fffu, max(v[n][i][h].z & 0x7fff7fffu, v[n][i][h].w & 0x7fff7fffu)));
+                        top = max(top, max(max(v[n][i][h].x << 16, v[n][i][h].y << 16), max(v[n][i][h].z << 16, v[n][i][h].w << 16)) & 0x7fffffffu);
                     }
-                }
-                sum += __shfl_xor_sync(~0u, sum, 1);
-                sq[i][x] = sum + __shfl_xor_sync(~0u, sum, 2);
             }
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            // f = 2^-e with 2^e <= top < 2^(e+1); rows of zeros and of infinities keep f = 1
-            int e = (int)((__float_as_uint(top) >> 23) & 255u);
+            // f = 2^-e, 2^e <= largest < 2^(e+1); zeros and infinities keep f = 1
+            int e = (int)(warp_max_u32(top) >> 23);
             e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
             const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-            const float f8 = f * 256.f, f4 = f * 16.f;  // the even nibbles stand for c * 2^-24, the odd ones for c * 2^-20
-            sc[x] = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 65536.f;
+            const float f8 = f * 4096.f, f4 = f * 256.f;  // the even nibbles stand for c * 2^-24, the odd ones for c * 2^-20
+            sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 4096.f;
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                sq[i][x] *= f * (1.f / 65536.f);
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t u[4] = {v[i][h].x, v[i][h].y, v[i][h].z, v[i][h].w};
+                for (int i = 0; i < NG; ++i) {
+                    float sum = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {  // nibbles (2j, 2j + 4) and (2j + 1, 2j + 5)
-                        Q[(i * 2 + h) * 2 + j][x] = pack_half2(bf16_f32(u[j], 0) * f8, bf16_f32(u[j + 2], 0) * f8);
-                        Q[(i * 2 + h) * 2 + j][2 + x] = pack_half2(bf16_f32(u[j], 1) * f4, bf16_f32(u[j + 2], 1) * f4);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u[4] = {v[n][i][h].x, v[n][i][h].y, v[n][i][h].z, v[n][i][h].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum += bf16_f32(u[j], 0) + bf16_f32(u[j], 1);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {  // nibbles (2j, 2j + 4) and (2j + 1, 2j + 5)
+                            Q[(i * 2 + h) * 2 + j][n][0] = pack_half2(bf16_f32(u[j], 0) * f8, bf16_f32(u[j + 2], 0) * f8);
+                            Q[(i * 2 + h) * 2 + j][n][1] = pack_half2(bf16_f32(u[j], 1) * f4, bf16_f32(u[j + 2], 1) * f4);
+                        }
                     }
+                    sum += __shfl_xor_sync(~0u, sum, 1);
+                    sum += __shfl_xor_sync(~0u, sum, 2);
+                    sum *= f * (1.f / 4096.f);
+                    sq[i][n][0] = __shfl_sync(~0u, sum, 8 * t);      // of rows 2t and 2t + 1
+                    sq[i][n][1] = __shfl_sync(~0u, sum, 8 * t + 4);
                 }
-            }
         }
-        max_lim = warp_max_s32(max_lim);
-        min_lim = -warp_max_s32(-min_lim);
-        const int min_from = max_lim < 0 ? 0 : min_lim - back_keys, max_from = max_lim - back_keys;
 
-        float O[NG][8][4];
-        float m[2] = {-1e30f, -1e30f}, l[2] = {0.f, 0.f}, bs[NG][2];
+        // Lane: outputs of channels 64 i + 8 g + 2 u + (e / 2), rows 2t + e % 2.
+        float O[NG][4][NQ][4];
+        float m[NQ][2], l[NQ][2], bs[NG][NQ][2];
         uint32_t eb = 0;          // exponent field of the largest value scale so far
         float ke = 2097152.f;     // 2^(21 - eb): probability * scale * ke stays below 2^15
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            bs[i][0] = bs[i][1] = 0.f;
+        for (int n = 0; n < NQ; ++n) {
+            m[n][0] = m[n][1] = -1e30f;
+            l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+            for (int i = 0; i < NG; ++i) {
+                bs[i][n][0] = bs[i][n][1] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) O[i][n][e] = 0.f;
+                for (int u = 0; u < 4; ++u) O[i][u][n][0] = O[i][u][n][1] = O[i][u][n][2] = O[i][u][n][3] = 0.f;
+            }
         }
+
+        // One step of 16 keys; MASKED: some row does not see some of them.
+        auto step16 = [&](auto masked_tag, const uint8_t* rec, const int off, const int key0) {
+            constexpr bool MASKED = decltype(masked_tag)::value;
+            const int kr = (g >> 1) + 4 * (g & 1);  // the key of fragment row g
+            float S[NG][NQ][4];
+            uint2 kc[2][NG];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+                    kc[j][i] = *reinterpret_cast<const uint2*>(rec + (off + 8 * j + kr) * (D / 2) + i * 32 + t * 8);
+            uint32_t kp[2][NG], vp[2][NG];  // the pairs of the keys of rows g and g + 8
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* pk = rec + 2 * half_b + (off + 8 * j + kr) * (NG * 4);
+                // what lies behind the last key may be anything
+                const bool there = !MASKED || key0 + 8 * j + kr < w.len;
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    kp[j][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
+                    vp[j][i] = there ? reinterpret_cast<const uint32_t*>(pk + pairs_b)[i] : 0;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) S[i][n][0] = S[i][n][1] = S[i][n][2] = S[i][n][3] = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    uint32_t x = h ? kc[0][i].y : kc[0][i].x, y = h ? kc[1][i].y : kc[1][i].x;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t A[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+                            mma_16816(S[i][n], A, Q[(i * 2 + h) * 2 + j][n][0], Q[(i * 2 + h) * 2 + j][n][1]);
+                        x >>= 8;
+                        y >>= 8;
+                    }
+                }
+            float s[2][NQ][2];  // [key block][row]
+            bool grow = false;
+            {
+                float2 p[2][NG];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) p[j][i] = half2_to_float2(kp[j][i]);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float v = p[j][0].y * sq[0][n][e];
+#pragma unroll
+                            for (int i = 1; i < NG; ++i) v = fmaf(p[j][i].y, sq[i][n][e], v);
+#pragma unroll
+                            for (int i = 0; i < NG; ++i) v = fmaf(p[j][i].x, S[i][n][2 * j + e], v);
+                            if (MASKED) {
+                                const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + row / a.group;
+                                const int key = key0 + 8 * j + kr;
+                                if (key > lim || key < lim - back_keys) v = -INFINITY;
+                            }
+                            s[j][n][e] = v;
+                        }
+                        grow |= fmaf(fmaxf(s[0][n][e], s[1][n][e]), sc, -m[n][e]) > kLazy;
+                    }
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < NG; ++i) top = max(top, vp[j][i] & 0x7c00u);
+            if (__any_sync(~0u, grow || top > eb << 10)) {  // rare: a maximum passed the lag, or a scale the exponent
+                const uint32_t neb = max(eb, warp_max_u32(top) >> 10);
+                const float down = __uint_as_float((127u + eb - neb) << 23);
+                eb = neb;
+                ke = __uint_as_float((148u - neb) << 23);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(s[0][n][e], s[1][n][e]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+                        const float nm = fmaxf(m[n][e], x * sc), f = ex2(m[n][e] - nm);
+                        m[n][e] = nm;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            bs[i][n][e] *= f;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) O[i][u][n][e] *= f * down, O[i][u][n][2 + e] *= f * down;
+                        }
+                    }
+            }
+            float2 p[2][NG];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    p[j][i] = half2_to_float2(vp[j][i]);
+                    p[j][i].x *= ke;
+                }
+            uint32_t B[NG][NQ][2];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[e] = ex2(fmaf(s[j][n][e], sc, -m[n][e]));
+                        l[n][e] += x[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        float y[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const bool hide = MASKED && x[e] == 0.f;  // a key that the row does not see may hold a NaN
+                            bs[i][n][e] = hide ? bs[i][n][e] : fmaf(x[e], p[j][i].y, bs[i][n][e]);
+                            y[e] = hide ? 0.f : x[e] * p[j][i].x;
+                        }
+                        B[i][n][j] = transpose_8x8(pack_half2(y[0], y[1]));
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const uint8_t* pv = rec + half_b + (off + t) * (D / 2) + i * 32 + g * 4;
+                uint32_t c[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e] = *reinterpret_cast<const uint32_t*>(pv + 4 * e * (D / 2));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t x = __byte_perm(c[0], c[1], h ? 0x7632 : 0x5410);
+                    uint32_t y = __byte_perm(c[2], c[3], h ? 0x7632 : 0x5410);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t A[4] = {x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u};
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) mma_16816(O[i][2 * h + j][n], A, B[i][n][0], B[i][n][1]);
+                        x >>= 8;
+                        y >>= 8;
+                    }
+                }
+            }
+        };
 
         int tile_key = (w.lo + w.tile) * kKvTile;
         for (int k = 0; k < cnt; k += C::kTiles, ++it, tile_key += C::kTiles * kKvTile) {
@@ -253,202 +429,76 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, RT, KW>::kCtas)) k
             for (int step = kw; step < steps; step += KW) {
                 const int key0 = tile_key + step * 16;
                 if ((gone >> step) & 1u || key0 > max_lim || key0 + 15 < min_from) continue;
-                const bool masked = key0 + 15 > min_lim || key0 < max_from;
-                const int in_tile = step * 16, off = in_tile & (P - 1);
-                const uint8_t* rec = stage + (in_tile >> a.g.page_log2) * a.g.rec;
-
-                float S[NG][2][4];
-#pragma unroll
-                for (int i = 0; i < NG; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) S[i][j][0] = S[i][j][1] = S[i][j][2] = S[i][j][3] = 0.f;
-                uint2 kc[2][NG];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int i = 0; i < NG; ++i)
-                        kc[j][i] = *reinterpret_cast<const uint2*>(rec + (off + 8 * j + (g >> 1) + 4 * (g & 1)) * (D / 2) + i * 32 + t * 8);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            const uint32_t c = h ? kc[j][i].y : kc[j][i].x, c8 = c >> 8;
-                            mma_16816(S[i][j], Q[(i * 2 + h) * 2], c & 0x000f000fu, c & 0x00f000f0u);
-                            mma_16816(S[i][j], Q[(i * 2 + h) * 2 + 1], c8 & 0x000f000fu, c8 & 0x00f000f0u);
-                        }
-                // the pairs of this thread's four keys; what lies behind the last key may be anything
-                uint32_t kp[4][NG];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint8_t* pk = rec + 2 * half_b + (off + 4 * c + t) * (NG * 4);
-                    const bool there = !masked || key0 + 4 * c + t < w.len;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        kp[c][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
-                    }
-                }
-                float s[2][4];  // [row][key]
-                float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float2 p[NG];
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) p[i] = half2_to_float2(kp[c][i]);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float v = 0.f;
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            v = i ? fmaf(p[i].x, S[i][c >> 1][2 * x + (c & 1)], v) : p[i].x * S[i][c >> 1][2 * x + (c & 1)];
-                            v = fmaf(p[i].y, sq[i][x], v);
-                        }
-                        if (masked) {
-                            const int key = key0 + 4 * c + t;
-                            if (key > lim[x] || key < lim[x] - back_keys) v = -INFINITY;
-                        }
-                        s[x][c] = v;
-                        mx[x] = fmaxf(mx[x], v);
-                    }
-                }
-                uint32_t top = 0, vp[4][NG];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint8_t* pk = rec + 2 * half_b + pairs_b + (off + 4 * c + t) * (NG * 4);
-                    const bool there = !masked || key0 + 4 * c + t < w.len;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) vp[c][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < NG; ++i) top = max(top, vp[c][i] & 0x7fffu);
-                top = warp_max_u32(top) >> 10;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 1));
-                    mx[x] = fmaxf(mx[x], __shfl_xor_sync(~0u, mx[x], 2)) * sc[x];
-                }
-                if (__any_sync(~0u, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy) || top > eb) {
-                    const uint32_t neb = max(eb, top);
-                    const float back = __uint_as_float((127u + eb - neb) << 23);
-                    eb = neb;
-                    ke = __uint_as_float((148u - neb) << 23);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float nm = fmaxf(m[x], mx[x]), f = ex2(m[x] - nm);
-                        m[x] = nm;
-                        l[x] *= f;
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            bs[i][x] *= f;
-#pragma unroll
-                            for (int n = 0; n < 8; ++n) {
-                                O[i][n][2 * x] *= f * back;
-                                O[i][n][2 * x + 1] *= f * back;
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[x][c] = ex2(fmaf(s[x][c], sc[x], -m[x]));
-                        l[x] += s[x][c];
-                    }
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    uint32_t A[4];
-#pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        const float2 p0 = half2_to_float2(vp[c][i]), p1 = half2_to_float2(vp[c + 1][i]);
-                        const float s0 = p0.x * ke, s1 = p1.x * ke;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float e0 = s[x][c], e1 = s[x][c + 1];
-                            float b0 = e0 * p0.y, b1 = e1 * p1.y, v0 = e0 * s0, v1 = e1 * s1;
-                            if (masked) {  // a key that the row does not see may hold a NaN
-                                if (e0 == 0.f) b0 = v0 = 0.f;
-                                if (e1 == 0.f) b1 = v1 = 0.f;
-                            }
-                            bs[i][x] += b0 + b1;
-                            A[c + x] = pack_half2(v0, v1);
-                        }
-                    }
-                    const uint8_t* pv = rec + half_b + (off + t) * (D / 2) + i * 32 + g * 4;
-                    uint32_t c[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e] = *reinterpret_cast<const uint32_t*>(pv + 4 * e * (D / 2));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x = __byte_perm(c[0], c[1], h ? 0x7632 : 0x5410);
-                        uint32_t y = __byte_perm(c[2], c[3], h ? 0x7632 : 0x5410);
-                        mma_16816(O[i][4 * h], A, x & 0x000f000fu, y & 0x000f000fu);
-                        mma_16816(O[i][4 * h + 1], A, x & 0x00f000f0u, y & 0x00f000f0u);
-                        x >>= 8;
-                        y >>= 8;
-                        mma_16816(O[i][4 * h + 2], A, x & 0x000f000fu, y & 0x000f000fu);
-                        mma_16816(O[i][4 * h + 3], A, x & 0x00f000f0u, y & 0x00f000f0u);
-                    }
-                }
+                const int in_stage = step * 16, off = in_stage & (P - 1);
+                const uint8_t* rec = stage + (in_stage >> a.g.page_log2) * a.g.rec;
+                if (key0 + 15 > min_lim || key0 < max_from)
+                    step16(std::true_type(), rec, off, key0);
+                else
+                    step16(std::false_type(), rec, off, key0);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + st);
         }
 
-        // ---- the piece's sums: over the four threads of a row, then over the key warps
+        // ---- the piece's sums: over the lanes of a row, then over the key warps
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            l[x] += __shfl_xor_sync(~0u, l[x], 1);
-            l[x] += __shfl_xor_sync(~0u, l[x], 2);
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                bs[i][x] += __shfl_xor_sync(~0u, bs[i][x], 1);
-                bs[i][x] += __shfl_xor_sync(~0u, bs[i][x], 2);
-            }
-        }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    l[n][e] += __shfl_xor_sync(~0u, l[n][e], o);
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) bs[i][n][e] += __shfl_xor_sync(~0u, bs[i][n][e], o);
+                }
         const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / ke
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    O[i][n][e] = fmaf(O[i][n][e], n & 1 ? even * 0.0625f : even, bs[i][e >> 1]);
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        O[i][u][n][e] = fmaf(O[i][u][n][e], e < 2 ? even : even * 0.0625f, bs[i][n][e & 1]);
 #pragma unroll
         for (int half = KW / 2; half; half >>= 1) {
             if (kw >= half && kw < 2 * half) {
-                float* b = merge + (rt * (KW / 2) + kw - half) * (C::kO + 4) * 32 + lane;
+                float* b = merge + (rt * (KW / 2) + kw - half) * C::kMerge * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < NG; ++i)
-#pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) b[((i * 8 + n) * 4 + e) * 32] = O[i][n][e];
-                b[C::kO * 32] = m[0], b[(C::kO + 1) * 32] = m[1];
-                b[(C::kO + 2) * 32] = l[0], b[(C::kO + 3) * 32] = l[1];
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-            if (kw < half) {
-                const float* b = merge + (rt * (KW / 2) + kw) * (C::kO + 4) * 32 + lane;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float om = b[(C::kO + x) * 32], nm = fmaxf(m[x], om);
-                    const float f0 = ex2(m[x] - nm), f1 = ex2(om - nm);
-                    m[x] = nm;
-                    l[x] = l[x] * f0 + b[(C::kO + 2 + x) * 32] * f1;
+                for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                     for (int i = 0; i < NG; ++i)
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) {
+                        for (int u = 0; u < 4; ++u)
 #pragma unroll
-                            for (int e = 2 * x; e < 2 * x + 2; ++e)
-                                O[i][n][e] = O[i][n][e] * f0 + b[((i * 8 + n) * 4 + e) * 32] * f1;
-                            if (n % 4 == 3) asm volatile("" ::: "memory");  // no more loads in flight than registers hold
-                        }
+                            for (int e = 0; e < 4; ++e) b[(((n * NG + i) * 4 + u) * 4 + e) * 32] = O[i][u][n][e];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        b[(C::kO + 4 * n + e) * 32] = m[n][e];
+                        b[(C::kO + 4 * n + 2 + e) * 32] = l[n][e];
+                    }
                 }
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
+            if (kw < half) {
+                const float* b = merge + (rt * (KW / 2) + kw) * C::kMerge * 32 + lane;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float om = b[(C::kO + 4 * n + e) * 32], nm = fmaxf(m[n][e], om);
+                        const float f0 = ex2(m[n][e] - nm), f1 = ex2(om - nm);
+                        m[n][e] = nm;
+                        l[n][e] = l[n][e] * f0 + b[(C::kO + 4 * n + 2 + e) * 32] * f1;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                                for (int x = e; x < 4; x += 2)
+                                    O[i][u][n][x] = O[i][u][n][x] * f0 + b[(((n * NG + i) * 4 + u) * 4 + x) * 32] * f1;
+                    }
             }
             asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         }
@@ -462,38 +512,35 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, RT, KW>::kCtas)) k
         }
         if (kw == 0) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int row = rt * 16 + g + 8 * x, tok = w.r * a.tq + row / a.group;
-                if (row >= a.tq * a.group || tok >= w.n) continue;
-                if (whole) {
-                    const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
-                    uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row % a.group) * a.o_sh;
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int i = 0; i < NG; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    const int row = row0 + n * 8 + 2 * t + e, tok = w.r * a.tq + row / a.group;
+                    if (row >= a.tq * a.group || tok >= w.n) continue;
+                    if (whole) {
+                        const float inv = l[n][e] != 0.f ? 1.f / l[n][e] : 0.f;
+                        uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row % a.group) * a.o_sh + g * 8;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int i = 0; i < NG; ++i) {
                             uint32_t u[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                u[e] = (uint32_t)f32_to_bf16_bits(O[i][2 * e][2 * x + h] * inv) |
-                                       ((uint32_t)f32_to_bf16_bits(O[i][2 * e + 1][2 * x + h] * inv) << 16);
-                            *reinterpret_cast<uint4*>(dst + i * 64 + t * 16 + h * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                            for (int x = 0; x < 4; ++x)
+                                u[x] = (uint32_t)f32_to_bf16_bits(O[i][x][n][e] * inv) |
+                                       ((uint32_t)f32_to_bf16_bits(O[i][x][n][2 + e] * inv) << 16);
+                            *reinterpret_cast<uint4*>(dst + i * 64) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
-                } else {
-                    const size_t slot = 2 * blockIdx.x + (w.tile == 0 ? 1 : 0);
-                    float* dst = a.part_o + (slot * a.rows + row) * D;
+                    } else {
+                        const size_t slot = 2 * blockIdx.x + (w.tile == 0 ? 1 : 0);
+                        float* dst = a.part_o + (slot * a.rows + row) * D + g * 8;
 #pragma unroll
-                    for (int i = 0; i < NG; ++i)
+                        for (int i = 0; i < NG; ++i)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<float4*>(dst + i * 64 + t * 16 + h * 8 + e * 4) =
-                                    make_float4(O[i][4 * e][2 * x + h], O[i][4 * e + 1][2 * x + h],
-                                                O[i][4 * e + 2][2 * x + h], O[i][4 * e + 3][2 * x + h]);
-                    if (t == 0) a.part_ml[slot * a.rows + row] = make_float2(m[x], l[x]);
+                            for (int x = 0; x < 4; x += 2)
+                                *reinterpret_cast<float4*>(dst + i * 64 + x * 2) =
+                                    make_float4(O[i][x][n][e], O[i][x][n][2 + e], O[i][x + 1][n][e], O[i][x + 1][n][2 + e]);
+                        if (g == 0) a.part_ml[slot * a.rows + row] = make_float2(m[n][e], l[n][e]);
+                    }
                 }
-            }
         }
         KvWalk next = w;
         next.left -= cnt;
@@ -567,21 +614,30 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const KvAttnArgs a) {
     }
 }
 
-template <int D, int RT, int KW>
+template <int D, int NQ, int RT, int KW>
 int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
-    using C = DecodeCfg<D, RT, KW>;
+    using C = DecodeCfg<D, NQ, RT, KW>;
     const int smem = C::smem(a.n_seqs);
-    const int st = hs_host::set_smem_attr((const void*)kv4_decode_kernel<D, RT, KW>, C::smem(kKvMaxSeqs));
+    const int st = hs_host::set_smem_attr((const void*)kv4_decode_kernel<D, NQ, RT, KW>, C::smem(kKvMaxSeqs));
     if (st != HS_OK) return st;
     a.rows = C::kRows;
     a.tq = C::kRows / a.group;
     a.min_units = 2;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
-    if (hs_host::launch_pdl(kv4_decode_kernel<D, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
+    if (hs_host::launch_pdl(kv4_decode_kernel<D, NQ, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
         return HS_ERR_CUDA;
     if (hs_host::launch_pdl(kv4_combine_kernel<D>, dim3(ctas, 16), dim3(128), 0, s, a) != cudaSuccess) return HS_ERR_CUDA;
     return HS_OK;
+}
+
+// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.
+template <int D>
+int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
+    if (rows <= 8) return launch_decode<D, 1, 1, 4>(a, sms, s);
+    if (rows <= 16) return launch_decode<D, 2, 1, 4>(a, sms, s);
+    if (rows <= 32) return launch_decode<D, 2, 2, 4>(a, sms, s);
+    return launch_decode<D, 2, 4, 2>(a, sms, s);
 }
 
 }  // namespace hs
@@ -636,15 +692,8 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.part_ml = reinterpret_cast<float2*>(w + round_up(rows * dim * 4, 256));
     a.meta = reinterpret_cast<int4*>(w + round_up(rows * dim * 4, 256) + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // Row tiles of 16, 32 or 64: the smallest that holds a request's rows.
     const long long need = std::max((long long)max_new, 1ll) * a.group;
-    int r;
-    if (dim == 64)
-        r = need <= 16 ? hs::launch_decode<64, 1, 4>(a, sms, s)
-                       : need <= 32 ? hs::launch_decode<64, 2, 4>(a, sms, s) : hs::launch_decode<64, 4, 2>(a, sms, s);
-    else
-        r = need <= 16 ? hs::launch_decode<128, 1, 4>(a, sms, s)
-                       : need <= 32 ? hs::launch_decode<128, 2, 4>(a, sms, s) : hs::launch_decode<128, 4, 2>(a, sms, s);
+    const int r = dim == 64 ? hs::launch_rows<64>(a, need, sms, s) : hs::launch_rows<128>(a, need, sms, s);
     return r != HS_OK ? r : launch_err();
 }
 
