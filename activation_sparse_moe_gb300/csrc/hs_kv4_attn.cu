@@ -1,6 +1,5 @@
 // Attention of new tokens over the 4-bit key/value cache, GB300 (sm_103a):
-// the kernel for few query rows (decode, verification of drafts) and the one
-// that joins divided items.  Contract: hs_kv4_attention in hs.h.
+// the kernel for few query rows (decode, verification of drafts).  Contract: hs_kv4_attention in hs.h.
 //
 // Mathematics.  With k_j = s_jg c_jd + b_jg (g the channel's group of 64),
 //   q . k_j = sum_g s_jg (q . c_j)_g + b_jg (sum of q over g),
@@ -16,19 +15,13 @@
 // lose nothing as fp16.
 #include <type_traits>
 
-#include "hs_kv4_sched.cuh"
+#include "hs_kv4_join.cuh"
 
 namespace hs {
 
-constexpr int kKvMaxCtas = 456;   // three CTAs on each of 152 SMs
 constexpr int kKvWsRows = 2 * 152 * 64;  // rows of partial sums of the widest launch
+constexpr int kKvStep = 32;        // keys of a warp's step
 constexpr float kLazy = 8.f;      // a row's maximum may lag by a factor 2^8 before the sums are rescaled
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // D += A * B, one 16 x 8 x 16 product of fp16 operands in fp32.
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -57,32 +50,26 @@ __device__ __forceinline__ float bf16_f32(uint32_t w, int hi) { return __uint_as
 template <int D, int NQ, int RT, int KW>
 struct DecodeCfg {
     static constexpr int kNg = D / 64;
-    static constexpr int kTiles = 2;                  // 64-key tiles of a ring stage
-    static constexpr int kStages = 3;
-    static constexpr int kStageBytes = kTiles * kv_record_bytes(kKvTile, D);
+    static constexpr int kCtas = RT > 1 ? 1 : NQ == 1 ? 3 : 2;  // resident on an SM
+    static constexpr int kSlots = RT == 1 && NQ == 2 ? 4 : 3;  // steps of a warp's ring
+    static constexpr int kSlotBytes = kv_record_bytes(kKvStep, D);
     static constexpr int kWarps = RT * KW;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kCtas = RT > 1 ? 1 : NQ == 1 || D == 64 ? 3 : 2;  // resident on an SM
     static constexpr int kO = 16 * NQ * kNg;          // accumulators of a thread
     static constexpr int kMerge = kO + 4 * NQ;        // and its maxima and sums
+    static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
     static constexpr int kMergeBytes = RT * (KW / 2) * kMerge * 128;
     static constexpr int kRows = 8 * NQ * RT;
-    static int smem(int n_seqs) {
-        return kStages * kStageBytes + kMergeBytes + 256 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16;
-    }
+    static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16; }
 };
 
-// What warp 0 knows of the ring's next stage.
-struct KvLoad {
-    KvWalk w;            // behind that stage
-    int tiles, head;     // of it (0 tiles: the run is done)
-};
-
-// Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 16-key steps
-// kw, kw + KW, ... of every ring stage.  Warp 0 also keeps the ring full: a
-// stage is up to two 64-key tiles of one item, copied as whole page records by
-// one bulk copy a page; the pages of the stage after the next are looked up
-// while the earlier ones are on their way.
+// Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 32-key steps
+// kw, kw + KW, ... of the CTA's piece of it.  Every warp keeps its own ring of
+// steps full: four lanes (eight for pages of 16) issue one bulk copy each, of K
+// codes, V codes, K pairs and V pairs, as soon as the warp has used a slot up,
+// across the ends of items.  So the warps do not wait for one another until an
+// item ends (a ring shared by the CTA's warps held them in step: 30% of the
+// issue slots went into waiting).
 //
 // Both products have the cache on the left: scores (16 keys x 8 rows) = K q^T
 // and outputs (channels x 8 rows) = V^T p^T, so that a word of codes taken
@@ -97,104 +84,102 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     using C = DecodeCfg<D, NQ, RT, KW>;
     constexpr int NG = C::kNg;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* ring = smem;
-    float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStageBytes + C::kMergeBytes);
-    uint64_t* empty = full + C::kStages;
-    uint32_t* absent = reinterpret_cast<uint32_t*>(empty + C::kStages);  // per stage: 16-key steps that are not there
-    long long* cum = reinterpret_cast<long long*>(full + 32);
+    float* merge = reinterpret_cast<float*>(smem + C::kRingBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRingBytes + C::kMergeBytes);
+    long long* cum = reinterpret_cast<long long*>(bars + 32);
     int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
     int* ls = qs + a.n_seqs + 1;
+    // Where a warp computes and where it loads, a copy a warp in shared memory
+    // (every lane writes the same): looked at once an item, and registers are short.
+    __shared__ KvWalk walks[C::kWarps], ahead[C::kWarps];
+    __shared__ int join_last;
+    static_assert(C::kWarps * C::kSlots <= 32, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rt = warp / KW, kw = warp % KW, g = lane >> 2, t = lane & 3;  // fragment row or column, and pair
 
-    if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(full + i, 1);
-            mbar_init(empty + i, C::kWarps);
-        }
+    if (tid < C::kWarps * C::kSlots) {
+        mbar_init(bars + tid, 1);
         fence_mbar_init();
     }
     pdl_wait();
     pdl_trigger();
     kv_schedule(a, qs, ls, cum);
-    __shared__ KvLoad load;
-    // The place in the line, kept in shared memory (a copy a warp, every lane
-    // writing the same): it is looked at once an item, and registers are short.
-    __shared__ KvWalk walks[C::kWarps];
     KvWalk& w = walks[warp];
-    w = kv_begin(a, qs, ls, cum);
+    w = ahead[warp] = kv_begin(a, qs, ls, cum);
     __syncwarp();
     const int P = 1 << a.g.page_log2;
 
-    const int per_tile = kKvTile >> a.g.page_log2;
-
-    // ---- the ring's loads (warp 0)
-    uint32_t loads = 0;
-    int page = -1;  // lane l: page l of the next stage
-    auto look_up = [&]() {
-        KvWalk v = load.w;
-        const int tiles = v.left > 0 ? min(C::kTiles, (int)min(v.left, (long long)(v.units - v.tile))) : 0;
-        if (tiles) {
-            const int p = (v.lo + v.tile) * per_tile + lane;
-            const bool in = lane < tiles * per_tile && v.hi >= v.lo && p < (v.len + P - 1) >> a.g.page_log2;
-            page = in ? a.table[(size_t)v.seq * a.width + p] : -1;
-            if (lane == 0) load.head = v.head;
-            v.left -= tiles;
-            v.tile += tiles;
-            if (v.tile == v.units && v.left > 0) kv_next_item(a, qs, ls, v);
-        }
-        __syncwarp();
-        if (lane == 0) {
-            load.w = v;
-            load.tiles = tiles;
-        }
-        __syncwarp();
+    // ---- the warp's ring
+    uint8_t* ring = smem + warp * C::kSlots * C::kSlotBytes;
+    uint64_t* full = bars + warp * C::kSlots;
+    const int parts_log2 = a.g.page_log2 == 4 ? 1 : 0;  // pages of a step: two of 16, or one
+    // Lane: copy seg (K codes, V codes, K pairs, V pairs) of page `part` of a step.
+    const int part = lane >> 2 & parts_log2, seg = lane & 3, row_bytes = seg < 2 ? D / 2 : NG * 4;
+    const uint32_t copy_bytes = lane < 4 << parts_log2 ? (uint32_t)(row_bytes * (kKvStep >> parts_log2)) : 0;
+    const uint32_t dst = smem_u32(ring) + (seg < 2 ? seg * (kKvStep * D / 2) : kKvStep * (D + (seg - 2) * NG * 4)) + part * copy_bytes;
+    const uint8_t* src = nullptr;  // of this lane's copies in page 0
+    uint32_t gone = 0;             // two bits a slot: blocks of 16 keys that are not there
+    int key = 0, key_end = 0;      // the next step's first key, and the end of the piece that is being loaded
+    int seen = 0, held = -1;       // its steps so far; lane: a table entry of the coming ones
+    int in_slot = 0;
+    auto piece_to_load = [&](const KvWalk& v) {
+        key = (v.lo + v.tile) * kKvTile;
+        key_end = key + kv_piece_tiles(v) * kKvTile;
+        key += kw * kKvStep;
+        seen = 0;
+        src = kv_record(a.g, 0, v.head) + ((seg < 2 ? seg * (D / 2) : D + (seg - 2) * NG * 4) << a.g.page_log2);
     };
-    auto refill = [&]() -> bool {
-        const int tiles = load.tiles;
-        if (!tiles) return true;
-        const int st = loads % C::kStages;
-        if (loads >= C::kStages && !mbar_wait(empty + st, (loads / C::kStages + 1) & 1)) return false;
-        const bool here = page >= 0 && page < a.g.n_pages;
-        const unsigned mask = __ballot_sync(~0u, here);
-        if (lane == 0) {
-            uint32_t gone = 0;
-#pragma unroll
-            for (int i = 0; i < 4 * C::kTiles; ++i)
-                if (!((mask >> (i * 16 >> a.g.page_log2)) & 1u)) gone |= 1u << i;
-            absent[st] = gone;
-            mbar_arrive_expect_tx(full + st, (uint32_t)__popc(mask) * (uint32_t)a.g.rec);
+    if (w.left > 0) piece_to_load(w);
+    auto load = [&]() {
+        if (key >= key_end) {  // to the next piece in which this warp has a step
+            if (ahead[warp].left <= 0) return;
+            do {
+                KvWalk n = ahead[warp];
+                kv_next_piece(a, qs, ls, n);
+                if (n.left > 0) piece_to_load(n);
+                __syncwarp();
+                ahead[warp] = n;
+                __syncwarp();
+                if (n.left <= 0) return;
+            } while (key >= key_end);
         }
+        const int at = (seen++ << parts_log2) & 31;
+        if (at == 0) {  // the table entries of the next 16 or 32 steps, one a lane
+            const KvWalk& v = ahead[warp];
+            const int k = key + (lane >> parts_log2) * KW * kKvStep + ((lane << 4) & (parts_log2 << 4));
+            held = v.hi >= v.lo && k < v.len ? a.table[(size_t)v.seq * a.width + (k >> a.g.page_log2)] : -1;
+        }
+        const int page = __shfl_sync(~0u, held, at + part);
+        const bool here = copy_bytes && (uint32_t)page < (uint32_t)a.g.n_pages;
+        const unsigned mask = __ballot_sync(~0u, here);
+        const unsigned all = parts_log2 ? 0xffu : 0xfu;
+        gone &= ~(3u << (2 * in_slot));
+        if (mask != all) gone |= ((mask & 1u ? 0u : parts_log2 ? 1u : 3u) | (parts_log2 && !(mask & 16u) ? 2u : 0u)) << (2 * in_slot);
+        if (lane == 0)
+            mbar_arrive_expect_tx(full + in_slot, (uint32_t)(__popc(mask) >> 2) * (uint32_t)((kKvStep >> parts_log2) * (D + D / 8)));
         __syncwarp();
         if (here)
-            bulk_g2s(ring + st * C::kStageBytes + lane * a.g.rec, kv_record(a.g, page, load.head), (uint32_t)a.g.rec,
-                     full + st, policy_evict_first());
-        ++loads;
-        look_up();
-        return true;
+            bulk_g2s_to(dst + in_slot * C::kSlotBytes,
+                        src + (size_t)(uint32_t)page * (uint32_t)(a.g.heads * a.g.rec) + (key & (P - 1) & kKvStep ? copy_bytes : 0),
+                        copy_bytes, smem_u32(full + in_slot), policy_evict_first());
+        key += KW * kKvStep;
+        in_slot = in_slot + 1 == C::kSlots ? 0 : in_slot + 1;
     };
-    if (warp == 0) {
-        if (lane == 0) load.w = w;
-        __syncwarp();
-        look_up();
-        for (int i = 0; i < C::kStages; ++i) refill();  // nothing to wait for yet
-    }
+    for (int i = 0; i < C::kSlots; ++i) load();
 
     // ---- the items
-    const int rt = warp / KW, kw = warp % KW, g = lane >> 2, t = lane & 3;  // fragment row or column, and pair
-    const int half_b = (D / 2) << a.g.page_log2, pairs_b = (NG * 4) << a.g.page_log2;
-    uint32_t it = 0;
-    int4 meta = make_int4(0, 0, 0, 0);
+    int slot = 0;
+    uint32_t phase = 0;  // bit 0: the ring's parity; bit 1: a wait has given up
     while (w.left > 0) {
-        const int cnt = (int)min(w.left, (long long)(w.units - w.tile));
+        const int cnt = kv_piece_tiles(w);
         const int ctx = w.len - w.n;
-        // the keys that the warp's rows see: all of [max_from, min_lim], none outside [min_from, max_lim]
+        // the warp's rows see no key past max_lim or before min_lim - back_keys, and all
+        // of those from max_lim - back_keys to min_lim
         const int row0 = rt * 8 * NQ, back_keys = a.window ? a.window - 1 : 0x3fffffff;
         const int tok0 = w.r * a.tq + row0 / a.group;
         const int tok1 = min(w.r * a.tq + min(row0 + 8 * NQ - 1, a.tq * a.group - 1) / a.group, w.n - 1);
         const bool some = row0 < a.tq * a.group && tok0 < w.n;
         const int min_lim = ctx + tok0, max_lim = some ? ctx + tok1 : -1;
-        const int min_from = some ? min_lim - back_keys : 0, max_from = max_lim - back_keys;
 
         // Query rows as the right operand of the first product (lane: row g, 16
         // channels of each group), all scaled by one power of two that brings
@@ -251,8 +236,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         // Lane: outputs of channels 64 i + 8 g + 2 u + (e / 2), rows 2t + e % 2.
         float O[NG][4][NQ][4];
         float m[NQ][2], l[NQ][2], bs[NG][NQ][2];
-        uint32_t eb = 0;          // exponent field of the largest value scale so far
-        float ke = 2097152.f;     // 2^(21 - eb): probability * scale * ke stays below 2^15
+        // Exponent field of the largest value scale so far: probability * scale *
+        // 2^(21 - eb) stays below 2^15.
+        uint32_t eb = 0;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             m[n][0] = m[n][1] = -1e30f;
@@ -265,92 +251,97 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             }
         }
 
-        // One step of 16 keys; MASKED: some row does not see some of them.
-        auto step16 = [&](auto masked_tag, const uint8_t* rec, const int off, const int key0) {
+        // One step of 32 keys at `rec`, key0 on.  MASKED: some row does not see some
+        // of them, or a block of 16 is not there (bit h of none).
+        auto step32 = [&](auto masked_tag, const uint8_t* rec, const int key0, const uint32_t none) {
             constexpr bool MASKED = decltype(masked_tag)::value;
+            constexpr int kV = kKvStep * D / 2, kKp = kKvStep * D, kVp = kKvStep * (D + NG * 4);
             const int kr = (g >> 1) + 4 * (g & 1);  // the key of fragment row g
-            float S[NG][NQ][4];
-            uint2 kc[2][NG];
+            float S[2][NG][NQ][4];
+            uint32_t kp[2][2][NG], vp[2][2][NG];  // the pairs of the keys of rows g and g + 8
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < NG; ++i)
-                    kc[j][i] = *reinterpret_cast<const uint2*>(rec + (off + 8 * j + kr) * (D / 2) + i * 32 + t * 8);
-            uint32_t kp[2][NG], vp[2][NG];  // the pairs of the keys of rows g and g + 8
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t* pk = rec + 2 * half_b + (off + 8 * j + kr) * (NG * 4);
-                // what lies behind the last key may be anything
-                const bool there = !MASKED || key0 + 8 * j + kr < w.len;
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    kp[j][i] = there ? reinterpret_cast<const uint32_t*>(pk)[i] : 0;
-                    vp[j][i] = there ? reinterpret_cast<const uint32_t*>(pk + pairs_b)[i] : 0;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) S[i][n][0] = S[i][n][1] = S[i][n][2] = S[i][n][3] = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    uint32_t x = h ? kc[0][i].y : kc[0][i].x, y = h ? kc[1][i].y : kc[1][i].x;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t A[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n)
-                            mma_16816(S[i][n], A, Q[(i * 2 + h) * 2 + j][n][0], Q[(i * 2 + h) * 2 + j][n][1]);
-                        x >>= 8;
-                        y >>= 8;
-                    }
-                }
-            float s[2][NQ][2];  // [key block][row]
-            bool grow = false;
-            {
-                float2 p[2][NG];
+            for (int h = 0; h < 2; ++h) {
+                uint2 kc[2][NG];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) p[j][i] = half2_to_float2(kp[j][i]);
+                    for (int i = 0; i < NG; ++i)
+                        kc[j][i] = *reinterpret_cast<const uint2*>(rec + (16 * h + 8 * j + kr) * (D / 2) + i * 32 + t * 8);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
+                for (int j = 0; j < 2; ++j) {
+                    const uint8_t* pk = rec + (16 * h + 8 * j + kr) * (NG * 4);
+                    // what lies behind the last key may be anything
+                    const bool there = !MASKED || (key0 + 16 * h + 8 * j + kr < w.len && !((none >> h) & 1u));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int i = 0; i < NG; ++i) {
+                        kp[h][j][i] = there ? reinterpret_cast<const uint32_t*>(pk + kKp)[i] : 0;
+                        vp[h][j][i] = there ? reinterpret_cast<const uint32_t*>(pk + kVp)[i] : 0;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) S[h][i][n][0] = S[h][i][n][1] = S[h][i][n][2] = S[h][i][n][3] = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        uint32_t x = c ? kc[0][i].y : kc[0][i].x, y = c ? kc[1][i].y : kc[1][i].x;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float v = p[j][0].y * sq[0][n][e];
+                            const uint32_t A[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
 #pragma unroll
-                            for (int i = 1; i < NG; ++i) v = fmaf(p[j][i].y, sq[i][n][e], v);
-#pragma unroll
-                            for (int i = 0; i < NG; ++i) v = fmaf(p[j][i].x, S[i][n][2 * j + e], v);
-                            if (MASKED) {
-                                const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + row / a.group;
-                                const int key = key0 + 8 * j + kr;
-                                if (key > lim || key < lim - back_keys) v = -INFINITY;
-                            }
-                            s[j][n][e] = v;
+                            for (int n = 0; n < NQ; ++n)
+                                mma_16816(S[h][i][n], A, Q[(i * 2 + c) * 2 + j][n][0], Q[(i * 2 + c) * 2 + j][n][1]);
+                            x >>= 8;
+                            y >>= 8;
                         }
-                        grow |= fmaf(fmaxf(s[0][n][e], s[1][n][e]), sc, -m[n][e]) > kLazy;
                     }
             }
+            float s[2][2][NQ][2];  // [block][rows 0-7, 8-15][query row]
+            bool grow = false;
             uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < NG; ++i) top = max(top, vp[j][i] & 0x7c00u);
+                for (int j = 0; j < 2; ++j) {
+                    float2 p[NG];
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        p[i] = half2_to_float2(kp[h][j][i]);
+                        top = max(top, vp[h][j][i] & 0x7c00u);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = p[0].y * sq[0][n][e];
+#pragma unroll
+                            for (int i = 1; i < NG; ++i) v = fmaf(p[i].y, sq[i][n][e], v);
+#pragma unroll
+                            for (int i = 0; i < NG; ++i) v = fmaf(p[i].x, S[h][i][n][2 * j + e], v);
+                            if (MASKED) {
+                                const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + row / a.group;
+                                const int key = key0 + 16 * h + 8 * j + kr;
+                                if (key > lim || key < lim - back_keys || ((none >> h) & 1u)) v = -INFINITY;
+                            }
+                            s[h][j][n][e] = v;
+                        }
+                }
+            auto largest = [&](int n, int e) { return fmaxf(fmaxf(s[0][0][n][e], s[0][1][n][e]), fmaxf(s[1][0][n][e], s[1][1][n][e])); };
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grow |= fmaf(largest(n, e), sc, -m[n][e]) > kLazy;
             if (__any_sync(~0u, grow || top > eb << 10)) {  // rare: a maximum passed the lag, or a scale the exponent
                 const uint32_t neb = max(eb, warp_max_u32(top) >> 10);
                 const float down = __uint_as_float((127u + eb - neb) << 23);
                 eb = neb;
-                ke = __uint_as_float((148u - neb) << 23);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(s[0][n][e], s[1][n][e]);
+                        float x = largest(n, e);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
                         const float nm = fmaxf(m[n][e], x * sc), f = ex2(m[n][e] - nm);
@@ -364,80 +355,80 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         }
                     }
             }
-            float2 p[2][NG];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    p[j][i] = half2_to_float2(vp[j][i]);
-                    p[j][i].x *= ke;
-                }
-            uint32_t B[NG][NQ][2];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int h = 0; h < 2; ++h) {
+                const float ke = __uint_as_float((148u - eb) << 23);
+                uint32_t B[NG][NQ][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float x[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[e] = ex2(fmaf(s[j][n][e], sc, -m[n][e]));
-                        l[n][e] += x[e];
-                    }
+                    float2 p[NG];
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
-                        float y[2];
+                        p[i] = half2_to_float2(vp[h][j][i]);
+                        p[i].x *= ke;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        float x[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const bool hide = MASKED && x[e] == 0.f;  // a key that the row does not see may hold a NaN
-                            bs[i][n][e] = hide ? bs[i][n][e] : fmaf(x[e], p[j][i].y, bs[i][n][e]);
-                            y[e] = hide ? 0.f : x[e] * p[j][i].x;
+                            x[e] = ex2(fmaf(s[h][j][n][e], sc, -m[n][e]));
+                            l[n][e] += x[e];
                         }
-                        B[i][n][j] = transpose_8x8(pack_half2(y[0], y[1]));
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            float y[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const bool hide = MASKED && x[e] == 0.f;  // a key that the row does not see may hold a NaN
+                                bs[i][n][e] = hide ? bs[i][n][e] : fmaf(x[e], p[i].y, bs[i][n][e]);
+                                y[e] = hide ? 0.f : x[e] * p[i].x;
+                            }
+                            B[i][n][j] = transpose_8x8(pack_half2(y[0], y[1]));
+                        }
                     }
                 }
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const uint8_t* pv = rec + half_b + (off + t) * (D / 2) + i * 32 + g * 4;
-                uint32_t c[4];
+                for (int i = 0; i < NG; ++i) {
+                    const uint8_t* pv = rec + kV + (16 * h + t) * (D / 2) + i * 32 + g * 4;
+                    uint32_t c[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[e] = *reinterpret_cast<const uint32_t*>(pv + 4 * e * (D / 2));
+                    for (int e = 0; e < 4; ++e) c[e] = *reinterpret_cast<const uint32_t*>(pv + 4 * e * (D / 2));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t x = __byte_perm(c[0], c[1], h ? 0x7632 : 0x5410);
-                    uint32_t y = __byte_perm(c[2], c[3], h ? 0x7632 : 0x5410);
+                    for (int hw = 0; hw < 2; ++hw) {
+                        uint32_t x = __byte_perm(c[0], c[1], hw ? 0x7632 : 0x5410);
+                        uint32_t y = __byte_perm(c[2], c[3], hw ? 0x7632 : 0x5410);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t A[4] = {x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u};
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t A[4] = {x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u};
 #pragma unroll
-                        for (int n = 0; n < NQ; ++n) mma_16816(O[i][2 * h + j][n], A, B[i][n][0], B[i][n][1]);
-                        x >>= 8;
-                        y >>= 8;
+                            for (int n = 0; n < NQ; ++n) mma_16816(O[i][2 * hw + j][n], A, B[i][n][0], B[i][n][1]);
+                            x >>= 8;
+                            y >>= 8;
+                        }
                     }
                 }
             }
         };
 
-        int tile_key = (w.lo + w.tile) * kKvTile;
-        for (int k = 0; k < cnt; k += C::kTiles, ++it, tile_key += C::kTiles * kKvTile) {
-            if (warp == 0 && it && !refill()) return;  // the stage of the iteration before
-            const int st = it % C::kStages;
-            const int steps = min(C::kTiles, cnt - k) * 4;
-            if (!mbar_wait(full + st, (it / C::kStages) & 1)) return;
-            const uint32_t gone = absent[st];
-            const uint8_t* stage = ring + st * C::kStageBytes;
+        const int end = (w.lo + w.tile + cnt) * kKvTile;
 #pragma unroll 1
-            for (int step = kw; step < steps; step += KW) {
-                const int key0 = tile_key + step * 16;
-                if ((gone >> step) & 1u || key0 > max_lim || key0 + 15 < min_from) continue;
-                const int in_stage = step * 16, off = in_stage & (P - 1);
-                const uint8_t* rec = stage + (in_stage >> a.g.page_log2) * a.g.rec;
-                if (key0 + 15 > min_lim || key0 < max_from)
-                    step16(std::true_type(), rec, off, key0);
+        for (int key0 = (w.lo + w.tile) * kKvTile + kw * kKvStep; key0 < end; key0 += KW * kKvStep) {
+            const uint32_t none = (gone >> (2 * slot)) & 3u;
+            // A wait that gives up (the error word is set) ends this warp's loads and
+            // sums; it still meets the others where they wait for it.
+            if (phase < 2 && !mbar_wait(full + slot, phase)) phase |= 2;
+            if (phase >= 2) continue;
+            if (none != 3u && key0 <= max_lim && key0 + kKvStep > min_lim - back_keys) {
+                const uint8_t* rec = ring + slot * C::kSlotBytes;
+                if (none || key0 + kKvStep - 1 > min_lim || key0 < max_lim - back_keys)
+                    step32(std::true_type(), rec, key0, none);
                 else
-                    step16(std::false_type(), rec, off, key0);
+                    step32(std::false_type(), rec, key0, none);
             }
+            if (++slot == C::kSlots) slot = 0, phase ^= 1;
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st);
+            load();
         }
 
         // ---- the piece's sums: over the lanes of a row, then over the key warps
@@ -451,7 +442,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
                     for (int i = 0; i < NG; ++i) bs[i][n][e] += __shfl_xor_sync(~0u, bs[i][n][e], o);
                 }
-        const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / ke
+        const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / 2^(21 - eb)
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -503,13 +494,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         }
 
-        const bool whole = w.tile == 0 && cnt == w.units;
-        if (!whole && w.tile == 0) {  // the item goes on in the next CTAs
-            const long long total = cum[a.n_seqs];
-            const int active = kv_active(a, total);
-            const long long end = kv_cut(total, blockIdx.x + 1, active) - cnt + w.units;
-            meta = make_int4((int)((end * active - 1) / total) - (int)blockIdx.x + 1, w.seq, w.head, w.r);
-        }
+        const bool whole = cnt == w.tiles;
         if (kw == 0) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -542,75 +527,12 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     }
                 }
         }
-        KvWalk next = w;
-        next.left -= cnt;
-        if (next.left > 0) kv_next_item(a, qs, ls, next);
+        if (!whole) join_pieces<D, C::kWarps, 1>(a, w, warp, cum[a.n_seqs], &join_last);
+        KvWalk n = w;
+        kv_next_piece(a, qs, ls, n);
         __syncwarp();
-        w = next;
+        w = n;
         __syncwarp();
-    }
-    if (tid == 0) a.meta[blockIdx.x] = meta;
-}
-
-// Joins the pieces of an item that several CTAs worked on: block (c, y) the
-// rows y, y + gridDim.y, ... of the item that began in CTA c and did not end
-// there.  The pieces are added in the order of the keys.
-template <int D>
-__global__ void __launch_bounds__(128) kv4_combine_kernel(const KvAttnArgs a) {
-    constexpr int kLanes = D / 4, kSets = 128 / kLanes;
-    __shared__ float wt[kKvMaxCtas];
-    __shared__ float red[4], l_s[kSets];
-    __shared__ float4 acc_s[kSets][kLanes];
-    pdl_wait();
-    pdl_trigger();
-    const int c = blockIdx.x, tid = threadIdx.x;
-    const int4 meta = a.meta[c];
-    if (!meta.x) return;
-    const int row0 = min(max(a.q_start[meta.y], 0), a.n_tokens);
-    const int n = min(max(a.q_start[meta.y + 1], 0), a.n_tokens) - row0;
-    auto slot = [&](int i) { return (size_t)(i ? 2 * (c + i) : 2 * c + 1); };
-    for (int row = blockIdx.y; row < a.tq * a.group; row += gridDim.y) {
-        const int tok = meta.w * a.tq + row / a.group;
-        if (tok >= n) break;
-        float m = -1e30f;
-        for (int i = tid; i < meta.x; i += 128) m = fmaxf(m, a.part_ml[slot(i) * a.rows + row].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        if ((tid & 31) == 0) red[tid >> 5] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        for (int i = tid; i < meta.x; i += 128) wt[i] = ex2(a.part_ml[slot(i) * a.rows + row].x - m);
-        __syncthreads();
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int set = tid / kLanes, d4 = tid % kLanes;
-#pragma unroll 8
-        for (int i = set; i < meta.x; i += kSets) {
-            const float f = wt[i];
-            const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * a.rows + row) * D)[d4];
-            l += f * a.part_ml[slot(i) * a.rows + row].y;
-            acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
-        }
-        acc_s[set][d4] = acc;
-        if (d4 == 0) l_s[set] = l;
-        __syncthreads();
-        if (tid < kLanes) {
-            float sum = 0.f;
-            acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kSets; ++i) {
-                const float4 v = acc_s[i][tid];
-                sum += l_s[i];
-                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-            }
-            const float inv = sum != 0.f ? 1.f / sum : 0.f;
-            uint2 u;
-            u.x = (uint32_t)f32_to_bf16_bits(acc.x * inv) | ((uint32_t)f32_to_bf16_bits(acc.y * inv) << 16);
-            u.y = (uint32_t)f32_to_bf16_bits(acc.z * inv) | ((uint32_t)f32_to_bf16_bits(acc.w * inv) << 16);
-            *reinterpret_cast<uint2*>(a.out + (long long)(row0 + tok) * a.o_st +
-                                      (long long)(meta.z * a.group + row % a.group) * a.o_sh + tid * 4) = u;
-        }
-        __syncthreads();
     }
 }
 
@@ -623,11 +545,14 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.rows = C::kRows;
     a.tq = C::kRows / a.group;
     a.min_units = 2;
+    // An item's own time in tiles: 0, 2, 4, 8 and 16 gave 91.0, 82.9, 78.2, 77.3 and 81.4 us for 64
+    // ragged decode requests, 17.7, 15.9, 15.3, 13.7 and 14.7 us for 33 windowed ones, and 34.3, 31.0,
+    // 29.7, 30.9 and 32.6 us for 48-row verification, whose tiles take longer.
+    a.pad = RT == 1 ? 8 : 4;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
     if (hs_host::launch_pdl(kv4_decode_kernel<D, NQ, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
         return HS_ERR_CUDA;
-    if (hs_host::launch_pdl(kv4_combine_kernel<D>, dim3(ctas, 16), dim3(128), 0, s, a) != cudaSuccess) return HS_ERR_CUDA;
     return HS_OK;
 }
 
@@ -644,10 +569,10 @@ int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
 
 using namespace hs_host;
 
-// Partial sums, (maximum, sum) pairs and item records of the widest launch.
+// Counters of arrived pieces, (maximum, sum) pairs and partial sums of the widest launch.
 static size_t kv4_ws_bytes(int dim) {
     const size_t rows = hs::kKvWsRows;
-    return round_up(rows * dim * 4, 256) + round_up(rows * 8, 256) + hs::kKvMaxCtas * 16;
+    return round_up(3 * hs::kKvMaxCtas * 4, 256) + round_up(rows * 8, 256) + rows * dim * 4;
 }
 
 extern "C" size_t hs_kv4_attention_workspace_size(const hs_kv4_cache* c, int n_seqs, int n_q_heads) {
@@ -688,9 +613,10 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.group = n_q_heads / cache->n_kv_heads;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.part_o = reinterpret_cast<float*>(w);
-    a.part_ml = reinterpret_cast<float2*>(w + round_up(rows * dim * 4, 256));
-    a.meta = reinterpret_cast<int4*>(w + round_up(rows * dim * 4, 256) + round_up(rows * 8, 256));
+    a.joined = reinterpret_cast<int*>(w);
+    w += round_up(3 * hs::kKvMaxCtas * 4, 256);
+    a.part_ml = reinterpret_cast<float2*>(w);
+    a.part_o = reinterpret_cast<float*>(w + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long need = std::max((long long)max_new, 1ll) * a.group;
     const int r = dim == 64 ? hs::launch_rows<64>(a, need, sms, s) : hs::launch_rows<128>(a, need, sms, s);

@@ -6,14 +6,15 @@
 // run of 64-key tiles that some row of it sees.  All items' tiles, in the
 // order (request, kv head, row tile, key tile), form one line that is cut into
 // equal pieces, one a CTA: long and short requests, prompts and single tokens
-// load the SMs alike, and the host needs none of the lengths.  An item that a
-// cut divides leaves partial results that the combine kernel joins.
+// load the SMs alike, and the host needs none of the lengths.  The pieces of an
+// item that a cut divides are joined by the CTA that comes last.
 #pragma once
 
 #include "hs_kv4.cuh"
 
 namespace hs {
 
+constexpr int kKvMaxCtas = 456;  // three on each of 152 SMs
 constexpr int kKvTile = 64;  // keys of a tile; pages of 16 to 64 tokens divide it
 
 struct KvAttnArgs {
@@ -25,11 +26,11 @@ struct KvAttnArgs {
     const int* q_start;
     const int* seq_len;
     const int* table;
-    int width, n_seqs, n_tokens, group, window, rows, tq, min_units;
+    int width, n_seqs, n_tokens, group, window, rows, tq, min_units, pad;
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [2 * CTAs][rows][dim] partial sums
     float2* part_ml;     // [2 * CTAs][rows] (maximum, sum)
-    int4* meta;          // [CTAs]: the item whose first piece ends this CTA's run: pieces (0: none), request, head, row tile
+    int* joined;         // [3 * CTAs] arrivals of pieces, zero between calls
 };
 
 struct KvSpan {
@@ -49,14 +50,15 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int n, int len, i
     }
     return s;
 }
-__device__ __forceinline__ int kv_span_units(const KvSpan& s) { return max(1, s.hi - s.lo + 1); }
+__device__ __forceinline__ int kv_span_tiles(const KvSpan& s) { return max(1, s.hi - s.lo + 1); }
+__device__ __forceinline__ int kv_span_units(const KvAttnArgs& a, const KvSpan& s) { return kv_span_tiles(s) + a.pad; }
 
-// Where a CTA's run of units stands.
+// Where a CTA's run of units stands; it always stands on a tile.
 struct KvWalk {
     long long left;          // units of the CTA's run still to do (this one included)
     int seq, head, r, tile;  // tile: unit within the item
     int n, len, row0;        // of the request: new tokens, length, first row of q
-    int units;               // of the item
+    int units, tiles;        // of the item: with its pad, and without
     int lo, hi;
     bool first;              // the run began inside this item
 };
@@ -66,6 +68,24 @@ struct KvWalk {
 __device__ __forceinline__ void kv_request(const KvAttnArgs& a, const int* qs, const int* ls, int i, int& n, int& len) {
     n = max(qs[i + 1] - qs[i], 0);
     len = (int)min((long long)max(ls[i], 0), (long long)a.width << a.g.page_log2);
+}
+
+// Key tiles of a request, over its row tiles (whole warps; every lane gets it).
+__device__ __forceinline__ int kv_many_units(const KvAttnArgs& a, int n, int len) {
+    const int tiles = (n + a.tq - 1) / a.tq;
+    int s = 0;
+    for (int r = threadIdx.x & 31; r < tiles; r += 32) s += kv_span_units(a, kv_span(a, n, len, r));
+    return (int)warp_add_u32((uint32_t)s);
+}
+
+__device__ __forceinline__ long long warp_scan(long long v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
 }
 
 // Fills cum[0..n_seqs] (units before each request), qs[0..n_seqs] and
@@ -82,7 +102,7 @@ __device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* l
         int n, len;
         kv_request(a, qs, ls, i, n, len);
         if (n <= a.tq)
-            cum[i + 1] = n ? (long long)a.g.heads * kv_span_units(kv_span(a, n, len, 0)) : 0;
+            cum[i + 1] = n ? (long long)a.g.heads * kv_span_units(a, kv_span(a, n, len, 0)) : 0;
         else
             many = true;
     }
@@ -91,10 +111,7 @@ __device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* l
             int n, len;
             kv_request(a, qs, ls, i, n, len);
             if (n <= a.tq) continue;
-            const int tiles = (n + a.tq - 1) / a.tq;
-            int s = 0;
-            for (int r = lane; r < tiles; r += 32) s += kv_span_units(kv_span(a, n, len, r));
-            s = (int)warp_add_u32((uint32_t)s);
+            const int s = kv_many_units(a, n, len);
             if (lane == 0) cum[i + 1] = (long long)a.g.heads * s;
         }
         __syncthreads();
@@ -103,12 +120,7 @@ __device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* l
         long long base = 0;
         for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
             const int i = i0 + lane;
-            long long v = i < a.n_seqs ? cum[i + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(~0u, v, o);
-                if (lane >= o) v += t;
-            }
+            const long long v = warp_scan(i < a.n_seqs ? cum[i + 1] : 0);
             if (i < a.n_seqs) cum[i + 1] = base + v;
             base += __shfl_sync(~0u, v, 31);
         }
@@ -119,24 +131,70 @@ __device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* l
 
 __device__ __forceinline__ void kv_set_item(const KvAttnArgs& a, KvWalk& w) {
     const KvSpan s = kv_span(a, w.n, w.len, w.r);
-    w.lo = s.lo, w.hi = s.hi, w.units = kv_span_units(s);
+    w.lo = s.lo, w.hi = s.hi, w.tiles = kv_span_tiles(s), w.units = w.tiles + a.pad;
 }
 
-// CTAs that share the line; the first unit of CTA c is total * c / active.
-__device__ __forceinline__ int kv_active(const KvAttnArgs& a, long long total) {
-    return (int)min((long long)gridDim.x, (total + a.min_units - 1) / a.min_units);
+// Quotient of numbers that are not negative; nearly always both fit 32 bits.
+__device__ __forceinline__ long long kv_div(long long x, long long y) {
+    return ((x | y) >> 32) ? x / y : (long long)((uint32_t)x / (uint32_t)y);
 }
-__device__ __forceinline__ long long kv_cut(long long total, int c, int active) { return total * c / active; }
+
+// The cut of the line: the first `more` of `active` CTAs take q + 1 units, the others q.
+struct KvCut {
+    long long q;
+    int active, more;
+    __device__ __forceinline__ long long at(int c) const { return q * c + min(c, more); }
+    __device__ __forceinline__ int cta_of(long long unit) const {
+        const long long wide = (q + 1) * more;
+        return unit < wide ? (int)kv_div(unit, q + 1) : more + (int)kv_div(unit - wide, q);
+    }
+};
+__device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, long long total) {
+    KvCut c;
+    c.active = (int)max(1ll, min((long long)gridDim.x, kv_div(total + a.min_units - 1, a.min_units)));
+    c.q = kv_div(total, c.active);
+    c.more = (int)(total - c.q * c.active);
+    return c;
+}
+
+// To the next item (the current one's units are done).
+__device__ __forceinline__ void kv_next_item(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w) {
+    w.first = false;
+    w.tile = 0;
+    if (++w.r * a.tq >= w.n) {
+        w.r = 0;
+        if (++w.head == a.g.heads) {
+            w.head = 0;
+            do {
+                ++w.seq;
+                kv_request(a, qs, ls, w.seq, w.n, w.len);
+            } while (!w.n);
+            w.row0 = qs[w.seq];
+        }
+    }
+    kv_set_item(a, w);
+}
+
+// The tiles of the run's current item that are its own, and the units they end with.
+__device__ __forceinline__ int kv_piece_tiles(const KvWalk& w) { return (int)min(w.left, (long long)(w.tiles - w.tile)); }
+// Takes `units` units off the run, which end the current item or the run.
+__device__ __forceinline__ void kv_skip(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w, long long units) {
+    w.left -= min(w.left, units);
+    if (w.left > 0) kv_next_item(a, qs, ls, w);
+}
+__device__ __forceinline__ void kv_next_piece(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w) {
+    kv_skip(a, qs, ls, w, w.units - w.tile);
+}
 
 // Start of this CTA's run (called by whole warps; every lane gets the same).
 __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const long long* cum) {
     KvWalk w;
     const long long total = cum[a.n_seqs];
-    const int active = kv_active(a, total);
+    const KvCut cut = kv_cut(a, total);
     w.left = 0;
-    if (!total || (int)blockIdx.x >= active) return w;
-    const long long u0 = kv_cut(total, blockIdx.x, active);
-    w.left = kv_cut(total, blockIdx.x + 1, active) - u0;
+    if (!total || (int)blockIdx.x >= cut.active) return w;
+    const long long u0 = cut.at(blockIdx.x);
+    w.left = cut.at(blockIdx.x + 1) - u0;
     int lo = 0, hi = a.n_seqs;
     while (hi - lo > 1) {  // the last request with cum <= u0: it has units
         const int mid = (lo + hi) >> 1;
@@ -146,16 +204,16 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
     w.seq = lo;
     kv_request(a, qs, ls, lo, w.n, w.len);
     w.row0 = qs[lo];
-    const long long per_head = (cum[lo + 1] - cum[lo]) / a.g.heads;
+    const long long per_head = kv_div(cum[lo + 1] - cum[lo], a.g.heads);
     long long rest = u0 - cum[lo];
-    w.head = (int)(rest / per_head);
+    w.head = (int)kv_div(rest, per_head);
     rest -= (long long)w.head * per_head;
     const int tiles = (w.n + a.tq - 1) / a.tq;
     w.r = 0;
     if (tiles > 1) {
         const int lane = threadIdx.x & 31;
         for (int r0 = 0; r0 < tiles; r0 += 32) {
-            const int mine = r0 + lane < tiles ? kv_span_units(kv_span(a, w.n, w.len, r0 + lane)) : 0;
+            const int mine = r0 + lane < tiles ? kv_span_units(a, kv_span(a, w.n, w.len, r0 + lane)) : 0;
             int incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -175,25 +233,8 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
     w.tile = (int)rest;
     w.first = true;
     kv_set_item(a, w);
+    if (w.tile >= w.tiles) kv_skip(a, qs, ls, w, w.units - w.tile);  // the run begins in a pad
     return w;
-}
-
-// To the next item (the current one's units are done).
-__device__ __forceinline__ void kv_next_item(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w) {
-    w.first = false;
-    w.tile = 0;
-    if (++w.r * a.tq >= w.n) {
-        w.r = 0;
-        if (++w.head == a.g.heads) {
-            w.head = 0;
-            do {
-                ++w.seq;
-                kv_request(a, qs, ls, w.seq, w.n, w.len);
-            } while (!w.n);
-            w.row0 = qs[w.seq];
-        }
-    }
-    kv_set_item(a, w);
 }
 
 }  // namespace hs

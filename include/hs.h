@@ -447,7 +447,10 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  * values (chunks) with fp16 queries scaled by a power of two, fp32 sums,
  * probabilities rounded to fp16 for the second product.
  * Deterministic.  Calls sharing one workspace must not overlap on the GPU.
- * The workspace needs no clearing. */
+ * The workspace must be ZERO-FILLED before its first use; each call leaves the
+ * counters at its start at zero, so consecutive calls of any shapes and CUDA
+ * graph replays need no clearing in between.  A workspace that another entry
+ * point has written must be zero-filled again first. */
 size_t hs_kv4_attention_workspace_size(const hs_kv4_cache* cache, int n_seqs, int n_q_heads);
 int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q_bf16_dev, long long q_stride_token,
                      long long q_stride_head, const int* q_start_dev, const int* seq_len_dev, const int* table_dev,

@@ -154,8 +154,8 @@ class Requests:
         n = len(self.len)
         q = self.q.to(dev) if q is None else q
         out = torch.full_like(q, float("nan")) if out is None else out
-        if ws is None:  # any contents will do
-            ws = torch.full((hs.hs_kv4_attention_workspace_size(cache, n, self.hq),), 0xA5, dtype=torch.uint8, device=dev)
+        if ws is None:
+            ws = torch.zeros(hs.hs_kv4_attention_workspace_size(cache, n, self.hq), dtype=torch.uint8, device=dev)
         table = torch.from_numpy(self.table).to(dev) if table is None else table
         hs.hs_kv4_attention(cache, q, torch.from_numpy(self.starts).to(dev),
                             torch.tensor(self.len, dtype=torch.int32, device=dev), table, n,

@@ -297,7 +297,7 @@ def test_attention_strides_streams_and_reuse_of_the_workspace():
     r.run(hs, 0.09, q=wide_q[:, 2:18, :128], out=out, stream=s)
     _close(out, ref, 0.09)
     assert (wide_o[:, 16] == 7).all() and (wide_o[:, :, 128:] == 7).all()
-    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
     a = r.run(hs, 0.09, ws=ws)
     big = _kv4.Requests(22, [3000], [1], 32, 2, 128, 64)
     b0 = big.run(hs, 0.09, ws=ws)
