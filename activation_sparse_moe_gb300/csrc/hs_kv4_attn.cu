@@ -19,9 +19,8 @@
 
 namespace hs {
 
-constexpr int kKvWsRows = 2 * 152 * 64;  // rows of partial sums of the widest launch
+constexpr int kKvTile = 64;        // keys of a tile; pages of 16 to 64 tokens divide it
 constexpr int kKvStep = 32;        // keys of a warp's step
-constexpr float kLazy = 8.f;      // a row's maximum may lag by a factor 2^8 before the sums are rescaled
 
 // D += A * B, one 16 x 8 x 16 product of fp16 operands in fp32.
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -200,7 +199,8 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     for (int h = 0; h < 2; ++h) {
                         v[n][i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
                         top = max(max(top, v[n][i][h].x & 0x7fff7fffu), max(v[n][i][h].y & 0x7fff7fffu, max(v[n][i][h].z & 0x7fff7fffu, v[n][i][h].w & 0x7fff7fffu)));
-                        top = max(top, max(max(v[n][i][h].x << 16, v[n][i][h].y << 16), max(v[n][i][h].z << 16, v[n][i][h].w << 16)) & 0x7fffffffu);
+                        top = max(top, max(max((v[n][i][h].x << 16) & 0x7fffffffu, (v[n][i][h].y << 16) & 0x7fffffffu),
+                                           max((v[n][i][h].z << 16) & 0x7fffffffu, (v[n][i][h].w << 16) & 0x7fffffffu)));
                     }
             }
             // f = 2^-e, 2^e <= largest < 2^(e+1); zeros and infinities keep f = 1
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     }
                 }
         }
-        if (!whole) join_pieces<D, C::kWarps, 1>(a, w, warp, cum[a.n_seqs], &join_last);
+        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, cum[a.n_seqs], &join_last, add_pieces<D, C::kWarps>);
         KvWalk n = w;
         kv_next_piece(a, qs, ls, n);
         __syncwarp();
@@ -545,6 +545,7 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.rows = C::kRows;
     a.tq = C::kRows / a.group;
     a.min_units = 2;
+    a.tile_log2 = 6;
     // An item's own time in tiles: 0, 2, 4, 8 and 16 gave 91.0, 82.9, 78.2, 77.3 and 81.4 us for 64
     // ragged decode requests, 17.7, 15.9, 15.3, 13.7 and 14.7 us for 33 windowed ones, and 34.3, 31.0,
     // 29.7, 30.9 and 32.6 us for 48-row verification, whose tiles take longer.
@@ -568,6 +569,10 @@ int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
 }  // namespace hs
 
 using namespace hs_host;
+
+// Rows of a request (new tokens x query heads of a kv head) from which the
+// chunk kernel is used.
+constexpr int kPrefillRows = 65;
 
 // Counters of arrived pieces, (maximum, sum) pairs and partial sums of the widest launch.
 static size_t kv4_ws_bytes(int dim) {
@@ -619,6 +624,7 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.part_o = reinterpret_cast<float*>(w + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long need = std::max((long long)max_new, 1ll) * a.group;
+    if (need >= kPrefillRows && hs_kv4_prefill_fits(dim, n_seqs)) return hs_kv4_prefill(a, dim, sms, s);
     const int r = dim == 64 ? hs::launch_rows<64>(a, need, sms, s) : hs::launch_rows<128>(a, need, sms, s);
     return r != HS_OK ? r : launch_err();
 }
@@ -628,5 +634,5 @@ unsigned hs_kv4_take_status() {
     unsigned v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, hs::g_status, sizeof(v)) != cudaSuccess) return 0;
     cudaMemcpyToSymbol(hs::g_status, &zero, sizeof(zero));
-    return v;
+    return v | hs_kv4_prefill_take_status();
 }

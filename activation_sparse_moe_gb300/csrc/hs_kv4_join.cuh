@@ -28,9 +28,9 @@ template <> struct FloatVec<4> { using T = float4; };
 
 // Adds pieces first, first + step, ... (count of them, at most 64) of the item
 // that began in CTA c: into out if `final`, else into piece `first`.  Called by
-// whole warps, `warp` of WARPS; a warp takes four rows at a time (16 loads in
-// flight a lane: it is latency that bounds this).
-template <int D, int WARPS>
+// whole warps, `warp` of WARPS; a warp takes four rows of BATCH pieces at a
+// time (it is latency that bounds this).
+template <int D, int WARPS, int BATCH = 4>
 __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
                                         bool final) {
     constexpr int V = D / 32;
@@ -64,16 +64,16 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[x][e] = 0.f;
         }
-        for (int i0 = 0; i0 < count; i0 += 4) {
-            Vec v[4][4];
+        for (int i0 = 0; i0 < count; i0 += BATCH) {
+            Vec v[BATCH][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 const size_t at = piece_slot(c, first + min(i0 + i, count - 1) * step) * a.rows;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < BATCH; ++i)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     float f = __shfl_sync(~0u, i0 < 32 ? wt[x][0] : wt[x][1], (i0 + i) & 31);
@@ -110,9 +110,10 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 }
 
 // Called by WARPS warps (`warp` the calling one's index) of a CTA that has
-// written its piece of w's item.  *last is a word of shared memory; the warps meet at named barrier BAR.
-template <int D, int WARPS, int BAR>
-__device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, long long total, int* last) {
+// written its piece of w's item.  *last is a word of shared memory; the warps meet at named barrier BAR; add is
+// add_pieces.
+template <int WARPS, int BAR, typename Add>
+__device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, long long total, int* last, Add add) {
     const KvCut cut = kv_cut(a, total);
     const int me = blockIdx.x;
     const bool lead = warp == 0 && (threadIdx.x & 31) == 0;
@@ -134,15 +135,15 @@ __device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w
         return *last != 0;
     };
     if (pieces <= kJoin) {
-        if (arrive(a.joined + c, pieces)) add_pieces<D, WARPS>(a, w, warp, c, 0, 1, pieces, true);
+        if (arrive(a.joined + c, pieces)) add(a, w, warp, c, 0, 1, pieces, true);
         return;
     }
     const int run = (me - c) / kJoin, size = min(kJoin, pieces - run * kJoin);
     // A run's counter is that of its first CTA; an item that begins in that CTA has another.
     if (!arrive(a.joined + kKvMaxCtas * (run ? 2 : 1) + c + run * kJoin, size)) return;
-    add_pieces<D, WARPS>(a, w, warp, c, run * kJoin, 1, size, false);
+    add(a, w, warp, c, run * kJoin, 1, size, false);
     const int runs = (pieces + kJoin - 1) / kJoin;
-    if (arrive(a.joined + c, runs)) add_pieces<D, WARPS>(a, w, warp, c, 0, kJoin, runs, true);
+    if (arrive(a.joined + c, runs)) add(a, w, warp, c, 0, kJoin, runs, true);
 }
 
 }  // namespace hs

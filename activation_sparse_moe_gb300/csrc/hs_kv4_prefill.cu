@@ -1,0 +1,504 @@
+// Attention of chunks of new tokens over the 4-bit key/value cache on the
+// tensor cores, GB300 (sm_103a).  Contract: hs_kv4_attention in hs.h; the
+// division of the work: hs_kv4_sched.cuh.
+//
+// A CTA takes 256 query rows (tokens x the query heads of one kv head) against
+// tiles of 128 keys: two row tiles of 128, each S = Q K^T (tcgen05, fp16
+// operands, fp32 in tensor memory), its softmax, and O += P V with P read from
+// tensor memory where S stood.  Roles, one CTA an SM:
+//   warps 0-3, 4-7   a row tile each, a thread a row: queries in, softmax, output
+//   warps 8-11       take the codes apart: K and V tiles of 128 keys in fp16
+//   warp 12          copies packed codes and pairs, page by page
+//   warp 13          issues the matrix products
+// The two row tiles take turns: one's softmax runs under the other's products,
+// and both use a K and V tile that was taken apart once.  Keys and values are
+// scale * code + bias rounded once to fp16; channels stand in both operands in
+// the order in which a word's nibbles come apart ([0 4 1 5 2 6 3 7] of each
+// eight), which the output undoes.
+//
+// Bounds, for 256 rows x 128 keys at head_dim 128 on one SM: the products 2048
+// cycles at the dense fp16 rate, the exponentials 1024 to 2048, the softmax's
+// other arithmetic about 1000 issue cycles, taking codes apart about 500.
+#include "hs_kv4_join.cuh"
+#include "hs_tc.cuh"
+
+namespace hs {
+
+constexpr int kPfKeys = 128, kPfRows = 256, kPfPacked = 3, kPfSlots = 3, kPfInfo = 8;
+constexpr int kPfThreads = 16 * 32;  // warps 14 and 15 fill the last warpgroup: registers move by warpgroups
+constexpr int kPfMaxSmem = 227 * 1024 - 1024;  // dynamic; the rest is the static part
+constexpr float kPfUp = 6.f;  // probabilities are held times 2^6: at most 2^14 in fp16, and small ones keep their bits
+
+template <int D>
+struct PrefillCfg {
+    static constexpr int kNg = D / 64;
+    static constexpr int kQBytes = 128 * D * 2;          // of a row tile
+    static constexpr int kTileBytes = kPfKeys * D * 2;   // a K or V tile
+    static constexpr int kPackedBytes = kPfKeys * (D / 2 + 4 * kNg);
+    static constexpr int kFixed = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes;
+    static constexpr int smem(int n_seqs) { return 1024 + kFixed + 1024 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16; }
+};
+
+struct PfShared {
+    uint64_t packed_full[kPfPacked], packed_empty[kPfPacked], kv_full[kPfSlots], kv_empty[kPfSlots];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint32_t gone[kPfInfo];            // per key tile: blocks of 16 keys that are not there
+    uint32_t nan_any[kPfInfo];         // some value of the tile is NaN
+    uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
+    uint32_t tmem;
+    int join_last;
+};
+
+// Shared-memory descriptor of a tile whose rows run along K (keys) and whose
+// 128-byte swizzled lines hold 64 elements along N: `lead` bytes to the next 64
+// along N, 1024 to the next 8 rows.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_addr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lead >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
+
+// Eight codes of a word as scale * code + bias in fp16: 1024 + c is exact in
+// fp16, so is c after the subtraction, and the product is rounded once.
+__device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
+    const __half2 k = as_h2(0x64006400u);
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = as_u32(__hfma2(__hsub2(as_h2(((w >> (4 * i)) & 0x000f000fu) | 0x64006400u), k), s, b));
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// A call of its own: its registers are not the softmax's.
+template <int D>
+__device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
+                                              bool final) {
+    add_pieces<D, 8, 2>(a, w, warp, c, first, step, count, final);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttnArgs a) {
+    using C = PrefillCfg<D>;
+    constexpr int NG = C::kNg;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* q_s = smem;                                    // [2] row tiles
+    uint8_t* kv_s = smem + 2 * C::kQBytes;                  // [kPfSlots] K and V tiles in turn
+    uint8_t* packed_s = kv_s + kPfSlots * C::kTileBytes;    // [kPfPacked] codes, pairs
+    PfShared& sh = *reinterpret_cast<PfShared*>(packed_s + kPfPacked * C::kPackedBytes);
+    static_assert(sizeof(PfShared) <= 1024, "barriers");
+    long long* cum = reinterpret_cast<long long*>(packed_s + kPfPacked * C::kPackedBytes + 1024);
+    int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
+    int* ls = qs + a.n_seqs + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kPfPacked; ++i) mbar_init(sh.packed_full + i, 1), mbar_init(sh.packed_empty + i, 4);
+        for (int i = 0; i < kPfSlots; ++i) mbar_init(sh.kv_full + i, 4), mbar_init(sh.kv_empty + i, 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
+        fence_mbar_init();
+    }
+    if (tid < kPfInfo) {
+        sh.nan_any[tid] = 0;
+        for (int i = 0; i < 8; ++i) sh.nan_keys[tid][i >> 2][i & 3] = 0;
+    }
+    if (warp == 13) tmem_alloc(&sh.tmem, 512);
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    kv_schedule(a, qs, ls, cum);
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
+    // A warp's place in the line, in shared memory: looked at once an item.
+    __shared__ KvWalk walks[kPfThreads / 32];
+    KvWalk& w = walks[warp];
+    w = kv_begin(a, qs, ls, cum);
+    __syncwarp();
+    auto next_piece = [&]() {
+        KvWalk n = w;
+        kv_next_piece(a, qs, ls, n);
+        __syncwarp();
+        w = n;
+        __syncwarp();
+    };
+    // 128 registers a thread at launch: 168 for the softmax, 88 for the others (2 * 168 + 2 * 88 = 4 * 128).
+    auto rows_of = [&](const KvWalk& v) { return min(a.tq, v.n - v.r * a.tq) * a.group; };
+
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 12) {
+        // ---- packed codes and pairs: K then V of each tile, two copies a page
+        const int per_tile = kPfKeys >> a.g.page_log2, codes = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
+        const int pg = lane >> 1, what = lane & 1;  // lane: codes or pairs of page pg of a tile
+        uint32_t f = 0, tiles = 0;
+        bool dead = false;
+        for (; w.left > 0 && !dead; next_piece()) {
+            const int cnt = kv_piece_tiles(w);
+            int base = -1, held = -1;
+            for (int k = 0; k < cnt && !dead; ++k, ++tiles) {
+                const int p0 = (w.lo + w.tile + k) * per_tile;
+                if (base < 0 || p0 - base >= 32) {  // the next 32 table entries, one a lane
+                    base = p0;
+                    const bool in = w.hi >= w.lo && (long long)(base + lane) << a.g.page_log2 < w.len;
+                    held = in ? a.table[(size_t)w.seq * a.width + base + lane] : -1;
+                }
+                const int page = __shfl_sync(~0u, held, (p0 - base + pg) & 31);
+                const bool here = pg < per_tile && (uint32_t)page < (uint32_t)a.g.n_pages;
+                const unsigned mask = __ballot_sync(~0u, here);
+                for (int v = 0; v < 2; ++v, ++f) {
+                    const int st = f % kPfPacked;
+                    if (f >= kPfPacked && !mbar_wait(sh.packed_empty + st, (f / kPfPacked + 1) & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (v == 0) {
+                            uint32_t gone = 0;
+                            for (int i = 0; i < 8; ++i)
+                                if (!((mask >> (2 * (i * 16 >> a.g.page_log2))) & 1u)) gone |= 1u << i;
+                            sh.gone[tiles % kPfInfo] = gone;
+                        }
+                        mbar_arrive_expect_tx(sh.packed_full + st, (uint32_t)(__popc(mask) >> 1) * (uint32_t)(codes + pairs));
+                    }
+                    __syncwarp();
+                    if (here) {
+                        const uint8_t* src = kv_record(a.g, page, w.head) + (what ? 2 * codes + v * pairs : v * codes);
+                        uint8_t* dst = packed_s + st * C::kPackedBytes + (what ? kPfKeys * (D / 2) + pg * pairs : pg * codes);
+                        bulk_g2s(dst, src, (uint32_t)(what ? pairs : codes), sh.packed_full + st, policy_evict_last());
+                    }
+                }
+            }
+        }
+    } else if (warp == 13) {
+        // ---- matrix products, issued by lane 0
+        {
+            constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kPfKeys);
+            constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | (1u << 16);  // V: rows along K
+            uint32_t f = 0, p_count[2] = {0, 0}, q_count[2] = {0, 0};
+            bool dead = false;
+            auto values = [&](int x, uint32_t fv, bool first) {  // O += P V of row tile x
+                const uint32_t at = smem_u32(kv_s + (fv % kPfSlots) * C::kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < kPfKeys / 16; ++kk)
+                    umma_f16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, umma_desc_sw128_mn(at + kk * 2048, kPfKeys * 128),
+                                    idesc_o, !first || kk);
+            };
+            for (; w.left > 0 && !dead; next_piece()) {
+                const int cnt = kv_piece_tiles(w), nx = rows_of(w) > 128 ? 2 : 1;
+                for (int k = 0; k <= cnt && !dead; ++k) {
+                    // tile k's scores and tile k - 1's outputs, a row tile at a time
+                    const uint32_t fk = f + 2 * k, fv = f + 2 * k - 1;  // fills of K k and V k - 1
+                    if (k < cnt && !mbar_wait(sh.kv_full + fk % kPfSlots, (fk / kPfSlots) & 1)) dead = true;
+                    if (k && !dead && !mbar_wait(sh.kv_full + fv % kPfSlots, (fv / kPfSlots) & 1)) dead = true;
+                    for (int x = 0; x < nx && !dead; ++x) {
+                        if (k) {
+                            if (!mbar_wait(sh.p_full + x, p_count[x]++ & 1)) {
+                                dead = true;
+                                break;
+                            }
+                            tc_fence_after();
+                            if (lane == 0) {
+                                values(x, fv, k == 1);
+                                if (k == cnt) umma_commit(sh.o_full + x);
+                                if (x == nx - 1) umma_commit(sh.kv_empty + fv % kPfSlots);
+                            }
+                        } else if (!mbar_wait(sh.q_full + x, q_count[x]++ & 1)) {
+                            dead = true;
+                            break;
+                        }
+                        if (k < cnt && lane == 0) {
+                            tc_fence_after();
+                            const uint32_t qa = smem_u32(q_s + x * C::kQBytes), ka = smem_u32(kv_s + (fk % kPfSlots) * C::kTileBytes);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t at = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                                umma_f16(tmem + x * 128, umma_desc_sw128(qa + at), umma_desc_sw128(ka + at), idesc_s, kk != 0);
+                            }
+                            umma_commit(sh.s_full + x);
+                        }
+                    }
+                    if (k < cnt && !dead && lane == 0) umma_commit(sh.kv_empty + fk % kPfSlots);
+                    __syncwarp();
+                }
+                f += 2 * cnt;
+            }
+        }
+        __syncwarp();
+    }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // ---- codes taken apart into swizzled fp16 tiles
+        const int idx = tid - 256;
+        uint32_t f = 0, tiles = 0;
+        bool dead = false;
+        for (; w.left > 0 && !dead; next_piece()) {
+            const int cnt = kv_piece_tiles(w);
+            for (int k = 0; k < cnt && !dead; ++k, ++tiles) {
+                const int key0 = (w.lo + w.tile + k) * kPfKeys, info = tiles % kPfInfo;
+                for (int v = 0; v < 2; ++v, ++f) {
+                    const int st = f % kPfPacked, slot = f % kPfSlots;
+                    if (!mbar_wait(sh.packed_full + st, (f / kPfPacked) & 1) ||
+                        (f >= kPfSlots && !mbar_wait(sh.kv_empty + slot, (f / kPfSlots + 1) & 1))) {
+                        dead = true;
+                        break;
+                    }
+                    const uint32_t gone = sh.gone[info];
+                    const uint8_t* from = packed_s + st * C::kPackedBytes;
+                    uint8_t* to = kv_s + slot * C::kTileBytes;
+                    if (v == 0 && idx < 9) {  // for four tiles on: no warp here is two ahead of another
+                        const int on = (tiles + 4) % kPfInfo;
+                        if (idx == 8) sh.nan_any[on] = 0;
+                        else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
+                    }
+#pragma unroll 2
+                    for (int i = 0; i < 2 * NG; ++i) {  // 32 channels of a key each
+                        const int id = i * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
+                        const uint4 q = *reinterpret_cast<const uint4*>(from + id * 16);
+                        uint32_t sb = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
+                        const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
+                        // A NaN value must not meet the zero probability of a row that does not see it.
+                        const bool nan = v && (sb & 0x7c000000u) == 0x7c000000u;
+                        if (there && nan) {
+                            atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
+                            sh.nan_any[info] = 1;
+                        }
+                        if (!there || nan) sb = 0;
+                        const __half2 p = as_h2(sb), s = __low2half2(p), b = __high2half2(p);
+                        uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
+                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(sh.packed_empty + st);
+                        mbar_arrive(sh.kv_full + slot);
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        // ---- a row tile's queries, softmax and output, a thread a row
+        const int x = warp >> 2, row = tid & 127, r = x * 128 + row;
+        const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+        const int back_keys = a.window ? a.window - 1 : 0x3fffffff;
+        uint32_t tiles = 0, s_count = 0, o_count = 0;
+        bool dead = false;
+        while (w.left > 0) {
+            const int cnt = kv_piece_tiles(w), nrows = rows_of(w), ctx = w.len - w.n;
+            const bool whole = cnt == w.tiles;
+            if (x * 128 < nrows) {
+                const bool valid = r < nrows;
+                const int tok = w.r * a.tq + r / a.group, lim = ctx + tok;
+                const long long q_row = w.row0 + tok, q_head = w.head * a.group + r % a.group;
+                float sc;
+                {
+                    // The row in fp16, scaled by the power of two that brings its largest
+                    // channel to [2^8, 2^9): bf16 values down to 2^-22 of it stay exact.
+                    uint32_t top = 0;
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + q_row * a.q_st + q_head * a.q_sh);
+#pragma unroll 8
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = valid ? src[i] : make_uint4(0, 0, 0, 0);
+                        top = max(max(top, v.x & 0x7fff7fffu), max(v.y & 0x7fff7fffu, max(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                        top = max(top, max(max((v.x << 16) & 0x7fffffffu, (v.y << 16) & 0x7fffffffu),
+                                           max((v.z << 16) & 0x7fffffffu, (v.w << 16) & 0x7fffffffu)));
+                    }
+                    int e = (int)(top >> 23);  // zeros and infinities keep the scale 1
+                    e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
+                    const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                    sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+#pragma unroll 8
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = valid ? src[i] : make_uint4(0, 0, 0, 0);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+                            const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
+                            const __half2 c = __floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
+                                                                __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f);
+                            h[j] = as_u32(c);
+                        }
+                        *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sh.q_full + x);
+                const int min_lim = -warp_max_s32(valid ? -lim : -0x7fffffff), max_lim = warp_max_s32(valid ? lim : -1);
+
+                float m = -1e30f, l = 0.f;
+                uint32_t nan = 0;  // by group: the row sees a value that is NaN
+                auto see_nan = [&](int k) {  // of tile k of the piece
+                    const int info = (tiles + k) % kPfInfo, key0 = (w.lo + w.tile + k) * kPfKeys;
+                    if (!*(volatile uint32_t*)&sh.nan_any[info]) return;
+                    for (int i = 0; i < NG * 4; ++i)
+                        for (uint32_t b = sh.nan_keys[info][i >> 2][i & 3]; b; b &= b - 1) {
+                            const int key = key0 + (i & 3) * 32 + __ffs(b) - 1;
+                            if (key <= lim && key >= lim - back_keys) nan |= 1u << (i >> 2);
+                        }
+                };
+                for (int k = 0; k < cnt && !dead; ++k) {
+                    const int key0 = (w.lo + w.tile + k) * kPfKeys;
+                    if (!mbar_wait(sh.s_full + x, s_count++ & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (k) see_nan(k - 1);  // its values have been taken apart: its product is done
+                    const uint32_t gone = sh.gone[(tiles + k) % kPfInfo];
+                    const bool masked = gone || key0 + kPfKeys - 1 > min_lim || key0 < max_lim - back_keys;
+                    auto hide = [&](int c, float (&v)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int key = key0 + c * 32 + i;
+                            if (key > lim || key < lim - back_keys || ((gone >> (c * 2 + (i >> 4))) & 1u)) v[i] = -INFINITY;
+                        }
+                    };
+                    // The row's maximum first, from tensor memory, then its exponentials from a
+                    // second reading: a whole row does not fit the registers of 14 warps.
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < kPfKeys / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(tl + x * 128 + c * 32, v);
+                        if (masked) hide(c, v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(v[i], v[i + 1]));
+                    }
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if (__any_sync(~0u, fmaf(mx, sc, -m) > kLazy)) {  // rare: raise the maximum and bring the sums to it
+                        const float nm = fmaxf(m, mx * sc), f = ex2(m - nm);
+                        m = nm;
+                        l *= f;
+                        if (k) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float v[32];
+                                uint32_t u[32];
+                                tmem_ld32(tl + 256 + x * 128 + c * 32, v);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * f);
+                                tmem_st32(tl + 256 + x * 128 + c * 32, u);
+                                tmem_st_wait();
+                            }
+                        }
+                    }
+                    const float mo = kPfUp - m;
+                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kPfKeys / 32; ++c) {
+                        float v[32];
+                        uint32_t p[16];
+                        tmem_ld32(tl + x * 128 + c * 32, v);
+                        if (masked) hide(c, v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float e0 = ex2(fmaf(v[i], sc, mo)), e1 = ex2(fmaf(v[i + 1], sc, mo));
+                            l4[(i >> 1) & 3] += e0 + e1;
+                            p[i >> 1] = as_u32(__floats2half2_rn(e0, e1));
+                        }
+                        tmem_st16(tl + x * 128 + c * 16, p);  // over scores that have been read
+                    }
+                    tmem_st_wait();
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sh.p_full + x);
+                }
+                if (!dead && !mbar_wait(sh.o_full + x, o_count++ & 1)) dead = true;
+                if (!dead) {
+                    tc_fence_after();
+                    see_nan(cnt - 1);
+                    const float inv = l != 0.f ? 1.f / l : 0.f;
+                    const size_t at = (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * a.rows + r;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(tl + 256 + x * 128 + c * 32, v);
+                        if ((nan >> (c >> 1)) & 1u) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7fc00000u);
+                        }
+                        if (!valid) continue;
+                        if (whole) {
+                            uint16_t* dst = a.out + q_row * a.o_st + q_head * a.o_sh + c * 32;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t u[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int from = 8 * j + (i & 1) * 4 + (i >> 1);  // channels 2i and 2i + 1 of eight
+                                    u[i] = (uint32_t)f32_to_bf16_bits(v[from] * inv) | ((uint32_t)f32_to_bf16_bits(v[from + 2] * inv) << 16);
+                                }
+                                *reinterpret_cast<uint4*>(dst + j * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                        } else {
+                            float* dst = a.part_o + at * D + c * 32;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    *reinterpret_cast<float4*>(dst + j * 8 + i * 4) =
+                                        make_float4(v[8 * j + i], v[8 * j + 2 + i], v[8 * j + 4 + i], v[8 * j + 6 + i]);
+                        }
+                    }
+                    if (valid && !whole) a.part_ml[at] = make_float2(m, l);
+                    tc_fence_before();
+                }
+            }
+            tiles += cnt;
+            if (!whole) join_pieces<8, 1>(a, w, warp, cum[a.n_seqs], &sh.join_last, add_pieces_apart<D>);
+            next_piece();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+int launch_prefill(KvAttnArgs& a, int sms, cudaStream_t s) {
+    const int st = hs_host::set_smem_attr((const void*)kv4_prefill_kernel<D>, kPfMaxSmem);
+    if (st != HS_OK) return st;
+    a.rows = kPfRows;
+    a.tq = kPfRows / a.group;
+    a.tile_log2 = 7;
+    a.min_units = 1;
+    a.pad = 2;
+    static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
+    if (hs_host::launch_pdl(kv4_prefill_kernel<D>, dim3(std::min(152, sms)), dim3(kPfThreads), PrefillCfg<D>::smem(a.n_seqs), s, a) !=
+        cudaSuccess)
+        return HS_ERR_CUDA;
+    return hs_host::launch_err();
+}
+
+}  // namespace hs
+
+bool hs_kv4_prefill_fits(int dim, int n_seqs) {
+    return (dim == 64 ? hs::PrefillCfg<64>::smem(n_seqs) : hs::PrefillCfg<128>::smem(n_seqs)) <= hs::kPfMaxSmem;
+}
+
+int hs_kv4_prefill(hs::KvAttnArgs a, int dim, int sms, cudaStream_t s) {
+    return dim == 64 ? hs::launch_prefill<64>(a, sms, s) : hs::launch_prefill<128>(a, sms, s);
+}
+
+unsigned hs_kv4_prefill_take_status() {
+    unsigned v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, hs::g_status, sizeof(v)) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(hs::g_status, &zero, sizeof(zero));
+    return v;
+}

@@ -3,7 +3,7 @@
 //
 // An item is (request, kv head, row tile): the row tile holds TQ of the
 // request's new tokens for all G query heads of the kv head.  Its work is the
-// run of 64-key tiles that some row of it sees.  All items' tiles, in the
+// run of key tiles (64 or 128 keys) that some row of it sees.  All items' tiles, in the
 // order (request, kv head, row tile, key tile), form one line that is cut into
 // equal pieces, one a CTA: long and short requests, prompts and single tokens
 // load the SMs alike, and the host needs none of the lengths.  The pieces of an
@@ -14,8 +14,9 @@
 
 namespace hs {
 
+constexpr float kLazy = 8.f;     // a row's maximum may lag by a factor 2^8 before the sums are rescaled
 constexpr int kKvMaxCtas = 456;  // three on each of 152 SMs
-constexpr int kKvTile = 64;  // keys of a tile; pages of 16 to 64 tokens divide it
+constexpr int kKvWsRows = 2 * 152 * 256;  // rows of partial sums of the widest launch
 
 struct KvAttnArgs {
     KvGeom g;
@@ -26,7 +27,7 @@ struct KvAttnArgs {
     const int* q_start;
     const int* seq_len;
     const int* table;
-    int width, n_seqs, n_tokens, group, window, rows, tq, min_units, pad;
+    int width, n_seqs, n_tokens, group, window, rows, tq, min_units, pad, tile_log2;
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [2 * CTAs][rows][dim] partial sums
     float2* part_ml;     // [2 * CTAs][rows] (maximum, sum)
@@ -34,7 +35,7 @@ struct KvAttnArgs {
 };
 
 struct KvSpan {
-    int lo, hi;  // first and last 64-key tile of an item (hi < lo: no key, counted as one tile)
+    int lo, hi;  // first and last key tile of an item (hi < lo: no key, counted as one tile)
 };
 
 // Key tiles of row tile r of a request with n new tokens and length len.
@@ -46,7 +47,7 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int n, int len, i
     if (last < 0 || first > last) {
         s.lo = 0, s.hi = -1;
     } else {
-        s.lo = first / kKvTile, s.hi = last / kKvTile;
+        s.lo = first >> a.tile_log2, s.hi = last >> a.tile_log2;
     }
     return s;
 }
@@ -238,3 +239,9 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
 }
 
 }  // namespace hs
+
+// The tensor-core kernel for chunks (hs_kv4_prefill.cu).
+bool hs_kv4_prefill_fits(int dim, int n_seqs);
+int hs_kv4_prefill(hs::KvAttnArgs a, int dim, int sms, cudaStream_t stream);
+// Reads and clears its device error word.
+unsigned hs_kv4_prefill_take_status();

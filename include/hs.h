@@ -408,8 +408,8 @@ int hs_kv4_plan(const int* cached_len_dev, const int* new_len_dev, int n_seqs, i
  * group of 64 channels: scale = fp16((max - min) / 15), bias = fp16(min),
  * code = clamp(rint((x - bias) / scale), 0, 15) (0 where scale = 0), each step
  * in fp32, round to nearest even, as hs_requant_down_rowscale.  A group that
- * holds an infinity or a NaN, or whose scale or bias passes the fp16 range,
- * reads back as NaN.  A slot outside the pool (such as -1) is skipped.  Two
+ * holds a NaN or a value of 65536 or more (past the fp16 range) reads back as
+ * NaN.  A slot outside the pool (such as -1) is skipped.  Two
  * tokens with the same slot leave one of the two in it, group by group.
  *   k_bf16_dev, v_bf16_dev  bf16, token t and head h at t * stride_token +
  *     h * stride_head elements (K and V each their own strides), channels

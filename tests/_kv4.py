@@ -14,7 +14,7 @@ def quantise(x):
         bias = lo.astype(np.float16)
         s, b = scale.astype(np.float32), bias.astype(np.float32)
         codes = np.where(s > 0, np.clip(np.rint((g - b) / s), 0, 15), 0)
-    bad = ~(np.isfinite(s) & np.isfinite(b))
+    bad = ~((np.abs(lo) < 65536) & (np.abs(hi) < 65536))
     scale = np.where(bad, np.float16(0), scale)
     bias = np.where(bad, np.float16("nan"), bias)
     codes = np.where(bad, 0, codes)

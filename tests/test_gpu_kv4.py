@@ -219,6 +219,8 @@ SHAPES = [  # cached, new, hq, hkv, dim, page
     ([130, 0, 64], [257, 129, 64], 16, 1, 128, 32),
     ([10], [20], 64, 1, 64, 64),
     ([0], [513], 4, 4, 128, 64),
+    ([5000, 2500], [20, 9], 16, 1, 128, 64),
+    ([4000], [70], 6, 2, 64, 16),
 ]
 
 
@@ -285,6 +287,22 @@ def test_attention_sizes_of_values(k_size, v_size, q_size, new):
     assert (np.abs(got - ref) <= bound).all()
 
 
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("spike", [0, 1, 77])
+def test_attention_query_with_one_large_channel(new, spike):
+    """The queries' common power of two follows their largest channel wherever it stands."""
+    r = _kv4.Requests(6, [200], [new], 8, 2, 128, 64)
+    q = r.q.float() * 0.01
+    q[:, :, spike] = 300.0
+    q[:, :, (spike + 2) % 128] = -0.03
+    r.q = q.bfloat16()
+    scale = 0.003  # scores of a few units
+    # in chunks the keys' fp16 rounding (2^-11) times 300 * 4 * scale moves a probability by 0.002
+    bound = 2.0 ** -8 + 6 * (2 * 2.0 ** -11 + 300 * 4 * scale * 2.0 ** -11)
+    ref = r.expected(scale)
+    assert (np.abs(r.run(hs, scale).float().cpu().double().numpy() - ref) <= bound * np.maximum(1, np.abs(ref))).all()
+
+
 def test_attention_strides_streams_and_reuse_of_the_workspace():
     r = _kv4.Requests(21, [700, 90], [2, 2], 16, 4, 128, 64)
     ref = r.expected(0.09)
@@ -297,7 +315,7 @@ def test_attention_strides_streams_and_reuse_of_the_workspace():
     r.run(hs, 0.09, q=wide_q[:, 2:18, :128], out=out, stream=s)
     _close(out, ref, 0.09)
     assert (wide_o[:, 16] == 7).all() and (wide_o[:, :, 128:] == 7).all()
-    ws = torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
     a = r.run(hs, 0.09, ws=ws)
     big = _kv4.Requests(22, [3000], [1], 32, 2, 128, 64)
     b0 = big.run(hs, 0.09, ws=ws)
