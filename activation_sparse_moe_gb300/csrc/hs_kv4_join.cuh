@@ -28,20 +28,20 @@ template <> struct FloatVec<4> { using T = float4; };
 
 // Adds pieces first, first + step, ... (count of them, at most 64) of the item
 // that began in CTA c: into out if `final`, else into piece `first`.  Called by
-// whole warps, `warp` of WARPS; a warp takes four rows of BATCH pieces at a
+// whole warps, `warp` of WARPS; a warp takes ROWS rows of BATCH pieces at a
 // time (it is latency that bounds this).
-template <int D, int WARPS, int BATCH = 4>
+template <int D, int WARPS, int ROWS = 4, int BATCH = 4>
 __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
                                         bool final) {
     constexpr int V = D / 32;
     using Vec = typename FloatVec<V>::T;
     const int lane = threadIdx.x & 31;
     const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
-    for (int r0 = warp; r0 < rows; r0 += 4 * WARPS) {
-        float wt[4][2], m[4], l[4], acc[4][V];
-        int row[4];
+    for (int r0 = warp; r0 < rows; r0 += ROWS * WARPS) {
+        float wt[ROWS][2], m[ROWS], l[ROWS], acc[ROWS][V];
+        int row[ROWS];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < ROWS; ++x) {
             row[x] = min(r0 + x * WARPS, rows - 1);
             float2 ml[2];
 #pragma unroll
@@ -53,7 +53,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
             l[x] = ml[0].y, acc[x][0] = ml[1].y;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < ROWS; ++x) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
             wt[x][0] = ex2(wt[x][0] - m[x]);
@@ -65,17 +65,17 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
             for (int e = 0; e < V; ++e) acc[x][e] = 0.f;
         }
         for (int i0 = 0; i0 < count; i0 += BATCH) {
-            Vec v[BATCH][4];
+            Vec v[BATCH][ROWS];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
                 const size_t at = piece_slot(c, first + min(i0 + i, count - 1) * step) * a.rows;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
+                for (int x = 0; x < ROWS; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
             }
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
+                for (int x = 0; x < ROWS; ++x) {
                     float f = __shfl_sync(~0u, i0 < 32 ? wt[x][0] : wt[x][1], (i0 + i) & 31);
                     if (i0 + i >= count) f = 0.f;
 #pragma unroll
@@ -83,7 +83,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
                 }
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < ROWS; ++x) {
             if (r0 + x * WARPS >= rows) continue;
             if (final) {
                 const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;

@@ -65,6 +65,27 @@ __device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t smem_addr, uint3
 __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
 
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
+    return r;
+}
+// (x & mask) | bits, one instruction (the constants in registers).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
+
 // Eight codes of a word as scale * code + bias in fp16: 1024 + c is exact in
 // fp16, so is c after the subtraction, and the product is rounded once.
 __device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
@@ -72,7 +93,7 @@ __device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        r[i] = as_u32(__hfma2(__hsub2(as_h2(((w >> (4 * i)) & 0x000f000fu) | 0x64006400u), k), s, b));
+        r[i] = as_u32(__hfma2(__hsub2(as_h2(and_or(w >> (4 * i), 0x000f000fu, 0x64006400u)), k), s, b));
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
@@ -80,7 +101,7 @@ __device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
 template <int D>
 __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
                                               bool final) {
-    add_pieces<D, 8, 2>(a, w, warp, c, first, step, count, final);
+    add_pieces<D, 8, 8, 2>(a, w, warp, c, first, step, count, final);
 }
 
 template <int D>
@@ -129,11 +150,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         w = n;
         __syncwarp();
     };
-    // 128 registers a thread at launch: 168 for the softmax, 88 for the others (2 * 168 + 2 * 88 = 4 * 128).
+    // 128 registers a thread at launch: 176 for the softmax, 80 for the others (2 * 176 + 2 * 80 = 4 * 128).
     auto rows_of = [&](const KvWalk& v) { return min(a.tq, v.n - v.r * a.tq) * a.group; };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 12) {
         // ---- packed codes and pairs: K then V of each tile, two copies a page
         const int per_tile = kPfKeys >> a.g.page_log2, codes = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
@@ -234,7 +255,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         __syncwarp();
     }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         // ---- codes taken apart into swizzled fp16 tiles
         const int idx = tid - 256;
         uint32_t f = 0, tiles = 0;
@@ -258,25 +279,34 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-#pragma unroll 2
-                    for (int i = 0; i < 2 * NG; ++i) {  // 32 channels of a key each
-                        const int id = i * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
-                        const uint4 q = *reinterpret_cast<const uint4*>(from + id * 16);
-                        uint32_t sb = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
-                        const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
-                        // A NaN value must not meet the zero probability of a row that does not see it.
-                        const bool nan = v && (sb & 0x7c000000u) == 0x7c000000u;
-                        if (there && nan) {
-                            atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
-                            sh.nan_any[info] = 1;
-                        }
-                        if (!there || nan) sb = 0;
-                        const __half2 p = as_h2(sb), s = __low2half2(p), b = __high2half2(p);
-                        uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
-                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll 1
+                    for (int half = 0; half < NG; ++half) {
+                        uint4 q[2];  // 32 channels of a key each
+                        uint32_t sb[2];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
+                        for (int i = 0; i < 2; ++i) {
+                            const int id = (half * 2 + i) * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
+                            q[i] = *reinterpret_cast<const uint4*>(from + id * 16);
+                            sb[i] = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int id = (half * 2 + i) * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
+                            const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
+                            // A NaN value must not meet the zero probability of a row that does not see it.
+                            const bool nan = v && (sb[i] & 0x7c000000u) == 0x7c000000u;
+                            if (there && nan) {
+                                atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
+                                sh.nan_any[info] = 1;
+                            }
+                            if (!there || nan) sb[i] = 0;
+                            const __half2 p = as_h2(sb[i]), s = __low2half2(p), b = __high2half2(p);
+                            uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
+                            const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -288,7 +318,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // ---- a row tile's queries, softmax and output, a thread a row
         const int x = warp >> 2, row = tid & 127, r = x * 128 + row;
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
@@ -301,38 +331,52 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
                 const int tok = w.r * a.tq + r / a.group, lim = ctx + tok;
-                const long long q_row = w.row0 + tok, q_head = w.head * a.group + r % a.group;
-                float sc;
+                float sc = 0.f;
                 {
-                    // The row in fp16, scaled by the power of two that brings its largest
-                    // channel to [2^8, 2^9): bf16 values down to 2^-22 of it stay exact.
-                    uint32_t top = 0;
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q + q_row * a.q_st + q_head * a.q_sh);
-#pragma unroll 8
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = valid ? src[i] : make_uint4(0, 0, 0, 0);
-                        top = max(max(top, v.x & 0x7fff7fffu), max(v.y & 0x7fff7fffu, max(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                        top = max(top, max(max((v.x << 16) & 0x7fffffffu, (v.y << 16) & 0x7fffffffu),
-                                           max((v.z << 16) & 0x7fffffffu, (v.w << 16) & 0x7fffffffu)));
-                    }
-                    int e = (int)(top >> 23);  // zeros and infinities keep the scale 1
-                    e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
-                    const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-                    sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-#pragma unroll 8
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = valid ? src[i] : make_uint4(0, 0, 0, 0);
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t h[4];
+                    // The warp's 32 rows in fp16, a row by D / 8 lanes.  Each is scaled by the power
+                    // of two that brings its largest channel to [2^8, 2^9): bf16 values down to
+                    // 2^-22 of it stay exact.
+                    constexpr int kL = D / 8, kAt = 32 / kL;  // lanes a row, rows at a time
+                    const int sub = lane / kL, c = lane % kL;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // channels j and j + 4
-                            const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
-                            const __half2 c = __floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
-                                                                __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f);
-                            h[j] = as_u32(c);
+                    for (int i0 = 0; i0 < 32 / kAt; i0 += 8) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int qr = x * 128 + (warp & 3) * 32 + (i0 + i) * kAt + sub, qt = qr / a.group;
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            if (qr < nrows)
+                                v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(w.row0 + w.r * a.tq + qt) * a.q_st +
+                                                                       (long long)(w.head * a.group + qr - qt * a.group) * a.q_sh + c * 8);
                         }
-                        *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (i >> 3) * (128 * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int qr = (warp & 3) * 32 + (i0 + i) * kAt + sub;
+                            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
+#pragma unroll
+                            for (int o = 1; o < kL; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+                            int e = (int)(top >> 23);  // zeros and infinities keep the scale 1
+                            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
+                            const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+#pragma unroll
+                            for (int o = 0; o < kAt; ++o) {
+                                const int eo = __shfl_sync(~0u, e, o * kL);
+                                if (lane == (i0 + i) * kAt + o) sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + eo) << 23);
+                            }
+                            uint32_t h[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+                                const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
+                                const __half2 z = __floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
+                                                                    __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f);
+                                h[j] = as_u32(z);
+                            }
+                            *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) =
+                                make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -361,24 +405,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     if (k) see_nan(k - 1);  // its values have been taken apart: its product is done
                     const uint32_t gone = sh.gone[(tiles + k) % kPfInfo];
                     const bool masked = gone || key0 + kPfKeys - 1 > min_lim || key0 < max_lim - back_keys;
-                    auto hide = [&](int c, float (&v)[32]) {
+                    float v[kPfKeys];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int key = key0 + c * 32 + i;
-                            if (key > lim || key < lim - back_keys || ((gone >> (c * 2 + (i >> 4))) & 1u)) v[i] = -INFINITY;
+                    for (int c = 0; c < kPfKeys / 32; ++c) tmem_ld32_async(tl + x * 128 + c * 32, v + c * 32);
+                    tmem_ld_wait(v);
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < kPfKeys; ++i) {
+                            const int key = key0 + i;
+                            if (key > lim || key < lim - back_keys || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
                         }
-                    };
-                    // The row's maximum first, from tensor memory, then its exponentials from a
-                    // second reading: a whole row does not fit the registers of 14 warps.
+                    }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < kPfKeys / 32; ++c) {
-                        float v[32];
-                        tmem_ld32(tl + x * 128 + c * 32, v);
-                        if (masked) hide(c, v);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(v[i], v[i + 1]));
-                    }
+                    for (int i = 0; i < kPfKeys; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(v[i], v[i + 1]));
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (__any_sync(~0u, fmaf(mx, sc, -m) > kLazy)) {  // rare: raise the maximum and bring the sums to it
                         const float nm = fmaxf(m, mx * sc), f = ex2(m - nm);
@@ -386,35 +426,34 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         l *= f;
                         if (k) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float v[32];
-                                uint32_t u[32];
-                                tmem_ld32(tl + 256 + x * 128 + c * 32, v);
+                            for (int c = 0; c < D / 16; ++c) {
+                                float o[16];
+                                uint32_t u[16];
+                                tmem_ld16(tl + 256 + x * 128 + c * 16, o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * f);
-                                tmem_st32(tl + 256 + x * 128 + c * 32, u);
+                                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * f);
+                                tmem_st16(tl + 256 + x * 128 + c * 16, u);
                                 tmem_st_wait();
                             }
                         }
                     }
-                    const float mo = kPfUp - m;
-                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 sc2 = make_float2(sc, sc), mo2 = make_float2(kPfUp - m, kPfUp - m);
+                    float2 l2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < kPfKeys / 32; ++c) {
-                        float v[32];
+                    for (int h = 0; h < kPfKeys / 32; ++h) {
                         uint32_t p[16];
-                        tmem_ld32(tl + x * 128 + c * 32, v);
-                        if (masked) hide(c, v);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float e0 = ex2(fmaf(v[i], sc, mo)), e1 = ex2(fmaf(v[i + 1], sc, mo));
-                            l4[(i >> 1) & 3] += e0 + e1;
-                            p[i >> 1] = as_u32(__floats2half2_rn(e0, e1));
+                        for (int i = 0; i < 16; ++i) {
+                            float2 e = fma2(make_float2(v[h * 32 + 2 * i], v[h * 32 + 2 * i + 1]), sc2, mo2);
+                            e.x = ex2(e.x), e.y = ex2(e.y);
+                            l2[i & 3] = add2(l2[i & 3], e);
+                            p[i] = as_u32(__floats2half2_rn(e.x, e.y));
                         }
-                        tmem_st16(tl + x * 128 + c * 16, p);  // over scores that have been read
+                        tmem_st16(tl + x * 128 + h * 16, p);  // over the scores
                     }
                     tmem_st_wait();
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    l2[0] = add2(add2(l2[0], l2[1]), add2(l2[2], l2[3]));
+                    l += l2[0].x + l2[0].y;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.p_full + x);
@@ -433,9 +472,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7fc00000u);
                         }
-                        if (!valid) continue;
-                        if (whole) {
-                            uint16_t* dst = a.out + q_row * a.o_st + q_head * a.o_sh + c * 32;
+                        if (whole) {  // by way of the queries' place, which is free
+                            uint8_t* line = q_s + x * C::kQBytes + row * (2 * D);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t u[4];
@@ -444,9 +482,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                                     const int from = 8 * j + (i & 1) * 4 + (i >> 1);  // channels 2i and 2i + 1 of eight
                                     u[i] = (uint32_t)f32_to_bf16_bits(v[from] * inv) | ((uint32_t)f32_to_bf16_bits(v[from + 2] * inv) << 16);
                                 }
-                                *reinterpret_cast<uint4*>(dst + j * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                                *reinterpret_cast<uint4*>(line + (((c * 4 + j) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                             }
-                        } else {
+                        } else if (valid) {
                             float* dst = a.part_o + at * D + c * 32;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -456,7 +494,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                                         make_float4(v[8 * j + i], v[8 * j + 2 + i], v[8 * j + 4 + i], v[8 * j + 6 + i]);
                         }
                     }
-                    if (valid && !whole) a.part_ml[at] = make_float2(m, l);
+                    if (whole) {
+                        constexpr int kL = D / 8, kAt = 32 / kL;
+                        const int sub = lane / kL, c = lane % kL;
+                        __syncwarp();
+#pragma unroll 4
+                        for (int i = 0; i < 32 / kAt; ++i) {
+                            const int orow = (warp & 3) * 32 + i * kAt + sub, qr = x * 128 + orow, qt = qr / a.group;
+                            const uint4 u = *reinterpret_cast<const uint4*>(q_s + x * C::kQBytes + orow * (2 * D) + ((c ^ (orow & 7)) << 4));
+                            if (qr < nrows)
+                                *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + qt) * a.o_st +
+                                                          (long long)(w.head * a.group + qr - qt * a.group) * a.o_sh + c * 8) = u;
+                        }
+                        __syncwarp();
+                    } else if (valid) {
+                        a.part_ml[at] = make_float2(m, l);
+                    }
                     tc_fence_before();
                 }
             }
