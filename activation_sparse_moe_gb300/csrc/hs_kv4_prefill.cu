@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     long long* cum = reinterpret_cast<long long*>(packed_s + kPfPacked * C::kPackedBytes + 1024);
     int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
     int* ls = qs + a.n_seqs + 1;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (Reductions of values that all lanes share: they come out in uniform registers,
+    // which the tensor-core instructions' operands have to be in.)
+    const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_max_u32(threadIdx.x >> 5);
 
     if (tid == 0) {
         for (int i = 0; i < kPfPacked; ++i) mbar_init(sh.packed_full + i, 1), mbar_init(sh.packed_empty + i, 4);
@@ -137,7 +139,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     tc_fence_before();
     kv_schedule(a, qs, ls, cum);
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
+    const uint32_t tmem = warp_max_u32(sh.tmem);  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
     // A warp's place in the line, in shared memory: looked at once an item.
     __shared__ KvWalk walks[kPfThreads / 32];
     KvWalk& w = walks[warp];
@@ -150,11 +152,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         w = n;
         __syncwarp();
     };
-    // 128 registers a thread at launch: 176 for the softmax, 80 for the others (2 * 176 + 2 * 80 = 4 * 128).
+    // 128 registers a thread at launch: 184 for the softmax, 72 for the others (2 * 184 + 2 * 72 = 4 * 128).
     auto rows_of = [&](const KvWalk& v) { return min(a.tq, v.n - v.r * a.tq) * a.group; };
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {
         // ---- packed codes and pairs: K then V of each tile, two copies a page
         const int per_tile = kPfKeys >> a.g.page_log2, codes = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
@@ -199,63 +201,69 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             }
         }
     } else if (warp == 13) {
-        // ---- matrix products, issued by lane 0
-        {
-            constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kPfKeys);
-            constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | (1u << 16);  // V: rows along K
-            uint32_t f = 0, p_count[2] = {0, 0}, q_count[2] = {0, 0};
-            bool dead = false;
-            auto values = [&](int x, uint32_t fv, bool first) {  // O += P V of row tile x
-                const uint32_t at = smem_u32(kv_s + (fv % kPfSlots) * C::kTileBytes);
+        // ---- matrix products, issued by one lane
+        constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kPfKeys);
+        constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | (1u << 16);  // V: rows along K
+        const uint32_t q_at = smem_u32(q_s), kv_at = smem_u32(kv_s);
+        uint32_t slot = 0, phase = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};  // slot: of the next K tile
+        bool dead = false;
+        auto wait = [&](uint64_t* bar, uint32_t parity) { dead |= !__all_sync(~0u, mbar_wait(bar, parity)); };
+        while (w.left > 0 && !dead) {
+            const int cnt = (int)warp_max_u32((uint32_t)kv_piece_tiles(w));
+            const bool two = warp_max_u32((uint32_t)rows_of(w)) > 128u;
+            uint32_t v_slot = 0, v_phase = 0;  // of the V tile before
+            for (int k = 0; k <= cnt && !dead; ++k) {
+                // tile k's scores and tile k - 1's outputs, a row tile at a time
+                if (k < cnt) wait(sh.kv_full + slot, phase);
+                if (k && !dead) wait(sh.kv_full + v_slot, v_phase);
 #pragma unroll
-                for (int kk = 0; kk < kPfKeys / 16; ++kk)
-                    umma_f16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, umma_desc_sw128_mn(at + kk * 2048, kPfKeys * 128),
-                                    idesc_o, !first || kk);
-            };
-            for (; w.left > 0 && !dead; next_piece()) {
-                const int cnt = kv_piece_tiles(w), nx = rows_of(w) > 128 ? 2 : 1;
-                for (int k = 0; k <= cnt && !dead; ++k) {
-                    // tile k's scores and tile k - 1's outputs, a row tile at a time
-                    const uint32_t fk = f + 2 * k, fv = f + 2 * k - 1;  // fills of K k and V k - 1
-                    if (k < cnt && !mbar_wait(sh.kv_full + fk % kPfSlots, (fk / kPfSlots) & 1)) dead = true;
-                    if (k && !dead && !mbar_wait(sh.kv_full + fv % kPfSlots, (fv / kPfSlots) & 1)) dead = true;
-                    for (int x = 0; x < nx && !dead; ++x) {
-                        if (k) {
-                            if (!mbar_wait(sh.p_full + x, p_count[x]++ & 1)) {
-                                dead = true;
-                                break;
-                            }
-                            tc_fence_after();
-                            if (lane == 0) {
-                                values(x, fv, k == 1);
-                                if (k == cnt) umma_commit(sh.o_full + x);
-                                if (x == nx - 1) umma_commit(sh.kv_empty + fv % kPfSlots);
-                            }
-                        } else if (!mbar_wait(sh.q_full + x, q_count[x]++ & 1)) {
-                            dead = true;
-                            break;
+                for (int x = 0; x < 2; ++x) {
+                    if ((x && !two) || dead) continue;
+                    if (k) {
+                        wait(sh.p_full + x, p_phase[x]);
+                        p_phase[x] ^= 1;
+                    } else {
+                        wait(sh.q_full + x, q_phase[x]);
+                        q_phase[x] ^= 1;
+                    }
+                    if (dead) continue;
+                    tc_fence_after();
+                    const bool last = x || !two;
+                    if (elect_one()) {
+                        if (k) {  // O += P V
+                            const uint64_t vd = umma_desc_sw128_mn(kv_at + v_slot * C::kTileBytes, kPfKeys * 128);
+#pragma unroll
+                            for (int kk = 0; kk < kPfKeys / 16; ++kk)
+                                umma_f16_tmem_a(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + kk * (2048 >> 4), idesc_o, kk ? 1 : k > 1);
+                            if (k == cnt) umma_commit(sh.o_full + x);
+                            if (last) umma_commit(sh.kv_empty + v_slot);
                         }
-                        if (k < cnt && lane == 0) {
-                            tc_fence_after();
-                            const uint32_t qa = smem_u32(q_s + x * C::kQBytes), ka = smem_u32(kv_s + (fk % kPfSlots) * C::kTileBytes);
+                        if (k < cnt) {  // S = Q K^T
+                            const uint64_t qd = umma_desc_sw128(q_at + x * C::kQBytes), kd = umma_desc_sw128(kv_at + slot * C::kTileBytes);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t at = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                                umma_f16(tmem + x * 128, umma_desc_sw128(qa + at), umma_desc_sw128(ka + at), idesc_s, kk != 0);
+                                const uint32_t at = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                                umma_f16(tmem + x * 128, qd + at, kd + at, idesc_s, kk != 0);
                             }
                             umma_commit(sh.s_full + x);
+                            if (last) umma_commit(sh.kv_empty + slot);
                         }
                     }
-                    if (k < cnt && !dead && lane == 0) umma_commit(sh.kv_empty + fk % kPfSlots);
                     __syncwarp();
                 }
-                f += 2 * cnt;
+                if (k < cnt) {  // K k, V k, K k + 1 follow one another round the ring
+                    v_slot = slot + 1 == kPfSlots ? 0 : slot + 1;
+                    v_phase = slot + 1 == kPfSlots ? phase ^ 1 : phase;
+                    const uint32_t next = v_slot + 1 == kPfSlots ? 0 : v_slot + 1;
+                    phase = v_slot + 1 == kPfSlots ? v_phase ^ 1 : v_phase;
+                    slot = next;
+                }
             }
+            next_piece();
         }
-        __syncwarp();
     }
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- codes taken apart into swizzled fp16 tiles
         const int idx = tid - 256;
         uint32_t f = 0, tiles = 0;
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---- a row tile's queries, softmax and output, a thread a row
         const int x = warp >> 2, row = tid & 127, r = x * 128 + row;
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
