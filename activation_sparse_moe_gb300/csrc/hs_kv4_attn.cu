@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         // the warp's rows see no key past max_lim or before min_lim - back_keys, and all
         // of those from max_lim - back_keys to min_lim
         const int row0 = rt * 8 * NQ, back_keys = a.window ? a.window - 1 : 0x3fffffff;
-        const int tok0 = w.r * a.tq + row0 / a.group;
-        const int tok1 = min(w.r * a.tq + min(row0 + 8 * NQ - 1, a.tq * a.group - 1) / a.group, w.n - 1);
+        const int tok0 = w.r * a.tq + kv_row_token(a, row0);
+        const int tok1 = min(w.r * a.tq + kv_row_token(a, min(row0 + 8 * NQ - 1, a.tq * a.group - 1)), w.n - 1);
         const bool some = row0 < a.tq * a.group && tok0 < w.n;
         const int min_lim = ctx + tok0, max_lim = some ? ctx + tok1 : -1;
 
@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             uint32_t top = 0;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                const int row = row0 + n * 8 + g, tok = w.r * a.tq + row / a.group;
+                const int row = row0 + n * 8 + g, in_tile = kv_row_token(a, row), tok = w.r * a.tq + in_tile;
                 const bool valid = row < a.tq * a.group && tok < w.n;
-                const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row % a.group) * a.q_sh;
+                const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row - in_tile * a.group) * a.q_sh;
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
                             for (int i = 0; i < NG; ++i) v = fmaf(p[i].x, S[h][i][n][2 * j + e], v);
                             if (MASKED) {
-                                const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + row / a.group;
+                                const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + kv_row_token(a, row);
                                 const int key = key0 + 16 * h + 8 * j + kr;
                                 if (key > lim || key < lim - back_keys || ((none >> h) & 1u)) v = -INFINITY;
                             }
@@ -500,11 +500,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = row0 + n * 8 + 2 * t + e, tok = w.r * a.tq + row / a.group;
+                    const int row = row0 + n * 8 + 2 * t + e, in_tile = kv_row_token(a, row), tok = w.r * a.tq + in_tile;
                     if (row >= a.tq * a.group || tok >= w.n) continue;
                     if (whole) {
                         const float inv = l[n][e] != 0.f ? 1.f / l[n][e] : 0.f;
-                        uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row % a.group) * a.o_sh + g * 8;
+                        uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row - in_tile * a.group) * a.o_sh + g * 8;
 #pragma unroll
                         for (int i = 0; i < NG; ++i) {
                             uint32_t u[4];
@@ -616,6 +616,7 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.q_start = q_start, a.seq_len = seq_len, a.table = table;
     a.width = table_width, a.n_seqs = n_seqs, a.n_tokens = n_tokens;
     a.group = n_q_heads / cache->n_kv_heads;
+    a.group_inv = (65536u + (uint32_t)a.group - 1u) / (uint32_t)a.group;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.joined = reinterpret_cast<int*>(w);

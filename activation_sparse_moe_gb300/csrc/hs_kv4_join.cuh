@@ -38,8 +38,33 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
     const int lane = threadIdx.x & 31;
     const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
     for (int r0 = warp; r0 < rows; r0 += ROWS * WARPS) {
-        float wt[ROWS][2], m[ROWS], l[ROWS], acc[ROWS][V];
+        float m[ROWS], l[ROWS], acc[ROWS][V];
         int row[ROWS];
+        if (count <= 2) {  // the commonest case: everything is read at once
+            Vec v[2][ROWS];
+            float2 ml[2][ROWS];
+#pragma unroll
+            for (int x = 0; x < ROWS; ++x) {
+                row[x] = min(r0 + x * WARPS, rows - 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const size_t at = piece_slot(c, first + min(i, count - 1) * step) * a.rows + row[x];
+                    v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + at * D) + lane);
+                    ml[i][x] = __ldcg(a.part_ml + at);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < ROWS; ++x) {
+                if (count == 1) ml[1][x] = make_float2(-1e30f, 0.f);
+                m[x] = fmaxf(ml[0][x].x, ml[1][x].x);
+                const float f0 = ex2(ml[0][x].x - m[x]), f1 = count == 1 ? 0.f : ex2(ml[1][x].x - m[x]);
+                l[x] = f0 * ml[0][x].y + f1 * ml[1][x].y;
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    acc[x][e] = f0 * reinterpret_cast<const float*>(&v[0][x])[e] + f1 * reinterpret_cast<const float*>(&v[1][x])[e];
+            }
+        } else {
+        float wt[ROWS][2];
 #pragma unroll
         for (int x = 0; x < ROWS; ++x) {
             row[x] = min(r0 + x * WARPS, rows - 1);
@@ -82,6 +107,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
                     for (int e = 0; e < V; ++e) acc[x][e] = fmaf(f, reinterpret_cast<const float*>(&v[i][x])[e], acc[x][e]);
                 }
         }
+        }
 #pragma unroll
         for (int x = 0; x < ROWS; ++x) {
             if (r0 + x * WARPS >= rows) continue;
@@ -91,8 +117,9 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
                     u[e] = (uint32_t)f32_to_bf16_bits(acc[x][2 * e] * inv) | ((uint32_t)f32_to_bf16_bits(acc[x][2 * e + 1] * inv) << 16);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (long long)(w.row0 + w.r * a.tq + row[x] / a.group) * a.o_st +
-                                                            (long long)(w.head * a.group + row[x] % a.group) * a.o_sh) + lane * (V / 2);
+                const int tok = kv_row_token(a, row[x]);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
+                                                            (long long)(w.head * a.group + row[x] - tok * a.group) * a.o_sh) + lane * (V / 2);
                 if (V == 4)
                     *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[V / 2 - 1]);
                 else

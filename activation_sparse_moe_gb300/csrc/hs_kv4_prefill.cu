@@ -7,9 +7,9 @@
 // operands, fp32 in tensor memory), its softmax, and O += P V with P read from
 // tensor memory where S stood.  Roles, one CTA an SM:
 //   warps 0-3, 4-7   a row tile each, a thread a row: queries in, softmax, output
-//   warps 8-11       take the codes apart: K and V tiles of 128 keys in fp16
 //   warp 12          copies packed codes and pairs, page by page
 //   warp 13          issues the matrix products
+//   warps 8-11, 14, 15   take the codes apart: K and V tiles of 128 keys in fp16
 // The two row tiles take turns: one's softmax runs under the other's products,
 // and both use a K and V tile that was taken apart once.  Keys and values are
 // scale * code + bias rounded once to fp16; channels stand in both operands in
@@ -25,7 +25,8 @@
 namespace hs {
 
 constexpr int kPfKeys = 128, kPfRows = 256, kPfPacked = 3, kPfSlots = 3, kPfInfo = 8;
-constexpr int kPfThreads = 16 * 32;  // warps 14 and 15 fill the last warpgroup: registers move by warpgroups
+constexpr int kPfThreads = 16 * 32;
+constexpr int kPfApart = 6;  // warps that take codes apart
 constexpr int kPfMaxSmem = 227 * 1024 - 1024;  // dynamic; the rest is the static part
 constexpr float kPfUp = 6.f;  // probabilities are held times 2^6: at most 2^14 in fp16, and small ones keep their bits
 
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_max_u32(threadIdx.x >> 5);
 
     if (tid == 0) {
-        for (int i = 0; i < kPfPacked; ++i) mbar_init(sh.packed_full + i, 1), mbar_init(sh.packed_empty + i, 4);
-        for (int i = 0; i < kPfSlots; ++i) mbar_init(sh.kv_full + i, 4), mbar_init(sh.kv_empty + i, 1);
+        for (int i = 0; i < kPfPacked; ++i) mbar_init(sh.packed_full + i, 1), mbar_init(sh.packed_empty + i, kPfApart);
+        for (int i = 0; i < kPfSlots; ++i) mbar_init(sh.kv_full + i, kPfApart), mbar_init(sh.kv_empty + i, 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
         fence_mbar_init();
@@ -155,8 +156,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     // 128 registers a thread at launch: 184 for the softmax, 72 for the others (2 * 184 + 2 * 72 = 4 * 128).
     auto rows_of = [&](const KvWalk& v) { return min(a.tq, v.n - v.r * a.tq) * a.group; };
 
-    if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {
         // ---- packed codes and pairs: K then V of each tile, two copies a page
         const int per_tile = kPfKeys >> a.g.page_log2, codes = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
@@ -261,11 +262,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             }
             next_piece();
         }
-    }
-    } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else {
         // ---- codes taken apart into swizzled fp16 tiles
-        const int idx = tid - 256;
+        const int idx = (warp < 12 ? warp - 8 : warp - 10) * 32 + lane;  // of 192
         uint32_t f = 0, tiles = 0;
         bool dead = false;
         for (; w.left > 0 && !dead; next_piece()) {
@@ -287,34 +286,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-#pragma unroll 1
-                    for (int half = 0; half < NG; ++half) {
-                        uint4 q[2];  // 32 channels of a key each
-                        uint32_t sb[2];
+                    // 32 channels of a key at a time
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int id = (half * 2 + i) * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
-                            q[i] = *reinterpret_cast<const uint4*>(from + id * 16);
-                            sb[i] = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
+                    for (int id = idx; id < kPfKeys * 2 * NG; id += 32 * kPfApart) {
+                        const int key = id / (2 * NG), c = id % (2 * NG);
+                        const uint4 q = *reinterpret_cast<const uint4*>(from + id * 16);
+                        uint32_t sb = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
+                        const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
+                        // A NaN value must not meet the zero probability of a row that does not see it.
+                        const bool nan = v && (sb & 0x7c000000u) == 0x7c000000u;
+                        if (there && nan) {
+                            atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
+                            sh.nan_any[info] = 1;
                         }
+                        if (!there || nan) sb = 0;
+                        const __half2 p = as_h2(sb), s = __low2half2(p), b = __high2half2(p);
+                        uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
+                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int id = (half * 2 + i) * 128 + idx, key = id / (2 * NG), c = id % (2 * NG);
-                            const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
-                            // A NaN value must not meet the zero probability of a row that does not see it.
-                            const bool nan = v && (sb[i] & 0x7c000000u) == 0x7c000000u;
-                            if (there && nan) {
-                                atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
-                                sh.nan_any[info] = 1;
-                            }
-                            if (!there || nan) sb[i] = 0;
-                            const __half2 p = as_h2(sb[i]), s = __low2half2(p), b = __high2half2(p);
-                            uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
-                            const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
-                        }
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -325,6 +316,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 }
             }
         }
+    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---- a row tile's queries, softmax and output, a thread a row
@@ -338,27 +330,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             const bool whole = cnt == w.tiles;
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
-                const int tok = w.r * a.tq + r / a.group, lim = ctx + tok;
+                const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
                 float sc = 0.f;
                 {
                     // The warp's 32 rows in fp16, a row by D / 8 lanes.  Each is scaled by the power
                     // of two that brings its largest channel to [2^8, 2^9): bf16 values down to
                     // 2^-22 of it stay exact.
-                    constexpr int kL = D / 8, kAt = 32 / kL;  // lanes a row, rows at a time
+                    constexpr int kL = D / 8, kAt = 32 / kL, kB = 32 / kAt;  // lanes a row, rows at a time, all in flight
                     const int sub = lane / kL, c = lane % kL;
 #pragma unroll
-                    for (int i0 = 0; i0 < 32 / kAt; i0 += 8) {
-                        uint4 v[8];
+                    for (int i0 = 0; i0 < 32 / kAt; i0 += kB) {
+                        uint4 v[kB];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int qr = x * 128 + (warp & 3) * 32 + (i0 + i) * kAt + sub, qt = qr / a.group;
+                        for (int i = 0; i < kB; ++i) {
+                            const int qr = x * 128 + (warp & 3) * 32 + (i0 + i) * kAt + sub, qt = kv_row_token(a, qr);
                             v[i] = make_uint4(0, 0, 0, 0);
                             if (qr < nrows)
                                 v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(w.row0 + w.r * a.tq + qt) * a.q_st +
                                                                        (long long)(w.head * a.group + qr - qt * a.group) * a.q_sh + c * 8);
                         }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < kB; ++i) {
                             const int qr = (warp & 3) * 32 + (i0 + i) * kAt + sub;
                             const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                             uint32_t top = 0;
@@ -508,7 +500,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         __syncwarp();
 #pragma unroll 4
                         for (int i = 0; i < 32 / kAt; ++i) {
-                            const int orow = (warp & 3) * 32 + i * kAt + sub, qr = x * 128 + orow, qt = qr / a.group;
+                            const int orow = (warp & 3) * 32 + i * kAt + sub, qr = x * 128 + orow, qt = kv_row_token(a, qr);
                             const uint4 u = *reinterpret_cast<const uint4*>(q_s + x * C::kQBytes + orow * (2 * D) + ((c ^ (orow & 7)) << 4));
                             if (qr < nrows)
                                 *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + qt) * a.o_st +
@@ -539,7 +531,7 @@ int launch_prefill(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tq = kPfRows / a.group;
     a.tile_log2 = 7;
     a.min_units = 1;
-    a.pad = 2;
+    a.pad = 4;
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
     if (hs_host::launch_pdl(kv4_prefill_kernel<D>, dim3(std::min(152, sms)), dim3(kPfThreads), PrefillCfg<D>::smem(a.n_seqs), s, a) !=
         cudaSuccess)

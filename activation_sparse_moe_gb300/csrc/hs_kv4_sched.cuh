@@ -28,11 +28,15 @@ struct KvAttnArgs {
     const int* seq_len;
     const int* table;
     int width, n_seqs, n_tokens, group, window, rows, tq, min_units, pad, tile_log2;
+    uint32_t group_inv;  // ceil(2^16 / group)
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [2 * CTAs][rows][dim] partial sums
     float2* part_ml;     // [2 * CTAs][rows] (maximum, sum)
     int* joined;         // [3 * CTAs] arrivals of pieces, zero between calls
 };
+
+// Token of a row of a row tile: row / group, for the at most 256 rows there are.
+__device__ __forceinline__ int kv_row_token(const KvAttnArgs& a, int row) { return (int)(((uint32_t)row * a.group_inv) >> 16); }
 
 struct KvSpan {
     int lo, hi;  // first and last key tile of an item (hi < lo: no key, counted as one tile)
