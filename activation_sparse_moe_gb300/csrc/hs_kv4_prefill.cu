@@ -286,11 +286,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-                    // 32 channels of a key at a time
+                    // 32 channels of a key at a time; eight lanes that store together hold four
+                    // keys and both halves of a 128-byte line: no two in one bank.
 #pragma unroll
                     for (int id = idx; id < kPfKeys * 2 * NG; id += 32 * kPfApart) {
-                        const int key = id / (2 * NG), c = id % (2 * NG);
-                        const uint4 q = *reinterpret_cast<const uint4*>(from + id * 16);
+                        const int key = NG == 1 ? id >> 1 : (id >> 1 & 3) | (id >> 4) << 2, c = NG == 1 ? id & 1 : (id & 1) | (id >> 2 & 2);
+                        const uint4 q = *reinterpret_cast<const uint4*>(from + key * (D / 2) + c * 16);
                         uint32_t sb = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
                         const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
                         // A NaN value must not meet the zero probability of a row that does not see it.
@@ -331,52 +332,46 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
                 const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
-                float sc = 0.f;
+                float sc;
                 {
-                    // The warp's 32 rows in fp16, a row by D / 8 lanes.  Each is scaled by the power
-                    // of two that brings its largest channel to [2^8, 2^9): bf16 values down to
-                    // 2^-22 of it stay exact.
+                    // The warp's 32 rows in fp16, a row by D / 8 lanes, all scaled by the power of
+                    // two that brings their largest channel to [2^8, 2^9): bf16 values down to
+                    // 2^-22 of it stay exact, smaller ones move a score by less than 2^-33 of the largest.
                     constexpr int kL = D / 8, kAt = 32 / kL, kB = 32 / kAt;  // lanes a row, rows at a time, all in flight
                     const int sub = lane / kL, c = lane % kL;
+                    uint4 v[kB];
+                    uint32_t top = 0;
 #pragma unroll
-                    for (int i0 = 0; i0 < 32 / kAt; i0 += kB) {
-                        uint4 v[kB];
+                    for (int i = 0; i < kB; ++i) {
+                        const int qr = x * 128 + (warp & 3) * 32 + i * kAt + sub, qt = kv_row_token(a, qr);
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (qr < nrows)
+                            v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(w.row0 + w.r * a.tq + qt) * a.q_st +
+                                                                   (long long)(w.head * a.group + qr - qt * a.group) * a.q_sh + c * 8);
+                    }
 #pragma unroll
-                        for (int i = 0; i < kB; ++i) {
-                            const int qr = x * 128 + (warp & 3) * 32 + (i0 + i) * kAt + sub, qt = kv_row_token(a, qr);
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if (qr < nrows)
-                                v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(w.row0 + w.r * a.tq + qt) * a.q_st +
-                                                                       (long long)(w.head * a.group + qr - qt * a.group) * a.q_sh + c * 8);
+                    for (int i = 0; i < kB; ++i) {
+                        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
+                    }
+                    int e = (int)(warp_max_u32(top) >> 23);  // zeros and infinities keep the scale 1
+                    e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
+                    const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+                    sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+#pragma unroll
+                    for (int i = 0; i < kB; ++i) {
+                        const int qr = (warp & 3) * 32 + i * kAt + sub;
+                        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+                            const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
+                            h[j] = as_u32(__floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
+                                                            __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f));
                         }
-#pragma unroll
-                        for (int i = 0; i < kB; ++i) {
-                            const int qr = (warp & 3) * 32 + (i0 + i) * kAt + sub;
-                            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
-#pragma unroll
-                            for (int o = 1; o < kL; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-                            int e = (int)(top >> 23);  // zeros and infinities keep the scale 1
-                            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
-                            const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-#pragma unroll
-                            for (int o = 0; o < kAt; ++o) {
-                                const int eo = __shfl_sync(~0u, e, o * kL);
-                                if (lane == (i0 + i) * kAt + o) sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + eo) << 23);
-                            }
-                            uint32_t h[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {  // channels j and j + 4
-                                const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
-                                const __half2 z = __floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
-                                                                    __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f);
-                                h[j] = as_u32(z);
-                            }
-                            *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) =
-                                make_uint4(h[0], h[1], h[2], h[3]);
-                        }
+                        *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -480,7 +475,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const int from = 8 * j + (i & 1) * 4 + (i >> 1);  // channels 2i and 2i + 1 of eight
-                                    u[i] = (uint32_t)f32_to_bf16_bits(v[from] * inv) | ((uint32_t)f32_to_bf16_bits(v[from + 2] * inv) << 16);
+                                    const __nv_bfloat162 z = __floats2bfloat162_rn(v[from] * inv, v[from + 2] * inv);
+                                    u[i] = *reinterpret_cast<const uint32_t*>(&z);
                                 }
                                 *reinterpret_cast<uint4*>(line + (((c * 4 + j) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
                             }
