@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     // A warp's place in the line, in shared memory: looked at once an item.
     __shared__ KvWalk walks[kPfThreads / 32];
     KvWalk& w = walks[warp];
-    w = kv_begin(a, qs, ls, cum);
-    __syncwarp();
+    if (warp == 0) walks[0] = kv_begin(a, qs, ls, cum);
+    __syncthreads();
+    if (warp) w = walks[0];
+    __syncthreads();
     auto next_piece = [&]() {
         KvWalk n = w;
         kv_next_piece(a, qs, ls, n);
@@ -273,47 +275,70 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 const int key0 = (w.lo + w.tile + k) * kPfKeys, info = tiles % kPfInfo;
                 for (int v = 0; v < 2; ++v, ++f) {
                     const int st = f % kPfPacked, slot = f % kPfSlots;
-                    if (!mbar_wait(sh.packed_full + st, (f / kPfPacked) & 1) ||
-                        (f >= kPfSlots && !mbar_wait(sh.kv_empty + slot, (f / kPfSlots + 1) & 1))) {
+                    if (!mbar_wait(sh.packed_full + st, (f / kPfPacked) & 1)) {
                         dead = true;
                         break;
                     }
+                    // 32 channels of a key at a time, into registers while the tile's place may
+                    // still be in use; eight lanes that store together hold four keys and both
+                    // halves of a 128-byte line: no two in one bank.
+                    constexpr int kItems = kPfKeys * 2 * NG, kMine = (kItems + 32 * kPfApart - 1) / (32 * kPfApart);
                     const uint32_t gone = sh.gone[info];
                     const uint8_t* from = packed_s + st * C::kPackedBytes;
-                    uint8_t* to = kv_s + slot * C::kTileBytes;
+                    uint4 q[kMine];
+                    uint32_t sb[kMine];
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        const int id = idx + i * 32 * kPfApart;
+                        const int key = NG == 1 ? id >> 1 : (id >> 1 & 3) | (id >> 4) << 2, c = NG == 1 ? id & 1 : (id & 1) | (id >> 2 & 2);
+                        if (kItems % (32 * kPfApart) == 0 || id < kItems) {
+                            q[i] = *reinterpret_cast<const uint4*>(from + key * (D / 2) + c * 16);
+                            sb[i] = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
+                            if (key0 + key >= w.len || (gone >> (key >> 4)) & 1u) sb[i] = 0;
+                            nan |= (sb[i] & 0x7c000000u) == 0x7c000000u;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sh.packed_empty + st);
                     if (v == 0 && idx < 9) {  // for four tiles on: no warp here is two ahead of another
                         const int on = (tiles + 4) % kPfInfo;
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-                    // 32 channels of a key at a time; eight lanes that store together hold four
-                    // keys and both halves of a 128-byte line: no two in one bank.
+                    if (v && nan) {  // a NaN value must not meet the zero probability of a row that does not see it
 #pragma unroll
-                    for (int id = idx; id < kPfKeys * 2 * NG; id += 32 * kPfApart) {
-                        const int key = NG == 1 ? id >> 1 : (id >> 1 & 3) | (id >> 4) << 2, c = NG == 1 ? id & 1 : (id & 1) | (id >> 2 & 2);
-                        const uint4 q = *reinterpret_cast<const uint4*>(from + key * (D / 2) + c * 16);
-                        uint32_t sb = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
-                        const bool there = key0 + key < w.len && !((gone >> (key >> 4)) & 1u);
-                        // A NaN value must not meet the zero probability of a row that does not see it.
-                        const bool nan = v && (sb & 0x7c000000u) == 0x7c000000u;
-                        if (there && nan) {
-                            atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
-                            sh.nan_any[info] = 1;
+                        for (int i = 0; i < kMine; ++i) {
+                            const int id = idx + i * 32 * kPfApart;
+                            const int key = NG == 1 ? id >> 1 : (id >> 1 & 3) | (id >> 4) << 2, c = NG == 1 ? id & 1 : (id & 1) | (id >> 2 & 2);
+                            if (id < kItems && (sb[i] & 0x7c000000u) == 0x7c000000u) {
+                                atomicOr(&sh.nan_keys[info][c >> 1][key >> 5], 1u << (key & 31));
+                                sh.nan_any[info] = 1;
+                                sb[i] = 0;
+                            }
                         }
-                        if (!there || nan) sb = 0;
-                        const __half2 p = as_h2(sb), s = __low2half2(p), b = __high2half2(p);
-                        uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
-                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+                    }
+                    if (f >= kPfSlots && !mbar_wait(sh.kv_empty + slot, (f / kPfSlots + 1) & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    uint8_t* to = kv_s + slot * C::kTileBytes;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
+                    for (int i = 0; i < kMine; ++i) {
+                        const int id = idx + i * 32 * kPfApart;
+                        const int key = NG == 1 ? id >> 1 : (id >> 1 & 3) | (id >> 4) << 2, c = NG == 1 ? id & 1 : (id & 1) | (id >> 2 & 2);
+                        if (kItems % (32 * kPfApart) == 0 || id < kItems) {
+                            const __half2 p = as_h2(sb[i]), s = __low2half2(p), b = __high2half2(p);
+                            uint8_t* line = to + (c >> 1) * (kPfKeys * 128) + key * 128;
+                            const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                *reinterpret_cast<uint4*>(line + ((((c & 1) * 4 + x) ^ (key & 7)) << 4)) = take_apart(words[x], s, b);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(sh.packed_empty + st);
-                        mbar_arrive(sh.kv_full + slot);
-                    }
+                    if (lane == 0) mbar_arrive(sh.kv_full + slot);
                 }
             }
         }
