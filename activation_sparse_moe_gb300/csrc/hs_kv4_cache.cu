@@ -160,123 +160,193 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
     }
 }
 
-// ---------------------------------------------------------------- append
-struct AppendArgs {
+// ------------------------------------------------------- append and read
+// A unit is a group of 64 channels of one (token, K or V, kv head); eight lanes
+// take one, eight channels each, and a CTA kUnits of them at a time, two a
+// lane group with their loads in flight together.
+constexpr int kUnits = 64;
+
+struct KvRows {
     KvGeom g;
-    const uint16_t* x[2];        // K, V
-    long long st[2], sh[2];      // strides of tokens and heads, elements
     const long long* slot;
-    uint32_t units;              // tokens * 2 * heads * groups
+    uint32_t units, per;  // tokens * per; groups of a token's K (and of its V)
+    uint32_t inv;         // ceil(2^32 / per)
+};
+
+struct KvUnit {
+    uint32_t t, kv, head, grp;
+    bool in;
+};
+
+// Unit `off` of the run that starts at unit u0 = q0 * per + r0.
+template <int NG>
+__device__ __forceinline__ KvUnit kv_unit(const KvRows& a, uint32_t u0, uint32_t q0, uint32_t r0, uint32_t off) {
+    KvUnit u;
+    u.in = u0 + off < a.units;
+    const uint32_t local = r0 + (u.in ? off : 0), q = __umulhi(local, a.inv);  // exact: local * per < 2^32
+    const uint32_t row = q0 + (a.per > 1 ? q : local), rest = a.per > 1 ? local - q * a.per : 0;
+    u.t = row >> 1, u.kv = row & 1;
+    u.head = rest / NG, u.grp = rest % NG;
+    return u;
+}
+
+struct KvPlace {
+    uint8_t *codes, *pair;  // of the group
+};
+template <int D>
+__device__ __forceinline__ KvPlace kv_place(const KvGeom& g, const KvUnit& u, long long slot) {
+    constexpr int NG = D / 64;
+    const int page = (int)(slot >> g.page_log2), off = (int)slot & ((1 << g.page_log2) - 1);
+    uint8_t* rec = kv_record(g, page, (int)u.head);
+    const int half_b = (D / 2) << g.page_log2, pairs = (NG * 4) << g.page_log2;
+    return {rec + u.kv * half_b + off * (D / 2) + u.grp * 32, rec + 2 * half_b + u.kv * pairs + (off * NG + u.grp) * 4};
+}
+
+struct AppendArgs {
+    KvRows r;
+    const uint16_t* x[2];    // K, V
+    long long st[2], sh[2];  // strides of tokens and heads, elements
 };
 
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
-// Eight lanes a group of 64 channels, eight channels (one 16-byte load) a lane:
-// minimum and maximum in packed bf16 (exact), the codes in fp32 with the
-// rounding steps of the definition, one 4-byte store a lane.  Bound by bytes:
-// 2 in and 0.56 out a value.
+// Minimum and maximum in packed bf16 (exact), the codes in fp32.  The
+// definition's code is rint of the rounded quotient (x - b) / s; (x - b) times
+// the reciprocal is off by at most 2^-19 for quotients up to 16, so its rint is
+// the same unless it lies within 2^-16 of a half, and only then (one group in
+// some thousands) are the quotients taken.  Bound by bytes: 2 in and 0.56 out a
+// value.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
-    constexpr int NG = D / 64;
     const int lane8 = threadIdx.x & 7;
     pdl_wait();
     pdl_trigger();
-    for (uint32_t u0 = blockIdx.x * 32u; u0 < a.units; u0 += gridDim.x * 32u) {
-        const uint32_t u = u0 + (threadIdx.x >> 3);
-        const bool in = u < a.units;
-        const uint32_t uu = in ? u : a.units - 1;
-        const uint32_t grp = uu % NG, r = uu / NG;
-        const uint32_t head = r % (uint32_t)a.g.heads, r2 = r / (uint32_t)a.g.heads;
-        const uint32_t kv = r2 & 1u, t = r2 >> 1;
-        const long long slot = a.slot[t];
-        const uint16_t* src = kv ? a.x[1] + (long long)t * a.st[1] + head * a.sh[1]
-                                 : a.x[0] + (long long)t * a.st[0] + head * a.sh[0];
-        const uint4 v = *reinterpret_cast<const uint4*>(src + grp * 64 + lane8 * 8);
-        __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf2(v.x), as_bf2(v.y)), __hmin2_nan(as_bf2(v.z), as_bf2(v.w)));
-        __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf2(v.x), as_bf2(v.y)), __hmax2_nan(as_bf2(v.z), as_bf2(v.w)));
+    for (uint32_t u0 = blockIdx.x * (uint32_t)kUnits; u0 < a.r.units; u0 += gridDim.x * (uint32_t)kUnits) {
+        const uint32_t q0 = u0 / a.r.per, r0 = u0 - q0 * a.r.per;
+        KvUnit un[2];
+        uint4 v[2];
+        long long slot[2];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            mn = __hmin2_nan(mn, as_bf2(__shfl_xor_sync(~0u, as_u32(mn), o)));
-            mx = __hmax2_nan(mx, as_bf2(__shfl_xor_sync(~0u, as_u32(mx), o)));
+        for (int j = 0; j < 2; ++j) {
+            un[j] = kv_unit<D / 64>(a.r, u0, q0, r0, (threadIdx.x >> 3) + 32 * j);
+            const KvUnit& u = un[j];
+            const uint16_t* src = u.kv ? a.x[1] + (long long)u.t * a.st[1] + u.head * a.sh[1]
+                                       : a.x[0] + (long long)u.t * a.st[0] + u.head * a.sh[0];
+            v[j] = *reinterpret_cast<const uint4*>(src + u.grp * 64 + lane8 * 8);
+            slot[j] = a.r.slot[u.t];
         }
-        const float lo = __bfloat162float(__hmin_nan(mn.x, mn.y)), hi = __bfloat162float(__hmax_nan(mx.x, mx.y));
-        __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-        __half bh = __float2half_rn(lo);
-        float s = __half2float(sh);
-        const float b = __half2float(bh);
-        if (!(fabsf(lo) < 65536.f && fabsf(hi) < 65536.f)) {  // the group reads back as NaN
-            sh = __ushort_as_half(0);
-            bh = __ushort_as_half(0x7e00);
-            s = 0.f;
-        }
-        const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-        uint32_t word = 0;
-        if (s > 0.f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = __uint_as_float(i & 1 ? w4[i >> 1] & 0xffff0000u : w4[i >> 1] << 16);
-                const float q = rintf(__fdiv_rn(__fsub_rn(x, b), s));
-                word |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * i);
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf2(w4[0]), as_bf2(w4[1])), __hmin2_nan(as_bf2(w4[2]), as_bf2(w4[3])));
+            __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf2(w4[0]), as_bf2(w4[1])), __hmax2_nan(as_bf2(w4[2]), as_bf2(w4[3])));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                mn = __hmin2_nan(mn, as_bf2(__shfl_xor_sync(~0u, as_u32(mn), o)));
+                mx = __hmax2_nan(mx, as_bf2(__shfl_xor_sync(~0u, as_u32(mx), o)));
             }
+            const float lo = __bfloat162float(__hmin_nan(mn.x, mn.y)), hi = __bfloat162float(__hmax_nan(mx.x, mx.y));
+            __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+            __half bh = __float2half_rn(lo);
+            float s = __half2float(sh);
+            const float b = __half2float(bh);
+            if (!(fabsf(lo) < 65536.f && fabsf(hi) < 65536.f)) {  // the group reads back as NaN
+                sh = __ushort_as_half(0);
+                bh = __ushort_as_half(0x7e00);
+                s = 0.f;
+            }
+            uint32_t word = 0;
+            if (s > 0.f) {
+                const float inv = __frcp_rn(s);
+                float worst = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = __uint_as_float(i & 1 ? w4[i >> 1] & 0xffff0000u : w4[i >> 1] << 16);
+                    const float q = fminf(fmaxf(__fsub_rn(x, b) * inv, 0.f), 15.f);
+                    const float y = __fadd_rn(q, 12582912.f);  // 1.5 * 2^23: rint(q) in the low bits
+                    worst = fmaxf(worst, fabsf(q - __fsub_rn(y, 12582912.f)));
+                    word |= (__float_as_uint(y) & 15u) << (4 * i);
+                }
+                if (worst > 0.5f - 1.f / 65536.f) {
+                    word = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t pair = i < 2 ? w4[0] : i < 4 ? w4[1] : i < 6 ? w4[2] : w4[3];
+                        const float x = __uint_as_float(i & 1 ? pair & 0xffff0000u : pair << 16);
+                        const float q = rintf(__fdiv_rn(__fsub_rn(x, b), s));
+                        word |= (uint32_t)fminf(fmaxf(q, 0.f), 15.f) << (4 * i);
+                    }
+                }
+            }
+            if (!un[j].in || slot[j] < 0 || slot[j] >= a.r.g.slots) continue;
+            const KvPlace p = kv_place<D>(a.r.g, un[j], slot[j]);
+            reinterpret_cast<uint32_t*>(p.codes)[lane8] = word;
+            if (lane8 == 0) *reinterpret_cast<uint32_t*>(p.pair) = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
         }
-        if (!in || slot < 0 || slot >= a.g.slots) continue;
-        const int page = (int)(slot >> a.g.page_log2), off = (int)slot & ((1 << a.g.page_log2) - 1);
-        uint8_t* rec = kv_record(a.g, page, (int)head);
-        const int half_b = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
-        *reinterpret_cast<uint32_t*>(rec + kv * half_b + off * (D / 2) + grp * 32 + lane8 * 4) = word;
-        if (lane8 == 0)
-            *reinterpret_cast<uint32_t*>(rec + 2 * half_b + kv * pairs + (off * NG + grp) * 4) =
-                (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
     }
 }
 
-// ------------------------------------------------------------------ read
 struct ReadArgs {
-    KvGeom g;
-    const long long* slot;
+    KvRows r;
     uint16_t* b16[2];
     float* f32[2];
-    uint32_t units;  // tokens * 2 * heads * groups
 };
 
-// The append's mapping turned round: eight lanes a group, eight channels a lane.
+// The append's mapping turned round.
 template <int D>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
-    constexpr int NG = D / 64;
     const int lane8 = threadIdx.x & 7;
     pdl_wait();
     pdl_trigger();
-    for (uint32_t u = blockIdx.x * 32u + (threadIdx.x >> 3); u < a.units; u += gridDim.x * 32u) {
-        const uint32_t grp = u % NG, r = u / NG;
-        const uint32_t head = r % (uint32_t)a.g.heads, r2 = r / (uint32_t)a.g.heads;
-        const uint32_t kv = r2 & 1u, t = r2 >> 1;
-        const long long slot = a.slot[t];
-        uint32_t word = 0, sb = 0;
-        if (slot >= 0 && slot < a.g.slots) {
-            const int page = (int)(slot >> a.g.page_log2), off = (int)slot & ((1 << a.g.page_log2) - 1);
-            const uint8_t* rec = kv_record(a.g, page, (int)head);
-            const int half_b = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
-            word = *reinterpret_cast<const uint32_t*>(rec + kv * half_b + off * (D / 2) + grp * 32 + lane8 * 4);
-            sb = *reinterpret_cast<const uint32_t*>(rec + 2 * half_b + kv * pairs + (off * NG + grp) * 4);
-        }
-        const float2 p = half2_to_float2(sb);
-        float x[8];
+    for (uint32_t u0 = blockIdx.x * (uint32_t)kUnits; u0 < a.r.units; u0 += gridDim.x * (uint32_t)kUnits) {
+        const uint32_t q0 = u0 / a.r.per, r0 = u0 - q0 * a.r.per;
+        KvUnit un[2];
+        uint32_t word[2], sb[2];
+        long long slot[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, (float)((word >> (4 * i)) & 15u), p.y);
-        const size_t at = ((size_t)t * a.g.heads + head) * D + grp * 64 + lane8 * 8;
-        if (uint16_t* o = kv ? a.b16[1] : a.b16[0]) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)f32_to_bf16_bits(x[2 * i]) | ((uint32_t)f32_to_bf16_bits(x[2 * i + 1]) << 16);
-            *reinterpret_cast<uint4*>(o + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 2; ++j) {
+            un[j] = kv_unit<D / 64>(a.r, u0, q0, r0, (threadIdx.x >> 3) + 32 * j);
+            slot[j] = a.r.slot[un[j].t];
         }
-        if (float* o = kv ? a.f32[1] : a.f32[0]) {
-            *reinterpret_cast<float4*>(o + at) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(o + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            word[j] = sb[j] = 0;
+            if (slot[j] >= 0 && slot[j] < a.r.g.slots) {
+                const KvPlace p = kv_place<D>(a.r.g, un[j], slot[j]);
+                word[j] = reinterpret_cast<const uint32_t*>(p.codes)[lane8];
+                sb[j] = *reinterpret_cast<const uint32_t*>(p.pair);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!un[j].in) continue;
+            const float2 p = half2_to_float2(sb[j]);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, (float)((word[j] >> (4 * i)) & 15u), p.y);
+            const size_t at = ((size_t)un[j].t * a.r.g.heads + un[j].head) * D + un[j].grp * 64 + lane8 * 8;
+            if (uint16_t* o = un[j].kv ? a.b16[1] : a.b16[0]) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = as_u32(__floats2bfloat162_rn(x[2 * i], x[2 * i + 1]));
+                *reinterpret_cast<uint4*>(o + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (float* o = un[j].kv ? a.f32[1] : a.f32[0]) {
+                *reinterpret_cast<float4*>(o + at) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(o + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
         }
     }
+}
+
+// Units of a call, its grid: 16 CTAs an SM at most.
+inline KvRows kv_rows(const KvGeom& g, int dim, const long long* slot, int n_tokens) {
+    const uint32_t per = (uint32_t)g.heads * (uint32_t)(dim / 64);
+    return {g, slot, (uint32_t)n_tokens * 2u * per, per, (uint32_t)(((1ull << 32) + per - 1) / per)};
+}
+inline dim3 kv_rows_grid(const KvRows& r, int sms) {
+    return dim3(std::min((r.units + (uint32_t)kUnits - 1u) / (uint32_t)kUnits, (uint32_t)sms * 16u));
 }
 
 }  // namespace hs
@@ -336,12 +406,9 @@ extern "C" int hs_kv4_append(const hs_kv4_cache* cache, const uint16_t* k, long 
     if (!n_tokens) return HS_OK;
     const int sms = sm_count();
     if (!sms) return HS_ERR_CUDA;
-    const int ng = cache->head_dim / 64;
-    hs::AppendArgs a = {kv4_geom(cache), {k, v}, {k_st, v_st}, {k_sh, v_sh}, slot,
-                        (uint32_t)n_tokens * 2u * (uint32_t)cache->n_kv_heads * (uint32_t)ng};
-    const dim3 grid(std::min((a.units + 31u) / 32u, (uint32_t)sms * 64u));
-    auto kern = ng == 1 ? hs::kv4_append_kernel<64> : hs::kv4_append_kernel<128>;
-    if (launch_pdl(kern, grid, dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    hs::AppendArgs a = {hs::kv_rows(kv4_geom(cache), cache->head_dim, slot, n_tokens), {k, v}, {k_st, v_st}, {k_sh, v_sh}};
+    auto kern = cache->head_dim == 64 ? hs::kv4_append_kernel<64> : hs::kv4_append_kernel<128>;
+    if (launch_pdl(kern, hs::kv_rows_grid(a.r, sms), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;
     return launch_err();
 }
@@ -356,12 +423,9 @@ extern "C" int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot, int
     if (!n_tokens) return HS_OK;
     const int sms = sm_count();
     if (!sms) return HS_ERR_CUDA;
-    const int ng = cache->head_dim / 64;
-    hs::ReadArgs a = {kv4_geom(cache), slot, {k16, v16}, {k32, v32},
-                      (uint32_t)n_tokens * 2u * (uint32_t)cache->n_kv_heads * (uint32_t)ng};
-    const dim3 grid(std::min((a.units + 31u) / 32u, (uint32_t)sms * 64u));
-    auto kern = ng == 1 ? hs::kv4_read_kernel<64> : hs::kv4_read_kernel<128>;
-    if (launch_pdl(kern, grid, dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    hs::ReadArgs a = {hs::kv_rows(kv4_geom(cache), cache->head_dim, slot, n_tokens), {k16, v16}, {k32, v32}};
+    auto kern = cache->head_dim == 64 ? hs::kv4_read_kernel<64> : hs::kv4_read_kernel<128>;
+    if (launch_pdl(kern, hs::kv_rows_grid(a.r, sms), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;
     return launch_err();
 }

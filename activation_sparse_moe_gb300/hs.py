@@ -61,6 +61,13 @@ class hs_kv4_cache(C.Structure):
     _fields_ = [("pool", C.c_void_p), ("n_pages", C.c_int), ("page_tokens", C.c_int), ("n_kv_heads", C.c_int),
                 ("head_dim", C.c_int)]
 
+    @property
+    def ref(self):
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = C.byref(self)
+        return r
+
 
 _lib = None
 
@@ -278,45 +285,65 @@ def make_kv4_cache(pool, n_pages, page_tokens, n_kv_heads, head_dim) -> hs_kv4_c
 
 
 def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
-    return lib().hs_kv4_pool_bytes(C.byref(cache))
+    return lib().hs_kv4_pool_bytes(cache.ref)
 
 
+# The key/value cache's calls are made for every layer of every token, so their
+# marshalling is kept short: pointers and strides straight from the tensors.
 def hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, table_width, ring, counters_in,
                 max_tokens, table_out, seq_len, q_start, slot, position, counters_out, short, stream=None):
-    _check("hs_kv4_plan", lib().hs_kv4_plan(
-        _p(cached_len), _p(new_len), n_seqs, page_tokens, n_pages, _p(table_in), table_width, _p(ring),
-        _p(counters_in), max_tokens, _p(table_out), _p(seq_len), _p(q_start), _p(slot), _p(position),
-        _p(counters_out), _p(short), _stream(stream)))
+    st = lib().hs_kv4_plan(
+        cached_len.data_ptr(), new_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width,
+        ring.data_ptr(), counters_in.data_ptr(), max_tokens, table_out.data_ptr(), seq_len.data_ptr(),
+        q_start.data_ptr(), slot.data_ptr(), _p(position), counters_out.data_ptr(), short.data_ptr(),
+        _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv4_plan", st)
 
 
-def _rows(t, fn: str):
-    """Pointer and (token, head) strides of a [tokens][heads][channels] tensor."""
-    if t.stride(2) != 1:
-        raise HsError(fn, HS_ERR_INVALID_ARG)
-    return _p(t), t.stride(0), t.stride(1)
+def _kv4_stream(stream):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def hs_kv4_append(cache: hs_kv4_cache, k, v, slots, n_tokens, stream=None):
     """k, v: bf16 [tokens][kv heads][head_dim], any token and head strides."""
-    _check("hs_kv4_append", lib().hs_kv4_append(C.byref(cache), *_rows(k, "hs_kv4_append"),
-                                                *_rows(v, "hs_kv4_append"), _p(slots), n_tokens, _stream(stream)))
+    (kt, kh, kc), (vt, vh, vc) = k.stride(), v.stride()
+    if kc != 1 or vc != 1:
+        raise HsError("hs_kv4_append", HS_ERR_INVALID_ARG)
+    st = lib().hs_kv4_append(cache.ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), n_tokens,
+                             _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv4_append", st)
 
 
 def hs_kv4_read(cache: hs_kv4_cache, slots, n_tokens, k_bf16=None, v_bf16=None, k_f32=None, v_f32=None, stream=None):
-    _check("hs_kv4_read", lib().hs_kv4_read(C.byref(cache), _p(slots), n_tokens, _p(k_bf16), _p(v_bf16), _p(k_f32),
-                                            _p(v_f32), _stream(stream)))
+    st = lib().hs_kv4_read(cache.ref, slots.data_ptr(), n_tokens, _p(k_bf16), _p(v_bf16), _p(k_f32), _p(v_f32),
+                           _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv4_read", st)
 
 
 def hs_kv4_attention_workspace_size(cache: hs_kv4_cache, n_seqs, n_q_heads) -> int:
-    return lib().hs_kv4_attention_workspace_size(C.byref(cache), n_seqs, n_q_heads)
+    return lib().hs_kv4_attention_workspace_size(cache.ref, n_seqs, n_q_heads)
 
 
 def hs_kv4_attention(cache: hs_kv4_cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out,
                      workspace=None, workspace_bytes=None, stream=None):
     """q, out: bf16 [tokens][query heads][head_dim], any token and head
     strides; table: int32 [n_seqs][table_width] contiguous."""
-    nb = workspace_bytes if workspace_bytes is not None else (workspace.numel() * workspace.element_size()
-                                                              if workspace is not None else 0)
-    _check("hs_kv4_attention", lib().hs_kv4_attention(
-        C.byref(cache), *_rows(q, "hs_kv4_attention"), _p(q_start), _p(seq_len), _p(table), table.shape[1], n_seqs,
-        q.shape[0], q.shape[1], max_new, scale, window, *_rows(out, "hs_kv4_attention"), _p(workspace), nb, _stream(stream)))
+    (qt, qh, qc), (ot, oh, oc) = q.stride(), out.stride()
+    if qc != 1 or oc != 1:
+        raise HsError("hs_kv4_attention", HS_ERR_INVALID_ARG)
+    if workspace is None:
+        ws, nb = None, 0
+    else:
+        ws, nb = workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes
+    tokens, heads, _ = q.shape
+    st = lib().hs_kv4_attention(
+        cache.ref, q.data_ptr(), qt, qh, q_start.data_ptr(), seq_len.data_ptr(), table.data_ptr(), table.shape[1],
+        n_seqs, tokens, heads, max_new, scale, window, out.data_ptr(), ot, oh, ws, nb, _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv4_attention", st)
