@@ -161,46 +161,48 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
 }
 
 // ------------------------------------------------------- append and read
-// A unit is a group of 64 channels of one (token, K or V, kv head); eight lanes
-// take one, eight channels each, and a CTA kUnits of them at a time, two a
-// lane group with their loads in flight together.
-constexpr int kUnits = 64;
+// Eight lanes take a group of 64 channels, eight channels each.  A warp's four
+// lane groups walk along one row (a token's K or V over all its heads), or
+// along two or four rows where a row has two groups or one: a row's addresses
+// are worked out once, then only stepped (worked out group by group they took
+// half of the instructions).
+constexpr int kAhead = 4;        // groups a lane group has in flight
+constexpr int kRowGroups = 64;   // groups of a row that one warp takes; more go to gridDim.y
 
 struct KvRows {
     KvGeom g;
     const long long* slot;
-    uint32_t units, per;  // tokens * per; groups of a token's K (and of its V)
-    uint32_t inv;         // ceil(2^32 / per)
+    int rows, per;   // 2 * tokens; groups of a row
+    int abreast;     // lane groups on one row: 1, 2 or 4
 };
 
-struct KvUnit {
-    uint32_t t, kv, head, grp;
-    bool in;
-};
-
-// Unit `off` of the run that starts at unit u0 = q0 * per + r0.
-template <int NG>
-__device__ __forceinline__ KvUnit kv_unit(const KvRows& a, uint32_t u0, uint32_t q0, uint32_t r0, uint32_t off) {
-    KvUnit u;
-    u.in = u0 + off < a.units;
-    const uint32_t local = r0 + (u.in ? off : 0), q = __umulhi(local, a.inv);  // exact: local * per < 2^32
-    const uint32_t row = q0 + (a.per > 1 ? q : local), rest = a.per > 1 ? local - q * a.per : 0;
-    u.t = row >> 1, u.kv = row & 1;
-    u.head = rest / NG, u.grp = rest % NG;
-    return u;
-}
-
-struct KvPlace {
-    uint8_t *codes, *pair;  // of the group
-};
+// The place of the calling lane group: its row and its first group there.
 template <int D>
-__device__ __forceinline__ KvPlace kv_place(const KvGeom& g, const KvUnit& u, long long slot) {
-    constexpr int NG = D / 64;
-    const int page = (int)(slot >> g.page_log2), off = (int)slot & ((1 << g.page_log2) - 1);
-    uint8_t* rec = kv_record(g, page, (int)u.head);
-    const int half_b = (D / 2) << g.page_log2, pairs = (NG * 4) << g.page_log2;
-    return {rec + u.kv * half_b + off * (D / 2) + u.grp * 32, rec + 2 * half_b + u.kv * pairs + (off * NG + u.grp) * 4};
-}
+struct KvLane {
+    static constexpr int NG = D / 64;
+    int t, kv, group, end, head, grp;
+    long long slot;
+    uint8_t *codes, *pair;  // of its first group; the next one's are `step` bytes on
+    size_t step;
+    __device__ __forceinline__ KvLane(const KvRows& a) {
+        const int lg = (threadIdx.x & 31) >> 3, warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+        const int row = a.abreast == 4 ? warp : a.abreast == 2 ? warp * 2 + (lg >> 1) : warp * 4 + lg;
+        group = blockIdx.y * kRowGroups + (lg & (a.abreast - 1));
+        end = row < a.rows ? min(a.per, (int)(blockIdx.y + 1) * kRowGroups) : 0;
+        t = row < a.rows ? row >> 1 : 0;
+        kv = row & 1;
+        head = group / NG, grp = group % NG;
+        slot = end ? a.slot[t] : -1;
+        if (slot >= a.g.slots) slot = -1;
+        const long long at = max(slot, 0ll);
+        const int page = (int)(at >> a.g.page_log2), off = (int)at & ((1 << a.g.page_log2) - 1);
+        uint8_t* rec = kv_record(a.g, page, head);
+        const int half_b = (D / 2) << a.g.page_log2, pairs = (NG * 4) << a.g.page_log2;
+        codes = rec + kv * half_b + off * (D / 2) + grp * 32;
+        pair = rec + 2 * half_b + kv * pairs + (off * NG + grp) * 4;
+        step = (size_t)(a.abreast > NG ? a.abreast / NG : 1) * (size_t)a.g.rec;
+    }
+};
 
 struct AppendArgs {
     KvRows r;
@@ -212,32 +214,37 @@ __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t v) { return *reinterpr
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
 
 // Minimum and maximum in packed bf16 (exact), the codes in fp32.  The
-// definition's code is rint of the rounded quotient (x - b) / s; (x - b) times
-// the reciprocal is off by at most 2^-19 for quotients up to 16, so its rint is
-// the same unless it lies within 2^-16 of a half, and only then (one group in
-// some thousands) are the quotients taken.  Bound by bytes: 2 in and 0.56 out a
-// value.
+// definition's code is rint of the rounded quotient (x - b) / s, clamped.
+// Here t = sat((x - b) * r), r an approximate 1 / (15 s): 15 t is within 2^-17
+// of the clamped quotient, so its rint is the same unless it lies within 2^-16
+// of a half, and only then (one group in some thousands) are the quotients
+// taken.  The four codes of a half word are summed as a float, exactly.  The
+// division of the range by 15 is one correction step of the product with the
+// rounded 1 / 15, which rounds as the division does.  Ten instructions a value
+// where the quotients took thirty: the instructions bounded this, not the bytes
+// (2 in and 0.56 out a value).
 template <int D>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(128) kv4_append_kernel(const AppendArgs a) {
     const int lane8 = threadIdx.x & 7;
     pdl_wait();
     pdl_trigger();
-    for (uint32_t u0 = blockIdx.x * (uint32_t)kUnits; u0 < a.r.units; u0 += gridDim.x * (uint32_t)kUnits) {
-        const uint32_t q0 = u0 / a.r.per, r0 = u0 - q0 * a.r.per;
-        KvUnit un[2];
-        uint4 v[2];
-        long long slot[2];
+    const KvLane<D> u(a.r);
+    const uint16_t* src = (u.kv ? a.x[1] : a.x[0]) + (long long)u.t * (u.kv ? a.st[1] : a.st[0]) +
+                          (long long)u.head * (u.kv ? a.sh[1] : a.sh[0]) + u.grp * 64 + lane8 * 8;
+    const long long src_step = (u.kv ? a.sh[1] : a.sh[0]) * (a.r.abreast > D / 64 ? a.r.abreast / (D / 64) : 1);
+    uint8_t *codes = u.codes, *pair = u.pair;
+    // the same number of turns for all lanes of a warp: they shuffle
+    for (int g0 = u.group; __any_sync(~0u, g0 < u.end); g0 += kAhead * a.r.abreast) {
+        uint4 v[kAhead];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            un[j] = kv_unit<D / 64>(a.r, u0, q0, r0, (threadIdx.x >> 3) + 32 * j);
-            const KvUnit& u = un[j];
-            const uint16_t* src = u.kv ? a.x[1] + (long long)u.t * a.st[1] + u.head * a.sh[1]
-                                       : a.x[0] + (long long)u.t * a.st[0] + u.head * a.sh[0];
-            v[j] = *reinterpret_cast<const uint4*>(src + u.grp * 64 + lane8 * 8);
-            slot[j] = a.r.slot[u.t];
+        for (int j = 0; j < kAhead; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (g0 + j * a.r.abreast < u.end) v[j] = *reinterpret_cast<const uint4*>(src);
+            src += src_step;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kAhead; ++j, codes += u.step, pair += u.step) {
+            if (!__any_sync(~0u, g0 + j * a.r.abreast < u.end)) break;
             const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
             __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf2(w4[0]), as_bf2(w4[1])), __hmin2_nan(as_bf2(w4[2]), as_bf2(w4[3])));
             __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf2(w4[0]), as_bf2(w4[1])), __hmax2_nan(as_bf2(w4[2]), as_bf2(w4[3])));
@@ -247,7 +254,8 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
                 mx = __hmax2_nan(mx, as_bf2(__shfl_xor_sync(~0u, as_u32(mx), o)));
             }
             const float lo = __bfloat162float(__hmin_nan(mn.x, mn.y)), hi = __bfloat162float(__hmax_nan(mx.x, mx.y));
-            __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+            const float range = __fsub_rn(hi, lo), fifteenth = range * (1.f / 15.f);
+            __half sh = __float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, fifteenth, range), 1.f / 15.f, fifteenth));
             __half bh = __float2half_rn(lo);
             float s = __half2float(sh);
             const float b = __half2float(bh);
@@ -258,16 +266,24 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
             }
             uint32_t word = 0;
             if (s > 0.f) {
-                const float inv = __frcp_rn(s);
-                float worst = 0.f;
+                float inv, worst = 0.f;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s * 15.f));
+                uint32_t half[2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x = __uint_as_float(i & 1 ? w4[i >> 1] & 0xffff0000u : w4[i >> 1] << 16);
-                    const float q = fminf(fmaxf(__fsub_rn(x, b) * inv, 0.f), 15.f);
-                    const float y = __fadd_rn(q, 12582912.f);  // 1.5 * 2^23: rint(q) in the low bits
-                    worst = fmaxf(worst, fabsf(q - __fsub_rn(y, 12582912.f)));
-                    word |= (__float_as_uint(y) & 15u) << (4 * i);
+                for (int h = 0; h < 2; ++h) {
+                    float sum = 8388608.f;  // 2^23: the sum's integer stands in the low bits
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = w4[2 * h + (i >> 1)];
+                        const float x = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+                        const float t = __saturatef(__fsub_rn(x, b) * inv);
+                        const float q = __fadd_rn(__fmaf_rn(t, 15.f, 12582912.f), -12582912.f);  // 1.5 * 2^23: rounds to an integer
+                        worst = fmaxf(worst, fabsf(__fmaf_rn(t, 15.f, -q)));
+                        sum = __fmaf_rn(q, (float)(1 << (4 * i)), sum);
+                    }
+                    half[h] = __float_as_uint(sum);
                 }
+                word = __byte_perm(half[0], half[1], 0x5410);
                 if (worst > 0.5f - 1.f / 65536.f) {
                     word = 0;
 #pragma unroll 1
@@ -279,10 +295,9 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const AppendArgs a) {
                     }
                 }
             }
-            if (!un[j].in || slot[j] < 0 || slot[j] >= a.r.g.slots) continue;
-            const KvPlace p = kv_place<D>(a.r.g, un[j], slot[j]);
-            reinterpret_cast<uint32_t*>(p.codes)[lane8] = word;
-            if (lane8 == 0) *reinterpret_cast<uint32_t*>(p.pair) = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
+            if (g0 + j * a.r.abreast >= u.end || u.slot < 0) continue;
+            reinterpret_cast<uint32_t*>(codes)[lane8] = word;
+            if (lane8 == 0) *reinterpret_cast<uint32_t*>(pair) = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
         }
     }
 }
@@ -295,58 +310,60 @@ struct ReadArgs {
 
 // The append's mapping turned round.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(128) kv4_read_kernel(const ReadArgs a) {
     const int lane8 = threadIdx.x & 7;
     pdl_wait();
     pdl_trigger();
-    for (uint32_t u0 = blockIdx.x * (uint32_t)kUnits; u0 < a.r.units; u0 += gridDim.x * (uint32_t)kUnits) {
-        const uint32_t q0 = u0 / a.r.per, r0 = u0 - q0 * a.r.per;
-        KvUnit un[2];
-        uint32_t word[2], sb[2];
-        long long slot[2];
+    const KvLane<D> u(a.r);
+    const uint8_t *codes = u.codes, *pair = u.pair;
+    uint16_t* b16 = u.kv ? a.b16[1] : a.b16[0];
+    float* f32 = u.kv ? a.f32[1] : a.f32[0];
+    size_t at = ((size_t)u.t * a.r.g.heads + u.head) * D + u.grp * 64 + lane8 * 8;
+    const int at_step = a.r.abreast * 64;  // outputs are packed: groups follow one another
+    for (int g0 = u.group; g0 < u.end; g0 += kAhead * a.r.abreast) {
+        uint32_t word[kAhead], sb[kAhead];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            un[j] = kv_unit<D / 64>(a.r, u0, q0, r0, (threadIdx.x >> 3) + 32 * j);
-            slot[j] = a.r.slot[un[j].t];
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kAhead; ++j, codes += u.step, pair += u.step) {
             word[j] = sb[j] = 0;
-            if (slot[j] >= 0 && slot[j] < a.r.g.slots) {
-                const KvPlace p = kv_place<D>(a.r.g, un[j], slot[j]);
-                word[j] = reinterpret_cast<const uint32_t*>(p.codes)[lane8];
-                sb[j] = *reinterpret_cast<const uint32_t*>(p.pair);
+            if (u.slot >= 0 && g0 + j * a.r.abreast < u.end) {
+                word[j] = reinterpret_cast<const uint32_t*>(codes)[lane8];
+                sb[j] = *reinterpret_cast<const uint32_t*>(pair);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (!un[j].in) continue;
+        for (int j = 0; j < kAhead; ++j, at += at_step) {
+            if (g0 + j * a.r.abreast >= u.end) break;
             const float2 p = half2_to_float2(sb[j]);
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(p.x, (float)((word[j] >> (4 * i)) & 15u), p.y);
-            const size_t at = ((size_t)un[j].t * a.r.g.heads + un[j].head) * D + un[j].grp * 64 + lane8 * 8;
-            if (uint16_t* o = un[j].kv ? a.b16[1] : a.b16[0]) {
+            for (int i = 0; i < 4; ++i) {  // channels i and i + 4: 1024 + code is exact in fp16
+                uint32_t h = ((word[j] >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+                const float2 c = __half22float2(__hsub2(*reinterpret_cast<__half2*>(&h), __half2half2(__ushort_as_half(0x6400))));
+                x[i] = fmaf(p.x, c.x, p.y);
+                x[i + 4] = fmaf(p.x, c.y, p.y);
+            }
+            if (b16) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = as_u32(__floats2bfloat162_rn(x[2 * i], x[2 * i + 1]));
-                *reinterpret_cast<uint4*>(o + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(b16 + at) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (float* o = un[j].kv ? a.f32[1] : a.f32[0]) {
-                *reinterpret_cast<float4*>(o + at) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(o + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            if (f32) {
+                *reinterpret_cast<float4*>(f32 + at) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(f32 + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
             }
         }
     }
 }
 
-// Units of a call, its grid: 16 CTAs an SM at most.
+constexpr int kRowThreads = 128;
 inline KvRows kv_rows(const KvGeom& g, int dim, const long long* slot, int n_tokens) {
-    const uint32_t per = (uint32_t)g.heads * (uint32_t)(dim / 64);
-    return {g, slot, (uint32_t)n_tokens * 2u * per, per, (uint32_t)(((1ull << 32) + per - 1) / per)};
+    const int per = g.heads * (dim / 64);
+    return {g, slot, 2 * n_tokens, per, per >= 3 ? 4 : per};
 }
-inline dim3 kv_rows_grid(const KvRows& r, int sms) {
-    return dim3(std::min((r.units + (uint32_t)kUnits - 1u) / (uint32_t)kUnits, (uint32_t)sms * 16u));
+inline dim3 kv_rows_grid(const KvRows& r) {
+    const int rows = kRowThreads / 32 * (4 / r.abreast);  // of a CTA
+    return dim3((r.rows + rows - 1) / rows, (r.per + kRowGroups - 1) / kRowGroups);
 }
 
 }  // namespace hs
@@ -404,11 +421,9 @@ extern "C" int hs_kv4_append(const hs_kv4_cache* cache, const uint16_t* k, long 
     if (n_tokens > hs::kKvMaxTokens) return HS_ERR_UNSUPPORTED_SHAPE;
     if (!al16(k) || !al16(v) || ((uintptr_t)slot & 7u) || (k_st | k_sh | v_st | v_sh) & 7) return HS_ERR_MISALIGNED;
     if (!n_tokens) return HS_OK;
-    const int sms = sm_count();
-    if (!sms) return HS_ERR_CUDA;
     hs::AppendArgs a = {hs::kv_rows(kv4_geom(cache), cache->head_dim, slot, n_tokens), {k, v}, {k_st, v_st}, {k_sh, v_sh}};
     auto kern = cache->head_dim == 64 ? hs::kv4_append_kernel<64> : hs::kv4_append_kernel<128>;
-    if (launch_pdl(kern, hs::kv_rows_grid(a.r, sms), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    if (launch_pdl(kern, hs::kv_rows_grid(a.r), dim3(hs::kRowThreads), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;
     return launch_err();
 }
@@ -421,11 +436,9 @@ extern "C" int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot, int
     if (n_tokens > hs::kKvMaxTokens) return HS_ERR_UNSUPPORTED_SHAPE;
     if (((uintptr_t)slot & 7u) || !al16(k16) || !al16(v16) || !al16(k32) || !al16(v32)) return HS_ERR_MISALIGNED;
     if (!n_tokens) return HS_OK;
-    const int sms = sm_count();
-    if (!sms) return HS_ERR_CUDA;
     hs::ReadArgs a = {hs::kv_rows(kv4_geom(cache), cache->head_dim, slot, n_tokens), {k16, v16}, {k32, v32}};
     auto kern = cache->head_dim == 64 ? hs::kv4_read_kernel<64> : hs::kv4_read_kernel<128>;
-    if (launch_pdl(kern, hs::kv_rows_grid(a.r, sms), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
+    if (launch_pdl(kern, hs::kv_rows_grid(a.r), dim3(hs::kRowThreads), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;
     return launch_err();
 }
