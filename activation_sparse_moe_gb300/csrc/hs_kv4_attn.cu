@@ -54,12 +54,11 @@ struct DecodeCfg {
     static constexpr int kSlotBytes = kv_record_bytes(kKvStep, D);
     static constexpr int kWarps = RT * KW;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kO = 16 * NQ * kNg;          // accumulators of a thread
-    static constexpr int kMerge = kO + 4 * NQ;        // and its maxima and sums
     static constexpr int kRingBytes = kWarps * kSlots * kSlotBytes;
-    static constexpr int kMergeBytes = RT * (KW / 2) * kMerge * 128;
+    static constexpr int kLine = D + 4;               // floats of a row of the warps' sums (padded against bank conflicts)
+    static constexpr int kMergeBytes = kWarps * 8 * NQ * (kLine + 2) * 4;
     static constexpr int kRows = 8 * NQ * RT;
-    static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16; }
+    static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (3 * n_seqs + 2) * 4 + 16; }
 };
 
 // Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 32-key steps
@@ -83,9 +82,10 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     using C = DecodeCfg<D, NQ, RT, KW>;
     constexpr int NG = C::kNg;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* merge = reinterpret_cast<float*>(smem + C::kRingBytes);
+    float* merge = reinterpret_cast<float*>(smem + C::kRingBytes);  // [warp][row][kLine], then (maximum, sum) [warp][row]
+    float2* merge_ml = reinterpret_cast<float2*>(merge + C::kWarps * 8 * NQ * C::kLine);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRingBytes + C::kMergeBytes);
-    long long* cum = reinterpret_cast<long long*>(bars + 32);
+    uint32_t* cum = reinterpret_cast<uint32_t*>(bars + 32);
     int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
     int* ls = qs + a.n_seqs + 1;
     // Where a warp computes and where it loads, a copy a warp in shared memory
@@ -102,6 +102,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     }
     pdl_wait();
     pdl_trigger();
+    for (int i = tid; i <= a.n_seqs; i += C::kThreads) {  // at hand in shared memory
+        qs[i] = a.q_start[i];
+        if (i < a.n_seqs) ls[i] = a.seq_len[i];
+    }
+    __syncthreads();
     kv_schedule(a, qs, ls, cum);
     KvWalk& w = walks[warp];
     w = ahead[warp] = kv_begin(a, qs, ls, cum);
@@ -452,81 +457,66 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         O[i][u][n][e] = fmaf(O[i][u][n][e], e < 2 ? even : even * 0.0625f, bs[i][n][e & 1]);
+        // The key warps' sums meet in shared memory; then a warp takes a row at a time,
+        // adds them in the order of the warps and writes the row, as output or as a piece.
 #pragma unroll
-        for (int half = KW / 2; half; half >>= 1) {
-            if (kw >= half && kw < 2 * half) {
-                float* b = merge + (rt * (KW / 2) + kw - half) * C::kMerge * 32 + lane;
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
+            for (int e = 0; e < 2; ++e) {
+                const int at = warp * 8 * NQ + n * 8 + 2 * t + e;
 #pragma unroll
-                    for (int i = 0; i < NG; ++i)
+                for (int i = 0; i < NG; ++i)
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) b[(((n * NG + i) * 4 + u) * 4 + e) * 32] = O[i][u][n][e];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        b[(C::kO + 4 * n + e) * 32] = m[n][e];
-                        b[(C::kO + 4 * n + 2 + e) * 32] = l[n][e];
-                    }
-                }
+                    for (int u = 0; u < 4; u += 2)
+                        *reinterpret_cast<float4*>(merge + at * C::kLine + i * 64 + g * 8 + u * 2) =
+                            make_float4(O[i][u][n][e], O[i][u][n][2 + e], O[i][u + 1][n][e], O[i][u + 1][n][2 + e]);
+                if (g == 0) merge_ml[at] = make_float2(m[n][e], l[n][e]);
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-            if (kw < half) {
-                const float* b = merge + (rt * (KW / 2) + kw) * C::kMerge * 32 + lane;
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float om = b[(C::kO + 4 * n + e) * 32], nm = fmaxf(m[n][e], om);
-                        const float f0 = ex2(m[n][e] - nm), f1 = ex2(om - nm);
-                        m[n][e] = nm;
-                        l[n][e] = l[n][e] * f0 + b[(C::kO + 4 * n + 2 + e) * 32] * f1;
-#pragma unroll
-                        for (int i = 0; i < NG; ++i)
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                                for (int x = e; x < 4; x += 2)
-                                    O[i][u][n][x] = O[i][u][n][x] * f0 + b[(((n * NG + i) * 4 + u) * 4 + x) * 32] * f1;
-                    }
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-        }
-
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         const bool whole = cnt == w.tiles;
-        if (kw == 0) {
+        const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
+        const size_t piece = (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * a.rows;
+#pragma unroll 1
+        for (int row = warp; row < rows; row += C::kWarps) {
+            constexpr int V = D / 32;
+            using Vec = typename FloatVec<V>::T;
+            const int from = (row / (8 * NQ)) * KW * 8 * NQ + row % (8 * NQ);
+            float2 ml[KW];
+            float top = -1e30f, sum = 0.f, acc[V];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int i = 0; i < KW; ++i) {
+                ml[i] = merge_ml[from + i * 8 * NQ];
+                top = fmaxf(top, ml[i].x);
+            }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = row0 + n * 8 + 2 * t + e, in_tile = kv_row_token(a, row), tok = w.r * a.tq + in_tile;
-                    if (row >= a.tq * a.group || tok >= w.n) continue;
-                    if (whole) {
-                        const float inv = l[n][e] != 0.f ? 1.f / l[n][e] : 0.f;
-                        uint16_t* dst = a.out + (long long)(w.row0 + tok) * a.o_st + (long long)(w.head * a.group + row - in_tile * a.group) * a.o_sh + g * 8;
+            for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            uint32_t u[4];
+            for (int i = 0; i < KW; ++i) {
+                const float f = ex2(ml[i].x - top);
+                const Vec v = reinterpret_cast<const Vec*>(merge + (from + i * 8 * NQ) * C::kLine)[lane];
+                sum = fmaf(f, ml[i].y, sum);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                u[x] = (uint32_t)f32_to_bf16_bits(O[i][x][n][e] * inv) |
-                                       ((uint32_t)f32_to_bf16_bits(O[i][x][n][2 + e] * inv) << 16);
-                            *reinterpret_cast<uint4*>(dst + i * 64) = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    } else {
-                        const size_t slot = 2 * blockIdx.x + (w.tile == 0 ? 1 : 0);
-                        float* dst = a.part_o + (slot * a.rows + row) * D + g * 8;
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(&v)[e], acc[e]);
+            }
+            if (whole) {
+                const int in_tile = kv_row_token(a, row);
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (long long)(w.row0 + w.r * a.tq + in_tile) * a.o_st +
+                                                            (long long)(w.head * a.group + row - in_tile * a.group) * a.o_sh) + lane * (V / 2);
 #pragma unroll
-                        for (int i = 0; i < NG; ++i)
-#pragma unroll
-                            for (int x = 0; x < 4; x += 2)
-                                *reinterpret_cast<float4*>(dst + i * 64 + x * 2) =
-                                    make_float4(O[i][x][n][e], O[i][x][n][2 + e], O[i][x + 1][n][e], O[i][x + 1][n][2 + e]);
-                        if (g == 0) a.part_ml[slot * a.rows + row] = make_float2(m[n][e], l[n][e]);
-                    }
+                for (int e = 0; e < V / 2; ++e) {
+                    const __nv_bfloat162 z = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+                    dst[e] = *reinterpret_cast<const uint32_t*>(&z);
                 }
+            } else {
+                Vec o;
+#pragma unroll
+                for (int e = 0; e < V; ++e) reinterpret_cast<float*>(&o)[e] = acc[e];
+                reinterpret_cast<Vec*>(a.part_o + (piece + row) * D)[lane] = o;
+                if (lane == 0) a.part_ml[piece + row] = make_float2(top, sum);
+            }
         }
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, cum[a.n_seqs], &join_last, add_pieces<D, C::kWarps>);
         KvWalk n = w;
         kv_next_piece(a, qs, ls, n);
@@ -552,18 +542,18 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.pad = RT == 1 ? 8 : 4;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
+    if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
     if (hs_host::launch_pdl(kv4_decode_kernel<D, NQ, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
         return HS_ERR_CUDA;
     return HS_OK;
 }
 
-// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.
+// Row tiles of 8, 16 or 32: the smallest that holds a request's rows.
 template <int D>
 int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
     if (rows <= 8) return launch_decode<D, 1, 1, 4>(a, sms, s);
     if (rows <= 16) return launch_decode<D, 2, 1, 4>(a, sms, s);
-    if (rows <= 32) return launch_decode<D, 2, 2, 4>(a, sms, s);
-    return launch_decode<D, 2, 4, 2>(a, sms, s);
+    return launch_decode<D, 2, 2, 4>(a, sms, s);
 }
 
 }  // namespace hs
@@ -572,7 +562,7 @@ using namespace hs_host;
 
 // Rows of a request (new tokens x query heads of a kv head) from which the
 // chunk kernel is used.
-constexpr int kPrefillRows = 65;
+constexpr int kPrefillRows = 33;
 
 // Counters of arrived pieces, (maximum, sum) pairs and partial sums of the widest launch.
 static size_t kv4_ws_bytes(int dim) {
@@ -625,7 +615,7 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.part_o = reinterpret_cast<float*>(w + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long need = std::max((long long)max_new, 1ll) * a.group;
-    if (need >= kPrefillRows && hs_kv4_prefill_fits(dim, n_seqs)) return hs_kv4_prefill(a, dim, sms, s);
+    if (need >= kPrefillRows) return hs_kv4_prefill(a, dim, sms, s);
     const int r = dim == 64 ? hs::launch_rows<64>(a, need, sms, s) : hs::launch_rows<128>(a, need, sms, s);
     return r != HS_OK ? r : launch_err();
 }

@@ -140,13 +140,13 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 // written its piece of w's item.  *last is a word of shared memory; the warps meet at named barrier BAR; add is
 // add_pieces.
 template <int WARPS, int BAR, typename Add>
-__device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, long long total, int* last, Add add) {
+__device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, uint32_t total, int* last, Add add) {
     const KvCut cut = kv_cut(a, total);
     const int me = blockIdx.x;
     const bool lead = warp == 0 && (threadIdx.x & 31) == 0;
     // the unit with which this piece began: of the run's first item the run's, else
     // what the run has left lies before the run's end
-    const long long begin = w.first ? cut.at(me) - w.tile : cut.at(me + 1) - w.left, end = begin + w.tiles;
+    const uint32_t begin = w.first ? cut.at(me) - w.tile : cut.at(me + 1) - w.left, end = begin + (uint32_t)w.tiles;
     const int c = cut.cta_of(begin), pieces = cut.cta_of(end - 1) - c + 1;
     auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(32 * WARPS) : "memory"); };
     auto arrive = [&](int* counter, int of) -> bool {

@@ -37,7 +37,7 @@ struct PrefillCfg {
     static constexpr int kTileBytes = kPfKeys * D * 2;   // a K or V tile
     static constexpr int kPackedBytes = kPfKeys * (D / 2 + 4 * kNg);
     static constexpr int kFixed = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes;
-    static constexpr int smem(int n_seqs) { return 1024 + kFixed + 1024 + (n_seqs + 1) * 8 + (2 * n_seqs + 1) * 4 + 16; }
+    static constexpr int smem(int n_seqs) { return 1024 + kFixed + 1024 + (n_seqs + 1) * 4; }
 };
 
 struct PfShared {
@@ -116,9 +116,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     uint8_t* packed_s = kv_s + kPfSlots * C::kTileBytes;    // [kPfPacked] codes, pairs
     PfShared& sh = *reinterpret_cast<PfShared*>(packed_s + kPfPacked * C::kPackedBytes);
     static_assert(sizeof(PfShared) <= 1024, "barriers");
-    long long* cum = reinterpret_cast<long long*>(packed_s + kPfPacked * C::kPackedBytes + 1024);
-    int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
-    int* ls = qs + a.n_seqs + 1;
+    uint32_t* cum = reinterpret_cast<uint32_t*>(packed_s + kPfPacked * C::kPackedBytes + 1024);
+    const int *qs = a.q_start, *ls = a.seq_len;  // looked at once an item: no room here for 4096 requests' copies
     // (Reductions of values that all lanes share: they come out in uniform registers,
     // which the tensor-core instructions' operands have to be in.)
     const int tid = threadIdx.x, lane = tid & 31, warp = (int)warp_max_u32(threadIdx.x >> 5);
@@ -554,6 +553,8 @@ int launch_prefill(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.min_units = 1;
     a.pad = 4;
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
+    static_assert(PrefillCfg<D>::smem(kKvMaxSeqs) <= kPfMaxSmem, "shared memory");
+    if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
     if (hs_host::launch_pdl(kv4_prefill_kernel<D>, dim3(std::min(152, sms)), dim3(kPfThreads), PrefillCfg<D>::smem(a.n_seqs), s, a) !=
         cudaSuccess)
         return HS_ERR_CUDA;
@@ -561,10 +562,6 @@ int launch_prefill(KvAttnArgs& a, int sms, cudaStream_t s) {
 }
 
 }  // namespace hs
-
-bool hs_kv4_prefill_fits(int dim, int n_seqs) {
-    return (dim == 64 ? hs::PrefillCfg<64>::smem(n_seqs) : hs::PrefillCfg<128>::smem(n_seqs)) <= hs::kPfMaxSmem;
-}
 
 int hs_kv4_prefill(hs::KvAttnArgs a, int dim, int sms, cudaStream_t s) {
     return dim == 64 ? hs::launch_prefill<64>(a, sms, s) : hs::launch_prefill<128>(a, sms, s);

@@ -60,7 +60,7 @@ __device__ __forceinline__ int kv_span_units(const KvAttnArgs& a, const KvSpan& 
 
 // Where a CTA's run of units stands; it always stands on a tile.
 struct KvWalk {
-    long long left;          // units of the CTA's run still to do (this one included)
+    uint32_t left;           // units of the CTA's run still to do (this one included)
     int seq, head, r, tile;  // tile: unit within the item
     int n, len, row0;        // of the request: new tokens, length, first row of q
     int units, tiles;        // of the item: with its pad, and without
@@ -70,9 +70,12 @@ struct KvWalk {
 
 // The lengths the schedule goes by: a length is cut to the table's width, and
 // a count of new tokens that q_start does not ascend by is 0.
+__device__ __forceinline__ int kv_start(const KvAttnArgs& a, const int* qs, int i) {
+    return min(max(qs[i], 0), a.n_tokens);  // no row outside q, whatever the device holds
+}
 __device__ __forceinline__ void kv_request(const KvAttnArgs& a, const int* qs, const int* ls, int i, int& n, int& len) {
-    n = max(qs[i + 1] - qs[i], 0);
-    len = (int)min((long long)max(ls[i], 0), (long long)a.width << a.g.page_log2);
+    n = max(kv_start(a, qs, i + 1) - kv_start(a, qs, i), 0);
+    len = min(max(ls[i], 0), a.width << a.g.page_log2);  // (the host has checked that product)
 }
 
 // Key tiles of a request, over its row tiles (whole warps; every lane gets it).
@@ -83,31 +86,26 @@ __device__ __forceinline__ int kv_many_units(const KvAttnArgs& a, int n, int len
     return (int)warp_add_u32((uint32_t)s);
 }
 
-__device__ __forceinline__ long long warp_scan(long long v) {
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(~0u, v, o);
+        const uint32_t t = __shfl_up_sync(~0u, v, o);
         if (lane >= o) v += t;
     }
     return v;
 }
 
-// Fills cum[0..n_seqs] (units before each request), qs[0..n_seqs] and
-// ls[0..n_seqs) in shared memory, by all threads of the CTA.
-__device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* ls, long long* cum) {
+// Fills cum[0..n_seqs] (units before each request) in shared memory, by all
+// threads of the CTA.  qs and ls: the requests' starts and lengths.
+__device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, const int* qs, const int* ls, uint32_t* cum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
-    for (int i = tid; i <= a.n_seqs; i += nt) {
-        qs[i] = min(max(a.q_start[i], 0), a.n_tokens);  // no row outside q, whatever the device holds
-        if (i < a.n_seqs) ls[i] = a.seq_len[i];
-    }
-    __syncthreads();
     bool many = false;  // some request has more than one row tile
     for (int i = tid; i < a.n_seqs; i += nt) {
         int n, len;
         kv_request(a, qs, ls, i, n, len);
         if (n <= a.tq)
-            cum[i + 1] = n ? (long long)a.g.heads * kv_span_units(a, kv_span(a, n, len, 0)) : 0;
+            cum[i + 1] = n ? (uint32_t)a.g.heads * (uint32_t)kv_span_units(a, kv_span(a, n, len, 0)) : 0;
         else
             many = true;
     }
@@ -117,15 +115,15 @@ __device__ __forceinline__ void kv_schedule(const KvAttnArgs& a, int* qs, int* l
             kv_request(a, qs, ls, i, n, len);
             if (n <= a.tq) continue;
             const int s = kv_many_units(a, n, len);
-            if (lane == 0) cum[i + 1] = (long long)a.g.heads * s;
+            if (lane == 0) cum[i + 1] = (uint32_t)a.g.heads * (uint32_t)s;
         }
         __syncthreads();
     }
     if (warp == 0) {
-        long long base = 0;
+        uint32_t base = 0;
         for (int i0 = 0; i0 < a.n_seqs; i0 += 32) {
             const int i = i0 + lane;
-            const long long v = warp_scan(i < a.n_seqs ? cum[i + 1] : 0);
+            const uint32_t v = warp_scan(i < a.n_seqs ? cum[i + 1] : 0u);
             if (i < a.n_seqs) cum[i + 1] = base + v;
             base += __shfl_sync(~0u, v, 31);
         }
@@ -139,26 +137,20 @@ __device__ __forceinline__ void kv_set_item(const KvAttnArgs& a, KvWalk& w) {
     w.lo = s.lo, w.hi = s.hi, w.tiles = kv_span_tiles(s), w.units = w.tiles + a.pad;
 }
 
-// Quotient of numbers that are not negative; nearly always both fit 32 bits.
-__device__ __forceinline__ long long kv_div(long long x, long long y) {
-    return ((x | y) >> 32) ? x / y : (long long)((uint32_t)x / (uint32_t)y);
-}
-
 // The cut of the line: the first `more` of `active` CTAs take q + 1 units, the others q.
 struct KvCut {
-    long long q;
-    int active, more;
-    __device__ __forceinline__ long long at(int c) const { return q * c + min(c, more); }
-    __device__ __forceinline__ int cta_of(long long unit) const {
-        const long long wide = (q + 1) * more;
-        return unit < wide ? (int)kv_div(unit, q + 1) : more + (int)kv_div(unit - wide, q);
+    uint32_t q, active, more;
+    __device__ __forceinline__ uint32_t at(uint32_t c) const { return q * c + min(c, more); }
+    __device__ __forceinline__ int cta_of(uint32_t unit) const {
+        const uint32_t wide = (q + 1) * more;
+        return (int)(unit < wide ? unit / (q + 1) : more + (unit - wide) / q);
     }
 };
-__device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, long long total) {
+__device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, uint32_t total) {
     KvCut c;
-    c.active = (int)max(1ll, min((long long)gridDim.x, kv_div(total + a.min_units - 1, a.min_units)));
-    c.q = kv_div(total, c.active);
-    c.more = (int)(total - c.q * c.active);
+    c.active = max(1u, min(gridDim.x, total / (uint32_t)a.min_units));
+    c.q = total / c.active;
+    c.more = total - c.q * c.active;
     return c;
 }
 
@@ -174,16 +166,16 @@ __device__ __forceinline__ void kv_next_item(const KvAttnArgs& a, const int* qs,
                 ++w.seq;
                 kv_request(a, qs, ls, w.seq, w.n, w.len);
             } while (!w.n);
-            w.row0 = qs[w.seq];
+            w.row0 = kv_start(a, qs, w.seq);
         }
     }
     kv_set_item(a, w);
 }
 
 // The tiles of the run's current item that are its own, and the units they end with.
-__device__ __forceinline__ int kv_piece_tiles(const KvWalk& w) { return (int)min(w.left, (long long)(w.tiles - w.tile)); }
+__device__ __forceinline__ int kv_piece_tiles(const KvWalk& w) { return (int)min(w.left, (uint32_t)(w.tiles - w.tile)); }
 // Takes `units` units off the run, which end the current item or the run.
-__device__ __forceinline__ void kv_skip(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w, long long units) {
+__device__ __forceinline__ void kv_skip(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w, uint32_t units) {
     w.left -= min(w.left, units);
     if (w.left > 0) kv_next_item(a, qs, ls, w);
 }
@@ -192,13 +184,13 @@ __device__ __forceinline__ void kv_next_piece(const KvAttnArgs& a, const int* qs
 }
 
 // Start of this CTA's run (called by whole warps; every lane gets the same).
-__device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const long long* cum) {
+__device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const uint32_t* cum) {
     KvWalk w;
-    const long long total = cum[a.n_seqs];
+    const uint32_t total = cum[a.n_seqs];
     const KvCut cut = kv_cut(a, total);
     w.left = 0;
-    if (!total || (int)blockIdx.x >= cut.active) return w;
-    const long long u0 = cut.at(blockIdx.x);
+    if (!total || blockIdx.x >= cut.active) return w;
+    const uint32_t u0 = cut.at(blockIdx.x);
     w.left = cut.at(blockIdx.x + 1) - u0;
     int lo = 0, hi = a.n_seqs;
     while (hi - lo > 1) {  // the last request with cum <= u0: it has units
@@ -208,23 +200,18 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
     }
     w.seq = lo;
     kv_request(a, qs, ls, lo, w.n, w.len);
-    w.row0 = qs[lo];
-    const long long per_head = kv_div(cum[lo + 1] - cum[lo], a.g.heads);
-    long long rest = u0 - cum[lo];
-    w.head = (int)kv_div(rest, per_head);
-    rest -= (long long)w.head * per_head;
+    w.row0 = kv_start(a, qs, lo);
+    const uint32_t per_head = (cum[lo + 1] - cum[lo]) / (uint32_t)a.g.heads;
+    uint32_t rest = u0 - cum[lo];
+    w.head = (int)(rest / per_head);
+    rest -= (uint32_t)w.head * per_head;
     const int tiles = (w.n + a.tq - 1) / a.tq;
     w.r = 0;
     if (tiles > 1) {
         const int lane = threadIdx.x & 31;
         for (int r0 = 0; r0 < tiles; r0 += 32) {
-            const int mine = r0 + lane < tiles ? kv_span_units(a, kv_span(a, w.n, w.len, r0 + lane)) : 0;
-            int incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(~0u, incl, o);
-                if (lane >= o) incl += t;
-            }
+            const uint32_t mine = r0 + lane < tiles ? (uint32_t)kv_span_units(a, kv_span(a, w.n, w.len, r0 + lane)) : 0u;
+            const uint32_t incl = warp_scan(mine);
             const unsigned past = __ballot_sync(~0u, mine && incl > rest);
             if (past) {
                 const int l = __ffs(past) - 1;
@@ -242,10 +229,16 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
     return w;
 }
 
+// Whether the line of a call with these row and key tiles stays below 2^32 units.
+inline bool kv_line_ok(const KvAttnArgs& a) {
+    const double row_tiles = (double)(a.n_tokens / a.tq) + a.n_seqs;
+    const double units = (double)((((long long)a.width << a.g.page_log2) >> a.tile_log2) + 2 + a.pad);
+    return row_tiles * units * a.g.heads < 4294967296.0;
+}
+
 }  // namespace hs
 
 // The tensor-core kernel for chunks (hs_kv4_prefill.cu).
-bool hs_kv4_prefill_fits(int dim, int n_seqs);
 int hs_kv4_prefill(hs::KvAttnArgs a, int dim, int sms, cudaStream_t stream);
 // Reads and clears its device error word.
 unsigned hs_kv4_prefill_take_status();
