@@ -58,7 +58,7 @@ struct DecodeCfg {
     static constexpr int kLine = D + 4;               // floats of a row of the warps' sums (padded against bank conflicts)
     static constexpr int kMergeBytes = kWarps * 8 * NQ * (kLine + 2) * 4;
     static constexpr int kRows = 8 * NQ * RT;
-    static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (3 * n_seqs + 2) * 4 + 16; }
+    static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (n_seqs <= kKvFew ? 0 : n_seqs + 1) * 4; }
 };
 
 // Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 32-key steps
@@ -86,8 +86,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     float2* merge_ml = reinterpret_cast<float2*>(merge + C::kWarps * 8 * NQ * C::kLine);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRingBytes + C::kMergeBytes);
     uint32_t* cum = reinterpret_cast<uint32_t*>(bars + 32);
-    int* qs = reinterpret_cast<int*>(cum + a.n_seqs + 1);
-    int* ls = qs + a.n_seqs + 1;
+    const int *qs = a.q_start, *ls = a.seq_len;  // looked at once an item
     // Where a warp computes and where it loads, a copy a warp in shared memory
     // (every lane writes the same): looked at once an item, and registers are short.
     __shared__ KvWalk walks[C::kWarps], ahead[C::kWarps];
@@ -102,14 +101,17 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     }
     pdl_wait();
     pdl_trigger();
-    for (int i = tid; i <= a.n_seqs; i += C::kThreads) {  // at hand in shared memory
-        qs[i] = a.q_start[i];
-        if (i < a.n_seqs) ls[i] = a.seq_len[i];
-    }
-    __syncthreads();
-    kv_schedule(a, qs, ls, cum);
     KvWalk& w = walks[warp];
-    w = ahead[warp] = kv_begin(a, qs, ls, cum);
+    uint32_t total;
+    if (a.n_seqs <= kKvFew) {
+        __syncthreads();  // the barriers are ready
+        w = kv_begin_few(a, total);
+    } else {
+        kv_schedule(a, qs, ls, cum);
+        w = kv_begin(a, qs, ls, cum);
+        total = cum[a.n_seqs];
+    }
+    ahead[warp] = w;
     __syncwarp();
     const int P = 1 << a.g.page_log2;
 
@@ -517,7 +519,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, cum[a.n_seqs], &join_last, add_pieces<D, C::kWarps>);
+        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, total, &join_last, add_pieces<D, C::kWarps>);
         KvWalk n = w;
         kv_next_piece(a, qs, ls, n);
         __syncwarp();

@@ -183,26 +183,15 @@ __device__ __forceinline__ void kv_next_piece(const KvAttnArgs& a, const int* qs
     kv_skip(a, qs, ls, w, w.units - w.tile);
 }
 
-// Start of this CTA's run (called by whole warps; every lane gets the same).
-__device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const uint32_t* cum) {
-    KvWalk w;
-    const uint32_t total = cum[a.n_seqs];
-    const KvCut cut = kv_cut(a, total);
-    w.left = 0;
-    if (!total || blockIdx.x >= cut.active) return w;
-    const uint32_t u0 = cut.at(blockIdx.x);
-    w.left = cut.at(blockIdx.x + 1) - u0;
-    int lo = 0, hi = a.n_seqs;
-    while (hi - lo > 1) {  // the last request with cum <= u0: it has units
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= u0) lo = mid;
-        else hi = mid;
-    }
+// Puts w at this CTA's first unit, which lies in request lo, whose units run
+// from `before` to `after` (called by whole warps).
+__device__ __forceinline__ void kv_place_run(const KvAttnArgs& a, const int* qs, const int* ls, KvWalk& w, uint32_t cut_at, int lo,
+                                             uint32_t before, uint32_t after) {
     w.seq = lo;
     kv_request(a, qs, ls, lo, w.n, w.len);
     w.row0 = kv_start(a, qs, lo);
-    const uint32_t per_head = (cum[lo + 1] - cum[lo]) / (uint32_t)a.g.heads;
-    uint32_t rest = u0 - cum[lo];
+    const uint32_t per_head = (after - before) / (uint32_t)a.g.heads;
+    uint32_t rest = cut_at - before;
     w.head = (int)(rest / per_head);
     rest -= (uint32_t)w.head * per_head;
     const int tiles = (w.n + a.tq - 1) / a.tq;
@@ -226,6 +215,70 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
     w.first = true;
     kv_set_item(a, w);
     if (w.tile >= w.tiles) kv_skip(a, qs, ls, w, w.units - w.tile);  // the run begins in a pad
+}
+
+// Start of this CTA's run (called by whole warps; every lane gets the same).
+__device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const uint32_t* cum) {
+    KvWalk w;
+    const uint32_t total = cum[a.n_seqs];
+    const KvCut cut = kv_cut(a, total);
+    w.left = 0;
+    if (!total || blockIdx.x >= cut.active) return w;
+    const uint32_t u0 = cut.at(blockIdx.x);
+    w.left = cut.at(blockIdx.x + 1) - u0;
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {  // the last request with cum <= u0: it has units
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= u0) lo = mid;
+        else hi = mid;
+    }
+    kv_place_run(a, qs, ls, w, u0, lo, cum[lo], cum[lo + 1]);
+    return w;
+}
+
+// The same by one warp alone, for at most 128 requests: four a lane at most,
+// and neither the CTA's other warps nor shared memory are waited for.
+__device__ __forceinline__ KvWalk kv_begin_few(const KvAttnArgs& a, uint32_t& total) {
+    const int lane = threadIdx.x & 31, per = (a.n_seqs + 31) >> 5;
+    uint32_t mine = 0, units[4];
+    int start[5], len[4];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) start[j] = j <= per && lane * per + j <= a.n_seqs ? a.q_start[lane * per + j] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) len[j] = j < per && lane * per + j < a.n_seqs ? a.seq_len[lane * per + j] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        units[j] = 0;
+        if (j >= per) break;
+        const bool in = lane * per + j < a.n_seqs;
+        const int n = in ? max(min(max(start[j + 1], 0), a.n_tokens) - min(max(start[j], 0), a.n_tokens), 0) : 0;
+        const int l = min(max(len[j], 0), a.width << a.g.page_log2);
+        if (n && n <= a.tq) units[j] = (uint32_t)a.g.heads * (uint32_t)kv_span_units(a, kv_span(a, n, l, 0));
+        for (unsigned many = __ballot_sync(~0u, n > a.tq); many; many &= many - 1) {
+            const int x = __ffs(many) - 1;
+            const uint32_t u = (uint32_t)a.g.heads * (uint32_t)kv_many_units(a, __shfl_sync(~0u, n, x), __shfl_sync(~0u, l, x));
+            if (lane == x) units[j] = u;
+        }
+        mine += units[j];
+    }
+    const uint32_t incl = warp_scan(mine);
+    total = __shfl_sync(~0u, incl, 31);
+    KvWalk w;
+    const KvCut cut = kv_cut(a, total);
+    w.left = 0;
+    if (!total || blockIdx.x >= cut.active) return w;
+    const uint32_t u0 = cut.at(blockIdx.x);
+    w.left = cut.at(blockIdx.x + 1) - u0;
+    const int x = __ffs(__ballot_sync(~0u, incl > u0)) - 1;  // the lane whose requests the run begins in
+    uint32_t before = __shfl_sync(~0u, incl - mine, x);
+    int seq = x * per;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t u = __shfl_sync(~0u, units[j], x);
+        if (j < per - 1 && before + u <= u0 && seq == x * per + j) before += u, ++seq;
+        if (seq == x * per + j) mine = u;
+    }
+    kv_place_run(a, a.q_start, a.seq_len, w, u0, seq, before, before + mine);
     return w;
 }
 
@@ -235,6 +288,8 @@ inline bool kv_line_ok(const KvAttnArgs& a) {
     const double units = (double)((((long long)a.width << a.g.page_log2) >> a.tile_log2) + 2 + a.pad);
     return row_tiles * units * a.g.heads < 4294967296.0;
 }
+
+constexpr int kKvFew = 128;  // requests that kv_begin_few takes
 
 }  // namespace hs
 

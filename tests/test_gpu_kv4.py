@@ -234,6 +234,19 @@ def test_attention(case, window):
     _close(out, r.expected(scale, window), scale)
 
 
+@pytest.mark.parametrize("n", [32, 33, 64, 100, 127, 128, 129, 300])
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_of_many_requests(n, new):
+    """The division of the work over one to four requests a lane and over more, some
+    requests without new tokens, some with many."""
+    rng = np.random.default_rng(n)
+    fresh = [int(x) for x in rng.integers(0, new + 1, n)]
+    fresh[n // 2] = 70 if new > 1 else 1
+    cached = [int(x) for x in rng.integers(0, 90, n)]
+    r = _kv4.Requests(n, cached, fresh, 4, 2, 64, 16)
+    _close(r.run(hs, 0.2), r.expected(0.2), 0.2)
+
+
 @pytest.mark.parametrize("new", [1, 5, 100])
 def test_attention_rows_and_pages_that_are_not_there(new):
     """Missing pages drop out of the softmax, a request of absent pages gives
