@@ -27,7 +27,7 @@ namespace hs {
 constexpr int kPfKeys = 128, kPfRows = 256, kPfPacked = 3, kPfSlots = 3, kPfInfo = 8;
 constexpr int kPfThreads = 16 * 32;
 constexpr int kPfApart = 6;  // warps that take codes apart
-constexpr int kPfMaxSmem = 227 * 1024 - 1024;  // dynamic; the rest is the static part
+constexpr int kPfMaxSmem = 227 * 1024 - 2048;  // dynamic; the rest is the static part
 constexpr float kPfUp = 6.f;  // probabilities are held times 2^6: at most 2^14 in fp16, and small ones keep their bits
 
 template <int D>
@@ -36,7 +36,7 @@ struct PrefillCfg {
     static constexpr int kQBytes = 128 * D * 2;          // of a row tile
     static constexpr int kTileBytes = kPfKeys * D * 2;   // a K or V tile
     static constexpr int kPackedBytes = kPfKeys * (D / 2 + 4 * kNg);
-    static constexpr int kFixed = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes;
+    static constexpr int kFixed = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes + 8 * 2048;
     static constexpr int smem(int n_seqs) { return 1024 + kFixed + 1024 + (n_seqs + 1) * 4; }
 };
 
@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     uint8_t* q_s = smem;                                    // [2] row tiles
     uint8_t* kv_s = smem + 2 * C::kQBytes;                  // [kPfSlots] K and V tiles in turn
     uint8_t* packed_s = kv_s + kPfSlots * C::kTileBytes;    // [kPfPacked] codes, pairs
-    PfShared& sh = *reinterpret_cast<PfShared*>(packed_s + kPfPacked * C::kPackedBytes);
+    uint8_t* out_s = packed_s + kPfPacked * C::kPackedBytes;  // [8] warps' buffers of 32 rows of 64 bytes
+    PfShared& sh = *reinterpret_cast<PfShared*>(out_s + 8 * 2048);
     static_assert(sizeof(PfShared) <= 1024, "barriers");
-    uint32_t* cum = reinterpret_cast<uint32_t*>(packed_s + kPfPacked * C::kPackedBytes + 1024);
+    uint32_t* cum = reinterpret_cast<uint32_t*>(out_s + 8 * 2048 + 1024);
     const int *qs = a.q_start, *ls = a.seq_len;  // looked at once an item: no room here for 4096 requests' copies
     // (Reductions of values that all lanes share: they come out in uniform registers,
     // which the tensor-core instructions' operands have to be in.)
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
     tc_fence_after();
     const uint32_t tmem = warp_max_u32(sh.tmem);  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
     // A warp's place in the line, in shared memory: looked at once an item.
-    __shared__ KvWalk walks[kPfThreads / 32];
+    __shared__ KvWalk walks[kPfThreads / 32], coming[8];
     KvWalk& w = walks[warp];
     if (warp == 0) walks[0] = kv_begin(a, qs, ls, cum);
     __syncthreads();
@@ -216,8 +217,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             uint32_t v_slot = 0, v_phase = 0;  // of the V tile before
             for (int k = 0; k <= cnt && !dead; ++k) {
                 // tile k's scores and tile k - 1's outputs, a row tile at a time
-                if (k < cnt) wait(sh.kv_full + slot, phase);
-                if (k && !dead) wait(sh.kv_full + v_slot, v_phase);
+                if (k) wait(sh.kv_full + v_slot, v_phase);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if ((x && !two) || dead) continue;
@@ -229,10 +229,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         q_phase[x] ^= 1;
                     }
                     if (dead) continue;
-                    tc_fence_after();
                     const bool last = x || !two;
-                    if (elect_one()) {
-                        if (k) {  // O += P V
+                    if (k) {  // O += P V
+                        tc_fence_after();
+                        if (elect_one()) {
                             const uint64_t vd = umma_desc_sw128_mn(kv_at + v_slot * C::kTileBytes, kPfKeys * 128);
 #pragma unroll
                             for (int kk = 0; kk < kPfKeys / 16; ++kk)
@@ -240,7 +240,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                             if (k == cnt) umma_commit(sh.o_full + x);
                             if (last) umma_commit(sh.kv_empty + v_slot);
                         }
-                        if (k < cnt) {  // S = Q K^T
+                        __syncwarp();
+                    }
+                    if (k < cnt) {  // S = Q K^T; the tile of K has had the outputs' time to come
+                        if (!x) wait(sh.kv_full + slot, phase);
+                        if (dead) continue;
+                        tc_fence_after();
+                        if (elect_one()) {
                             const uint64_t qd = umma_desc_sw128(q_at + x * C::kQBytes), kd = umma_desc_sw128(kv_at + slot * C::kTileBytes);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
@@ -350,57 +356,86 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         const int back_keys = a.window ? a.window - 1 : 0x3fffffff;
         uint32_t tiles = 0, s_count = 0, o_count = 0;
         bool dead = false;
+        // The warp's 32 rows of a piece's queries, a row by D / 8 lanes: fetched as they are
+        // into the lines of the tile that they will fill (16-byte chunk c of a row at place c
+        // of its line), ...
+        constexpr int kL = D / 8, kAt = 32 / kL, kB = 32 / kAt;  // lanes a row, rows at a time
+        const int sub = lane / kL, c = lane % kL;
+        uint8_t* q_lines = q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + ((warp & 3) * 32 + sub) * 128;
+        auto fetch_q = [&](const KvWalk& v) {
+            const int nr = rows_of(v);
+#pragma unroll 4
+            for (int i = 0; i < kB; ++i) {
+                const int qr = x * 128 + (warp & 3) * 32 + i * kAt + sub, qt = kv_row_token(a, qr);
+                uint8_t* dst = q_lines + i * kAt * 128 + (c & 7) * 16;
+                if (qr < nr)
+                    cp_async16_hint(dst, a.q + (long long)(v.row0 + v.r * a.tq + qt) * a.q_st +
+                                             (long long)(v.head * a.group + qr - qt * a.group) * a.q_sh + c * 8, policy_evict_first());
+                else
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+            }
+        };
+        // ... then put into fp16 in place, all scaled by the power of two that brings their
+        // largest channel to [2^8, 2^9): bf16 values down to 2^-22 of it stay exact, smaller
+        // ones move a score by less than 2^-33 of the largest.  Returns the scores' factor.
+        auto convert_q = [&]() -> float {
+            cp_async_wait_all();
+            __syncwarp();
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int i = 0; i < kB; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(q_lines + i * kAt * 128 + (c & 7) * 16);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
+            }
+            int e = (int)(warp_max_u32(top) >> 23);  // zeros and infinities keep the scale 1
+            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
+            const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+#pragma unroll 4
+            for (int i = 0; i < kB; ++i) {
+                uint8_t* line = q_lines + i * kAt * 128;
+                const uint4 v = *reinterpret_cast<const uint4*>(line + (c & 7) * 16);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // channels j and j + 4
+                    const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
+                    h[j] = as_u32(__floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
+                                                    __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f));
+                }
+                __syncwarp();  // the line has been read
+                *reinterpret_cast<uint4*>(line + (((c & 7) ^ ((i * kAt + sub) & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.q_full + x);
+            return a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+        };
+        float sc = 0.f;
+        if (w.left > 0 && x * 128 < rows_of(w)) {
+            fetch_q(w);
+            sc = convert_q();
+        }
         while (w.left > 0) {
             const int cnt = kv_piece_tiles(w), nrows = rows_of(w), ctx = w.len - w.n;
             const bool whole = cnt == w.tiles;
+            KvWalk& nx = coming[warp];  // the piece after this one
+            {
+                KvWalk n = w;
+                kv_next_piece(a, qs, ls, n);
+                __syncwarp();
+                nx = n;
+                __syncwarp();
+            }
+            const bool more = nx.left > 0 && x * 128 < rows_of(nx);
+            if (x * 128 >= nrows && more) {  // this row tile has been idle
+                fetch_q(nx);
+                sc = convert_q();
+            }
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
                 const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
-                float sc;
-                {
-                    // The warp's 32 rows in fp16, a row by D / 8 lanes, all scaled by the power of
-                    // two that brings their largest channel to [2^8, 2^9): bf16 values down to
-                    // 2^-22 of it stay exact, smaller ones move a score by less than 2^-33 of the largest.
-                    constexpr int kL = D / 8, kAt = 32 / kL, kB = 32 / kAt;  // lanes a row, rows at a time, all in flight
-                    const int sub = lane / kL, c = lane % kL;
-                    uint4 v[kB];
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < kB; ++i) {
-                        const int qr = x * 128 + (warp & 3) * 32 + i * kAt + sub, qt = kv_row_token(a, qr);
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (qr < nrows)
-                            v[i] = *reinterpret_cast<const uint4*>(a.q + (long long)(w.row0 + w.r * a.tq + qt) * a.q_st +
-                                                                   (long long)(w.head * a.group + qr - qt * a.group) * a.q_sh + c * 8);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kB; ++i) {
-                        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
-                    }
-                    int e = (int)(warp_max_u32(top) >> 23);  // zeros and infinities keep the scale 1
-                    e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
-                    const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-                    sc = a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
-#pragma unroll
-                    for (int i = 0; i < kB; ++i) {
-                        const int qr = (warp & 3) * 32 + i * kAt + sub;
-                        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t h[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // channels j and j + 4
-                            const uint32_t lo = u[j >> 1], hi = u[2 + (j >> 1)];
-                            h[j] = as_u32(__floats2half2_rn(__uint_as_float(j & 1 ? lo & 0xffff0000u : lo << 16) * f,
-                                                            __uint_as_float(j & 1 ? hi & 0xffff0000u : hi << 16) * f));
-                        }
-                        *reinterpret_cast<uint4*>(q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sh.q_full + x);
                 const int min_lim = -warp_max_s32(valid ? -lim : -0x7fffffff), max_lim = warp_max_s32(valid ? lim : -1);
 
                 float m = -1e30f, l = 0.f;
@@ -421,6 +456,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         break;
                     }
                     tc_fence_after();
+                    if (k == cnt - 1 && more) fetch_q(nx);  // the last scores are there: the queries' place is free
                     if (k) see_nan(k - 1);  // its values have been taken apart: its product is done
                     const uint32_t gone = sh.gone[(tiles + k) % kPfInfo];
                     const bool masked = gone || key0 + kPfKeys - 1 > min_lim || key0 < max_lim - back_keys;
@@ -477,65 +513,80 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.p_full + x);
                 }
+                // The next piece's first scores are worked out while this one is written.
+                const float next_sc = more ? convert_q() : 0.f;
                 if (!dead && !mbar_wait(sh.o_full + x, o_count++ & 1)) dead = true;
                 if (!dead) {
                     tc_fence_after();
                     see_nan(cnt - 1);
                     const float inv = l != 0.f ? 1.f / l : 0.f;
                     const size_t at = (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * a.rows + r;
+                    // 64 bytes of each of the warp's rows at a time, by way of a buffer (chunk j of
+                    // row i at j ^ (i / 2 % 4): no two in one bank), so that four lanes write a row's
+                    // 64 bytes together: a thread writing its own row took the load-store unit 4000
+                    // cycles a piece.
+                    uint8_t* buf = out_s + warp * 2048;
+                    auto write64 = [&](const uint4 (&u)[4], uint8_t* base, bool part, int d) {
+                        __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
+                        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = u[j];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int orow = i * 8 + (lane >> 2), qr = x * 128 + (warp & 3) * 32 + orow, qt = kv_row_token(a, qr);
+                            const uint4 z = *reinterpret_cast<const uint4*>(buf + orow * 64 + (((lane & 3) ^ (orow >> 1 & 3)) << 4));
+                            if (qr >= nrows) continue;
+                            uint8_t* dst = part ? base + ((at - r + qr) * D + d) * 4
+                                                : base + ((long long)qt * a.o_st + (long long)(qr - qt * a.group) * a.o_sh + d) * 2;
+                            *reinterpret_cast<uint4*>(dst + (lane & 3) * 16) = z;
+                        }
+                    };
+                    uint8_t* out0 = reinterpret_cast<uint8_t*>(a.out + (long long)(w.row0 + w.r * a.tq) * a.o_st + (long long)w.head * a.group * a.o_sh);
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
                         float v[32];
-                        tmem_ld32(tl + 256 + x * 128 + c * 32, v);
-                        if ((nan >> (c >> 1)) & 1u) {
+                        tmem_ld32(tl + 256 + x * 128 + d, v);
+                        if ((nan >> (d >> 6)) & 1u) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7fc00000u);
                         }
-                        if (whole) {  // by way of the queries' place, which is free
-                            uint8_t* line = q_s + x * C::kQBytes + row * (2 * D);
+                        uint4 u[4];
+                        if (whole) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                uint32_t u[4];
+                                uint32_t z[4];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const int from = 8 * j + (i & 1) * 4 + (i >> 1);  // channels 2i and 2i + 1 of eight
-                                    const __nv_bfloat162 z = __floats2bfloat162_rn(v[from] * inv, v[from + 2] * inv);
-                                    u[i] = *reinterpret_cast<const uint32_t*>(&z);
+                                    const __nv_bfloat162 y = __floats2bfloat162_rn(v[from] * inv, v[from + 2] * inv);
+                                    z[i] = *reinterpret_cast<const uint32_t*>(&y);
                                 }
-                                *reinterpret_cast<uint4*>(line + (((c * 4 + j) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                                u[j] = make_uint4(z[0], z[1], z[2], z[3]);
                             }
-                        } else if (valid) {
-                            float* dst = a.part_o + at * D + c * 32;
+                            write64(u, out0, false, d);
+                        } else {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
+                            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    *reinterpret_cast<float4*>(dst + j * 8 + i * 4) =
-                                        make_float4(v[8 * j + i], v[8 * j + 2 + i], v[8 * j + 4 + i], v[8 * j + 6 + i]);
+                                for (int j = 0; j < 4; ++j) {
+                                    const int from = 16 * h + 8 * (j >> 1) + (j & 1);  // channels 0-3 or 4-7 of eight
+                                    u[j] = make_uint4(__float_as_uint(v[from]), __float_as_uint(v[from + 2]), __float_as_uint(v[from + 4]),
+                                                      __float_as_uint(v[from + 6]));
+                                }
+                                write64(u, reinterpret_cast<uint8_t*>(a.part_o), true, d + 16 * h);
+                            }
                         }
                     }
-                    if (whole) {
-                        constexpr int kL = D / 8, kAt = 32 / kL;
-                        const int sub = lane / kL, c = lane % kL;
-                        __syncwarp();
-#pragma unroll 4
-                        for (int i = 0; i < 32 / kAt; ++i) {
-                            const int orow = (warp & 3) * 32 + i * kAt + sub, qr = x * 128 + orow, qt = kv_row_token(a, qr);
-                            const uint4 u = *reinterpret_cast<const uint4*>(q_s + x * C::kQBytes + orow * (2 * D) + ((c ^ (orow & 7)) << 4));
-                            if (qr < nrows)
-                                *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + qt) * a.o_st +
-                                                          (long long)(w.head * a.group + qr - qt * a.group) * a.o_sh + c * 8) = u;
-                        }
-                        __syncwarp();
-                    } else if (valid) {
-                        a.part_ml[at] = make_float2(m, l);
-                    }
+                    if (valid && !whole) a.part_ml[at] = make_float2(m, l);
                     tc_fence_before();
                 }
+                sc = next_sc;
             }
             tiles += cnt;
             if (!whole) join_pieces<8, 1>(a, w, warp, cum[a.n_seqs], &sh.join_last, add_pieces_apart<D>);
-            next_piece();
+            __syncwarp();
+            w = nx;
+            __syncwarp();
         }
     }
     tc_fence_before();
