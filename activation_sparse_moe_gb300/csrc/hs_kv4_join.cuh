@@ -64,49 +64,54 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
                     acc[x][e] = f0 * reinterpret_cast<const float*>(&v[0][x])[e] + f1 * reinterpret_cast<const float*>(&v[1][x])[e];
             }
         } else {
-        float wt[ROWS][2];
-#pragma unroll
-        for (int x = 0; x < ROWS; ++x) {
-            row[x] = min(r0 + x * WARPS, rows - 1);
-            float2 ml[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                ml[y] = lane + 32 * y < count ? __ldcg(a.part_ml + piece_slot(c, first + (lane + 32 * y) * step) * a.rows + row[x])
-                                              : make_float2(-1e30f, 0.f);
-            m[x] = fmaxf(ml[0].x, ml[1].x);
-            wt[x][0] = ml[0].x, wt[x][1] = ml[1].x;
-            l[x] = ml[0].y, acc[x][0] = ml[1].y;
-        }
-#pragma unroll
-        for (int x = 0; x < ROWS; ++x) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
-            wt[x][0] = ex2(wt[x][0] - m[x]);
-            wt[x][1] = ex2(wt[x][1] - m[x]);
-            l[x] = wt[x][0] * l[x] + wt[x][1] * acc[x][0];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], o);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[x][e] = 0.f;
-        }
-        for (int i0 = 0; i0 < count; i0 += BATCH) {
+            // the first pieces' rows come along with all pieces' (maximum, sum)
+            float wt[ROWS][2];
             Vec v[BATCH][ROWS];
+            auto fetch = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const size_t at = piece_slot(c, first + min(i0 + i, count - 1) * step) * a.rows;
+                for (int i = 0; i < BATCH; ++i) {
+                    const size_t at = piece_slot(c, first + min(i0 + i, count - 1) * step) * a.rows;
 #pragma unroll
-                for (int x = 0; x < ROWS; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
-            }
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-                for (int x = 0; x < ROWS; ++x) {
-                    float f = __shfl_sync(~0u, i0 < 32 ? wt[x][0] : wt[x][1], (i0 + i) & 31);
-                    if (i0 + i >= count) f = 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) acc[x][e] = fmaf(f, reinterpret_cast<const float*>(&v[i][x])[e], acc[x][e]);
+                    for (int x = 0; x < ROWS; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
                 }
-        }
+            };
+#pragma unroll
+            for (int x = 0; x < ROWS; ++x) {
+                row[x] = min(r0 + x * WARPS, rows - 1);
+                float2 ml[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    ml[y] = lane + 32 * y < count ? __ldcg(a.part_ml + piece_slot(c, first + (lane + 32 * y) * step) * a.rows + row[x])
+                                                  : make_float2(-1e30f, 0.f);
+                m[x] = fmaxf(ml[0].x, ml[1].x);
+                wt[x][0] = ml[0].x, wt[x][1] = ml[1].x;
+                l[x] = ml[0].y, acc[x][0] = ml[1].y;
+            }
+            fetch(0);
+#pragma unroll
+            for (int x = 0; x < ROWS; ++x) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
+                wt[x][0] = ex2(wt[x][0] - m[x]);
+                wt[x][1] = ex2(wt[x][1] - m[x]);
+                l[x] = wt[x][0] * l[x] + wt[x][1] * acc[x][0];
+#pragma unroll
+                for (int o = 16; o; o >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], o);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[x][e] = 0.f;
+            }
+            for (int i0 = 0; i0 < count; i0 += BATCH) {
+                if (i0) fetch(i0);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                    for (int x = 0; x < ROWS; ++x) {
+                        float f = __shfl_sync(~0u, i0 + i < 32 ? wt[x][0] : wt[x][1], (i0 + i) & 31);
+                        if (i0 + i >= count) f = 0.f;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) acc[x][e] = fmaf(f, reinterpret_cast<const float*>(&v[i][x])[e], acc[x][e]);
+                    }
+            }
         }
 #pragma unroll
         for (int x = 0; x < ROWS; ++x) {
@@ -152,11 +157,11 @@ __device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w
     auto arrive = [&](int* counter, int of) -> bool {
         meet();  // the CTA's writes ...
         if (lead) {
-            __threadfence();  // ... are seen before its arrival
-            const bool is_last = atomicAdd(counter, 1) == of - 1;
-            if (is_last) *counter = 0;  // for the next call
-            *last = is_last;
-            __threadfence();
+            // ... are seen before its arrival, and the other CTAs' after the last one's
+            int before;
+            asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+            *last = before == of - 1;
+            if (before == of - 1) *counter = 0;  // for the next call
         }
         meet();
         return *last != 0;
