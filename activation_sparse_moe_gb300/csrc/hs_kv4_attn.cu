@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "hs_kv4_join.cuh"
+#include "hs_tc.cuh"
 
 namespace hs {
 
@@ -63,9 +64,8 @@ struct DecodeCfg {
 
 // Warp (rt, kw): rows 8 NQ rt and up of the item's row tile, the 32-key steps
 // kw, kw + KW, ... of the CTA's piece of it.  Every warp keeps its own ring of
-// steps full: four lanes (eight for pages of 16) issue one bulk copy each, of K
-// codes, V codes, K pairs and V pairs, as soon as the warp has used a slot up,
-// across the ends of items.  So the warps do not wait for one another until an
+// steps full: a lane issues the bulk copies of K codes, V codes, K pairs and V
+// pairs as soon as the warp has used a slot up, across the ends of items.  So the warps do not wait for one another until an
 // item ends (a ring shared by the CTA's warps held them in step: 30% of the
 // issue slots went into waiting).
 //
@@ -119,11 +119,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     uint8_t* ring = smem + warp * C::kSlots * C::kSlotBytes;
     uint64_t* full = bars + warp * C::kSlots;
     const int parts_log2 = a.g.page_log2 == 4 ? 1 : 0;  // pages of a step: two of 16, or one
-    // Lane: copy seg (K codes, V codes, K pairs, V pairs) of page `part` of a step.
-    const int part = lane >> 2 & parts_log2, seg = lane & 3, row_bytes = seg < 2 ? D / 2 : NG * 4;
-    const uint32_t copy_bytes = lane < 4 << parts_log2 ? (uint32_t)(row_bytes * (kKvStep >> parts_log2)) : 0;
-    const uint32_t dst = smem_u32(ring) + (seg < 2 ? seg * (kKvStep * D / 2) : kKvStep * (D + (seg - 2) * NG * 4)) + part * copy_bytes;
-    const uint8_t* src = nullptr;  // of this lane's copies in page 0
+    const uint8_t* src = nullptr;  // the head's record in page 0
     uint32_t gone = 0;             // two bits a slot: blocks of 16 keys that are not there
     int key = 0, key_end = 0;      // the next step's first key, and the end of the piece that is being loaded
     int seen = 0, held = -1;       // its steps so far; lane: a table entry of the coming ones
@@ -133,7 +129,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         key_end = key + kv_piece_tiles(v) * kKvTile;
         key += kw * kKvStep;
         seen = 0;
-        src = kv_record(a.g, 0, v.head) + ((seg < 2 ? seg * (D / 2) : D + (seg - 2) * NG * 4) << a.g.page_log2);
+        src = kv_record(a.g, 0, v.head);
     };
     if (w.left > 0) piece_to_load(w);
     auto load = [&]() {
@@ -155,19 +151,27 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             const int k = key + (lane >> parts_log2) * KW * kKvStep + ((lane << 4) & (parts_log2 << 4));
             held = v.hi >= v.lo && k < v.len ? a.table[(size_t)v.seq * a.width + (k >> a.g.page_log2)] : -1;
         }
-        const int page = __shfl_sync(~0u, held, at + part);
-        const bool here = copy_bytes && (uint32_t)page < (uint32_t)a.g.n_pages;
-        const unsigned mask = __ballot_sync(~0u, here);
-        const unsigned all = parts_log2 ? 0xffu : 0xfu;
-        gone &= ~(3u << (2 * in_slot));
-        if (mask != all) gone |= ((mask & 1u ? 0u : parts_log2 ? 1u : 3u) | (parts_log2 && !(mask & 16u) ? 2u : 0u)) << (2 * in_slot);
-        if (lane == 0)
-            mbar_arrive_expect_tx(full + in_slot, (uint32_t)(__popc(mask) >> 2) * (uint32_t)((kKvStep >> parts_log2) * (D + D / 8)));
+        // Two pages of 16 tokens, or (part of) one: K codes, V codes, K pairs and V pairs
+        // by a copy each, issued by one lane.
+        const int page0 = __shfl_sync(~0u, held, at), page1 = __shfl_sync(~0u, held, at + parts_log2);
+        const bool here0 = (uint32_t)page0 < (uint32_t)a.g.n_pages, here1 = (uint32_t)page1 < (uint32_t)a.g.n_pages;
+        gone = (gone & ~(3u << (2 * in_slot))) | ((here0 ? 0u : 1u) | (here1 ? 0u : 2u)) << (2 * in_slot);
+        if (elect_one()) {
+            const uint32_t tokens = kKvStep >> parts_log2, bar = smem_u32(full + in_slot), dst = smem_u32(ring) + in_slot * C::kSlotBytes;
+            mbar_arrive_expect_tx(full + in_slot, (here0 ? tokens : 0u) * (D + D / 8) + (parts_log2 && here1 ? tokens : 0u) * (D + D / 8));
+            const uint64_t policy = policy_evict_first();
+            auto copy_page = [&](int page, uint32_t to) {  // to: the step's token that its tokens start at
+                const uint8_t* rec = src + (size_t)(uint32_t)page * (uint32_t)(a.g.heads * a.g.rec);
+                const uint32_t from = key & (P - 1) & ~15u & (parts_log2 ? 0u : ~0u);
+                bulk_g2s_to(dst + to * (D / 2), rec + from * (D / 2), tokens * (D / 2), bar, policy);
+                bulk_g2s_to(dst + (kKvStep + to) * (D / 2), rec + (P + from) * (D / 2), tokens * (D / 2), bar, policy);
+                bulk_g2s_to(dst + kKvStep * D + to * (NG * 4), rec + P * D + from * (NG * 4), tokens * (NG * 4), bar, policy);
+                bulk_g2s_to(dst + kKvStep * D + (kKvStep + to) * (NG * 4), rec + P * D + (P + from) * (NG * 4), tokens * (NG * 4), bar, policy);
+            };
+            if (here0) copy_page(page0, 0);
+            if (parts_log2 && here1) copy_page(page1, 16);
+        }
         __syncwarp();
-        if (here)
-            bulk_g2s_to(dst + in_slot * C::kSlotBytes,
-                        src + (size_t)(uint32_t)page * (uint32_t)(a.g.heads * a.g.rec) + (key & (P - 1) & kKvStep ? copy_bytes : 0),
-                        copy_bytes, smem_u32(full + in_slot), policy_evict_first());
         key += KW * kKvStep;
         in_slot = in_slot + 1 == C::kSlots ? 0 : in_slot + 1;
     };

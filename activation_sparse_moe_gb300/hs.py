@@ -301,10 +301,17 @@ def hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, tab
         raise HsError("hs_kv4_plan", st)
 
 
+_current = None  # torch's own lookups of the current device and its raw stream
+
+
 def _kv4_stream(stream):
+    global _current
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current is None:
+            import torch
+            torch.cuda.init()
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        return _current[1](_current[0]())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
