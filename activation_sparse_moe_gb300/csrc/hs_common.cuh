@@ -166,15 +166,6 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
         : "memory");
 }
 
-// The same with shared-memory addresses of the 32-bit window.
-__device__ __forceinline__ void bulk_g2s_to(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-        : "memory");
-}
-
 // 16-byte global -> shared copy through L2 (cp.async), with an L2 cache policy;
 // both addresses 16-byte aligned.
 __device__ __forceinline__ void cp_async16_hint(void* dst, const void* src, uint64_t policy) {

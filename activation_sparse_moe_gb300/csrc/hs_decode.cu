@@ -522,6 +522,8 @@ extern "C" const char* hs_status_string(int status) {
     }
 }
 
+unsigned hs_kv4_take_status();  // of the key/value cache attention (hs_kv4_attn.cu)
+
 extern "C" int hs_device_status(int* status) {
     if (!status) return HS_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess) return HS_ERR_CUDA;

@@ -133,8 +133,6 @@ int hs_batch_decode(const hs_moe_layer* L, const uint16_t* x, const float* logit
 unsigned hs_batch_take_status();
 // Reads and clears the prefill translation unit's device error word.
 unsigned hs_prefill_take_status();
-// Reads and clears the key/value cache attention's device error word.
-unsigned hs_kv4_take_status();
 // Batch decode of this many tokens or more runs on the prefill kernels (tensor
 // cores: each weight tile is dequantised once for all of an expert's tokens),
 // where the layer allows it; below, the batch decode kernels are faster.

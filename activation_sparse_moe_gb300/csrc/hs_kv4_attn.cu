@@ -16,7 +16,6 @@
 #include <type_traits>
 
 #include "hs_kv4_join.cuh"
-#include "hs_tc.cuh"
 
 namespace hs {
 
