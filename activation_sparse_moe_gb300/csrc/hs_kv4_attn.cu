@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     const int *qs = a.q_start, *ls = a.seq_len;  // looked at once an item
     // Where a warp computes and where it loads, a copy a warp in shared memory
     // (every lane writes the same): looked at once an item, and registers are short.
-    __shared__ KvWalk walks[C::kWarps], ahead[C::kWarps];
+    __shared__ KvWalk walks[C::kWarps], ahead[C::kWarps], comings[C::kWarps];
     __shared__ int join_last;
     static_assert(C::kWarps * C::kSlots <= 32, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -174,6 +174,24 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         key += KW * kKvStep;
         in_slot = in_slot + 1 == C::kSlots ? 0 : in_slot + 1;
     };
+    // The queries of an item (lane: row g, 16 channels of each group), read ahead: the
+    // first ones before the ring's first pages are looked up, the next ones while
+    // the warps' sums of an item are joined.
+    uint4 v[NQ][NG][2];
+    auto fetch_q = [&](const KvWalk& of) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            const int row = rt * 8 * NQ + n * 8 + g, in_tile = kv_row_token(a, row), tok = of.r * a.tq + in_tile;
+            const bool valid = row < a.tq * a.group && tok < of.n;
+            const uint16_t* src = a.q + (long long)(of.row0 + tok) * a.q_st + (long long)(of.head * a.group + row - in_tile * a.group) * a.q_sh;
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    v[n][i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    if (w.left > 0) fetch_q(w);
     for (int i = 0; i < C::kSlots; ++i) load();
 
     // ---- the items
@@ -196,18 +214,13 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         uint32_t Q[4 * NG][NQ][2];
         float sq[NG][NQ][2], sc;
         {
-            uint4 v[NQ][NG][2];
             uint32_t top = 0;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                const int row = row0 + n * 8 + g, in_tile = kv_row_token(a, row), tok = w.r * a.tq + in_tile;
-                const bool valid = row < a.tq * a.group && tok < w.n;
-                const uint16_t* src = a.q + (long long)(w.row0 + tok) * a.q_st + (long long)(w.head * a.group + row - in_tile * a.group) * a.q_sh;
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        v[n][i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
                         top = max(max(top, v[n][i][h].x & 0x7fff7fffu), max(v[n][i][h].y & 0x7fff7fffu, max(v[n][i][h].z & 0x7fff7fffu, v[n][i][h].w & 0x7fff7fffu)));
                         top = max(top, max(max((v[n][i][h].x << 16) & 0x7fffffffu, (v[n][i][h].y << 16) & 0x7fffffffu),
                                            max((v[n][i][h].z << 16) & 0x7fffffffu, (v[n][i][h].w << 16) & 0x7fffffffu)));
@@ -478,6 +491,14 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                 if (g == 0) merge_ml[at] = make_float2(m[n][e], l[n][e]);
             }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
+        KvWalk& coming = comings[warp];
+        {
+            KvWalk n = w;
+            kv_next_piece(a, qs, ls, n);
+            coming = n;
+            __syncwarp();
+            if (n.left > 0) fetch_q(coming);
+        }
         const bool whole = cnt == w.tiles;
         const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
         const size_t piece = (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * a.rows;
@@ -498,10 +519,10 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
             for (int i = 0; i < KW; ++i) {
                 const float f = ex2(ml[i].x - top);
-                const Vec v = reinterpret_cast<const Vec*>(merge + (from + i * 8 * NQ) * C::kLine)[lane];
+                const Vec y = reinterpret_cast<const Vec*>(merge + (from + i * 8 * NQ) * C::kLine)[lane];
                 sum = fmaf(f, ml[i].y, sum);
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(&v)[e], acc[e]);
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(&y)[e], acc[e]);
             }
             if (whole) {
                 const int in_tile = kv_row_token(a, row);
@@ -523,10 +544,8 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, total, &join_last, add_pieces<D, C::kWarps>);
-        KvWalk n = w;
-        kv_next_piece(a, qs, ls, n);
         __syncwarp();
-        w = n;
+        w = coming;
         __syncwarp();
     }
 }
