@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             const int row = rt * 8 * NQ + n * 8 + g, in_tile = kv_row_token(a, row), tok = of.r * a.tq + in_tile;
-            const bool valid = row < a.tq * a.group && tok < of.n;
+            const bool valid = of.left > 0 && row < a.tq * a.group && tok < of.n;
             const uint16_t* src = a.q + (long long)(of.row0 + tok) * a.q_st + (long long)(of.head * a.group + row - in_tile * a.group) * a.q_sh;
 #pragma unroll
             for (int i = 0; i < NG; ++i)
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     v[n][i][h] = valid ? *reinterpret_cast<const uint4*>(src + i * 64 + t * 16 + h * 8) : make_uint4(0, 0, 0, 0);
         }
     };
-    if (w.left > 0) fetch_q(w);
+    fetch_q(w);
     for (int i = 0; i < C::kSlots; ++i) load();
 
     // ---- the items
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             kv_next_piece(a, qs, ls, n);
             coming = n;
             __syncwarp();
-            if (n.left > 0) fetch_q(coming);
+            fetch_q(coming);
         }
         const bool whole = cnt == w.tiles;
         const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
