@@ -50,7 +50,7 @@ template <int D, int NQ, int RT, int KW>
 struct DecodeCfg {
     static constexpr int kNg = D / 64;
     static constexpr int kCtas = RT > 1 ? 1 : NQ == 1 ? 3 : 2;  // resident on an SM
-    static constexpr int kSlots = RT == 1 && NQ == 2 ? 4 : 3;  // steps of a warp's ring
+    static constexpr int kSlots = 3;  // steps of a warp's ring
     static constexpr int kSlotBytes = kv_record_bytes(kKvStep, D);
     static constexpr int kWarps = RT * KW;
     static constexpr int kThreads = 32 * kWarps;
@@ -560,10 +560,10 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tq = C::kRows / a.group;
     a.min_units = 2;
     a.tile_log2 = 6;
-    // An item's own time in tiles: 0, 2, 4, 8 and 16 gave 91.0, 82.9, 78.2, 77.3 and 81.4 us for 64
-    // ragged decode requests, 17.7, 15.9, 15.3, 13.7 and 14.7 us for 33 windowed ones, and 34.3, 31.0,
-    // 29.7, 30.9 and 32.6 us for 48-row verification, whose tiles take longer.
-    a.pad = RT == 1 ? 8 : 4;
+    // An item's own time in tiles, for 64 ragged decode requests and 33 windowed ones: 6, 8 and 10 take
+    // 71.2, 71.6 and 73.3 us, 11.2, 11.4 and 11.4 us; none at all took 91.0 instead of 77.3 us, 17.7
+    // instead of 13.7 us. Two row tiles' tiles take longer: 4 gave 29.7 us for 48 rows, 8 gave 30.9 us.
+    a.pad = RT == 1 ? 6 : 4;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
