@@ -58,6 +58,7 @@ struct DecodeCfg {
     static constexpr int kLine = D + 4;               // floats of a row of the warps' sums (padded against bank conflicts)
     static constexpr int kMergeBytes = kWarps * 8 * NQ * (kLine + 2) * 4;
     static constexpr int kRows = 8 * NQ * RT;
+    static constexpr int kJoinSets = D == 128 && NQ == 2 ? 2 : 1;  // a warp's share of the rows in the joins
     static int smem(int n_seqs) { return kRingBytes + kMergeBytes + 256 + (n_seqs <= kKvFew ? 0 : n_seqs + 1) * 4; }
 };
 
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll 1
         for (int row = warp; row < rows; row += C::kWarps) {
             constexpr int V = D / 32;
-            using Vec = typename FloatVec<V>::T;
+            using Vec = typename std::conditional<V == 4, float4, float2>::type;
             const int from = (row / (8 * NQ)) * KW * 8 * NQ + row % (8 * NQ);
             float2 ml[KW];
             float top = -1e30f, sum = 0.f, acc[V];
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, total, &join_last, add_pieces<D, C::kWarps>);
+        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, total, &join_last, add_pieces<D, C::kWarps, C::kJoinSets, 8 / C::kJoinSets>);
         __syncwarp();
         w = coming;
         __syncwarp();

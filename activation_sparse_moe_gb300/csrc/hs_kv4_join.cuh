@@ -22,120 +22,97 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ size_t piece_slot(int c, int i) { return i ? 2 * (size_t)(c + i) : 2 * (size_t)c + 1; }
 
-template <int N> struct FloatVec;
-template <> struct FloatVec<2> { using T = float2; };
-template <> struct FloatVec<4> { using T = float4; };
-
-// Adds pieces first, first + step, ... (count of them, at most 64) of the item
+// Adds pieces first, first + step, ... (count of them, at most 32) of the item
 // that began in CTA c: into out if `final`, else into piece `first`.  Called by
-// whole warps, `warp` of WARPS; a warp takes ROWS rows of BATCH pieces at a
-// time (it is latency that bounds this).
-template <int D, int WARPS, int ROWS = 4, int BATCH = 4>
+// whole warps, `warp` of WARPS.  D / 8 lanes take a row, eight channels each; a
+// warp takes SETS sets of 32 / (D / 8) rows and BATCH pieces of each at a time,
+// as many bytes in flight as its registers hold.  Lane i of a row knows the
+// weight of pieces i, i + D / 8, ...
+template <int D, int WARPS, int SETS, int BATCH>
 __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
                                         bool final) {
-    constexpr int V = D / 32;
-    using Vec = typename FloatVec<V>::T;
-    const int lane = threadIdx.x & 31;
+    constexpr int kL = D / 8, kR = 32 / kL, kP = 32 / kL;  // lanes a row, rows at a time, pieces a lane
+    const int lane = threadIdx.x & 31, sub = lane / kL, i8 = lane % kL;
     const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
-    for (int r0 = warp; r0 < rows; r0 += ROWS * WARPS) {
-        float m[ROWS], l[ROWS], acc[ROWS][V];
-        int row[ROWS];
-        if (count <= 2) {  // the commonest case: everything is read at once
-            Vec v[2][ROWS];
-            float2 ml[2][ROWS];
+    // row `row` of piece i: fewer than 2^18 rows of the workspace (kKvWsRows)
+    auto place = [&](int i, int row) { return (uint32_t)(piece_slot(c, first + min(i, count - 1) * step) * a.rows + row); };
+    for (int s0 = warp; s0 * kR < rows; s0 += SETS * WARPS) {
+        float wt[SETS][kP], acc[SETS][8], m[SETS], l[SETS];
+        float4 v[BATCH][SETS][2];
+        int row[SETS];
+        auto fetch = [&](int i0) {
 #pragma unroll
-            for (int x = 0; x < ROWS; ++x) {
-                row[x] = min(r0 + x * WARPS, rows - 1);
+            for (int i = 0; i < BATCH; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const size_t at = piece_slot(c, first + min(i, count - 1) * step) * a.rows + row[x];
-                    v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + at * D) + lane);
-                    ml[i][x] = __ldcg(a.part_ml + at);
+                for (int x = 0; x < SETS; ++x) {
+                    const float4* src = reinterpret_cast<const float4*>(a.part_o + place(i0 + i, row[x]) * (uint32_t)D + i8 * 8);
+                    v[i][x][0] = __ldcg(src);
+                    v[i][x][1] = __ldcg(src + 1);
                 }
-            }
+        };
 #pragma unroll
-            for (int x = 0; x < ROWS; ++x) {
-                if (count == 1) ml[1][x] = make_float2(-1e30f, 0.f);
-                m[x] = fmaxf(ml[0][x].x, ml[1][x].x);
-                const float f0 = ex2(ml[0][x].x - m[x]), f1 = count == 1 ? 0.f : ex2(ml[1][x].x - m[x]);
-                l[x] = f0 * ml[0][x].y + f1 * ml[1][x].y;
+        for (int x = 0; x < SETS; ++x) {
+            row[x] = min((s0 + x * WARPS) * kR + sub, rows - 1);
+            m[x] = -1e30f;
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    acc[x][e] = f0 * reinterpret_cast<const float*>(&v[0][x])[e] + f1 * reinterpret_cast<const float*>(&v[1][x])[e];
-            }
-        } else {
-            // the first pieces' rows come along with all pieces' (maximum, sum)
-            float wt[ROWS][2];
-            Vec v[BATCH][ROWS];
-            auto fetch = [&](int i0) {
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const size_t at = piece_slot(c, first + min(i0 + i, count - 1) * step) * a.rows;
-#pragma unroll
-                    for (int x = 0; x < ROWS; ++x) v[i][x] = __ldcg(reinterpret_cast<const Vec*>(a.part_o + (at + row[x]) * D) + lane);
-                }
-            };
-#pragma unroll
-            for (int x = 0; x < ROWS; ++x) {
-                row[x] = min(r0 + x * WARPS, rows - 1);
-                float2 ml[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    ml[y] = lane + 32 * y < count ? __ldcg(a.part_ml + piece_slot(c, first + (lane + 32 * y) * step) * a.rows + row[x])
-                                                  : make_float2(-1e30f, 0.f);
-                m[x] = fmaxf(ml[0].x, ml[1].x);
-                wt[x][0] = ml[0].x, wt[x][1] = ml[1].x;
-                l[x] = ml[0].y, acc[x][0] = ml[1].y;
-            }
-            fetch(0);
-#pragma unroll
-            for (int x = 0; x < ROWS; ++x) {
-#pragma unroll
-                for (int o = 16; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
-                wt[x][0] = ex2(wt[x][0] - m[x]);
-                wt[x][1] = ex2(wt[x][1] - m[x]);
-                l[x] = wt[x][0] * l[x] + wt[x][1] * acc[x][0];
-#pragma unroll
-                for (int o = 16; o; o >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], o);
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[x][e] = 0.f;
-            }
-            for (int i0 = 0; i0 < count; i0 += BATCH) {
-                if (i0) fetch(i0);
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-                    for (int x = 0; x < ROWS; ++x) {
-                        float f = __shfl_sync(~0u, i0 + i < 32 ? wt[x][0] : wt[x][1], (i0 + i) & 31);
-                        if (i0 + i >= count) f = 0.f;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) acc[x][e] = fmaf(f, reinterpret_cast<const float*>(&v[i][x])[e], acc[x][e]);
-                    }
+            for (int y = 0; y < kP; ++y) {
+                float2 ml = make_float2(-1e30f, 0.f);
+                if (i8 + y * kL < count) ml = __ldcg(a.part_ml + place(i8 + y * kL, row[x]));
+                wt[x][y] = ml.x, acc[x][y] = ml.y;
+                m[x] = fmaxf(m[x], ml.x);
             }
         }
+        fetch(0);
 #pragma unroll
-        for (int x = 0; x < ROWS; ++x) {
-            if (r0 + x * WARPS >= rows) continue;
+        for (int x = 0; x < SETS; ++x) {
+#pragma unroll
+            for (int o = kL / 2; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
+            l[x] = 0.f;
+#pragma unroll
+            for (int y = 0; y < kP; ++y) {
+                wt[x][y] = i8 + y * kL < count ? ex2(wt[x][y] - m[x]) : 0.f;
+                l[x] = fmaf(wt[x][y], acc[x][y], l[x]);
+            }
+#pragma unroll
+            for (int o = kL / 2; o; o >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[x][e] = 0.f;
+        }
+        for (int i0 = 0; i0 < count; i0 += BATCH) {
+            if (i0) fetch(i0);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                for (int x = 0; x < SETS; ++x) {
+                    float mine = wt[x][0];
+#pragma unroll
+                    for (int y = 1; y < kP; ++y) mine = i0 + i >= y * kL ? wt[x][y] : mine;
+                    float f = __shfl_sync(~0u, mine, (i0 + i) % kL, kL);
+                    if (i0 + i >= count) f = 0.f;
+                    const float* from = reinterpret_cast<const float*>(v[i][x]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[x][e] = fmaf(f, from[e], acc[x][e]);
+                }
+        }
+#pragma unroll
+        for (int x = 0; x < SETS; ++x) {
+            if ((s0 + x * WARPS) * kR + sub >= rows) continue;
             if (final) {
                 const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
-                uint32_t u[V / 2];
+                uint32_t u[4];
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e)
+                for (int e = 0; e < 4; ++e)
                     u[e] = (uint32_t)f32_to_bf16_bits(acc[x][2 * e] * inv) | ((uint32_t)f32_to_bf16_bits(acc[x][2 * e + 1] * inv) << 16);
                 const int tok = kv_row_token(a, row[x]);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
-                                                            (long long)(w.head * a.group + row[x] - tok * a.group) * a.o_sh) + lane * (V / 2);
-                if (V == 4)
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[V / 2 - 1]);
-                else
-                    *dst = u[0];
+                *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
+                                          (long long)(w.head * a.group + row[x] - tok * a.group) * a.o_sh + i8 * 8) =
+                    make_uint4(u[0], u[1], u[2], u[3]);
             } else {
-                const size_t at = piece_slot(c, first) * a.rows + row[x];
-                Vec o;
-#pragma unroll
-                for (int e = 0; e < V; ++e) reinterpret_cast<float*>(&o)[e] = acc[x][e];
-                reinterpret_cast<Vec*>(a.part_o + at * D)[lane] = o;
-                if (lane == 0) a.part_ml[at] = make_float2(m[x], l[x]);
+                const uint32_t at = place(0, row[x]);
+                float4* dst = reinterpret_cast<float4*>(a.part_o + at * (uint32_t)D + i8 * 8);
+                dst[0] = make_float4(acc[x][0], acc[x][1], acc[x][2], acc[x][3]);
+                dst[1] = make_float4(acc[x][4], acc[x][5], acc[x][6], acc[x][7]);
+                if (i8 == 0) a.part_ml[at] = make_float2(m[x], l[x]);
             }
         }
     }

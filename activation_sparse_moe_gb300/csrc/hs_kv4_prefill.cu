@@ -102,7 +102,7 @@ __device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
 template <int D>
 __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
                                               bool final) {
-    add_pieces<D, 8, 8, 2>(a, w, warp, c, first, step, count, final);
+    add_pieces<D, 8, 4, 2>(a, w, warp, c, first, step, count, final);
 }
 
 template <int D>
