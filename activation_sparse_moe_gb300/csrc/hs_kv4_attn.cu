@@ -544,7 +544,13 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
-        if (!whole) join_pieces<C::kWarps, 1>(a, w, warp, total, &join_last, add_pieces<D, C::kWarps, C::kJoinSets, 8 / C::kJoinSets>);
+        if (!whole) {
+            const KvPieces of = kv_pieces(a, w, total);
+            auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory"); };
+            join_pieces(of, a.joined, tid == 0, &join_last, meet, [&](int first, int step, int count, bool final) {
+                add_pieces<D, C::kJoinSets, 8 / C::kJoinSets>(a, w, warp, C::kWarps, 0, rows, of.c, first, step, count, final);
+            });
+        }
         __syncwarp();
         w = coming;
         __syncwarp();

@@ -23,20 +23,20 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ size_t piece_slot(int c, int i) { return i ? 2 * (size_t)(c + i) : 2 * (size_t)c + 1; }
 
 // Adds pieces first, first + step, ... (count of them, at most 32) of the item
-// that began in CTA c: into out if `final`, else into piece `first`.  Called by
-// whole warps, `warp` of WARPS.  D / 8 lanes take a row, eight channels each; a
+// that began in CTA c, their rows row0 <= row < row1: into out if `final`, else
+// into piece `first`.  Called by
+// whole warps, `warp` of `warps`.  D / 8 lanes take a row, eight channels each; a
 // warp takes SETS sets of 32 / (D / 8) rows and BATCH pieces of each at a time,
 // as many bytes in flight as its registers hold.  Lane i of a row knows the
 // weight of pieces i, i + D / 8, ...
-template <int D, int WARPS, int SETS, int BATCH>
-__device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
-                                        bool final) {
+template <int D, int SETS, int BATCH>
+__device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, int warps, int row0, int row1, int c, int first,
+                                           int step, int count, bool final) {
     constexpr int kL = D / 8, kR = 32 / kL, kP = 32 / kL;  // lanes a row, rows at a time, pieces a lane
     const int lane = threadIdx.x & 31, sub = lane / kL, i8 = lane % kL;
-    const int rows = min(a.tq, w.n - w.r * a.tq) * a.group;
     // row `row` of piece i: fewer than 2^18 rows of the workspace (kKvWsRows)
     auto place = [&](int i, int row) { return (uint32_t)(piece_slot(c, first + min(i, count - 1) * step) * a.rows + row); };
-    for (int s0 = warp; s0 * kR < rows; s0 += SETS * WARPS) {
+    for (int s0 = warp; row0 + s0 * kR < row1; s0 += SETS * warps) {
         float wt[SETS][kP], acc[SETS][8], m[SETS], l[SETS];
         float4 v[BATCH][SETS][2];
         int row[SETS];
@@ -52,7 +52,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
         };
 #pragma unroll
         for (int x = 0; x < SETS; ++x) {
-            row[x] = min((s0 + x * WARPS) * kR + sub, rows - 1);
+            row[x] = min(row0 + (s0 + x * warps) * kR + sub, row1 - 1);
             m[x] = -1e30f;
 #pragma unroll
             for (int y = 0; y < kP; ++y) {
@@ -96,7 +96,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
         }
 #pragma unroll
         for (int x = 0; x < SETS; ++x) {
-            if ((s0 + x * WARPS) * kR + sub >= rows) continue;
+            if (row0 + (s0 + x * warps) * kR + sub >= row1) continue;
             if (final) {
                 const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
                 uint32_t u[4];
@@ -118,41 +118,46 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
     }
 }
 
-// Called by WARPS warps (`warp` the calling one's index) of a CTA that has
-// written its piece of w's item.  *last is a word of shared memory; the warps meet at named barrier BAR; add is
-// add_pieces.
-template <int WARPS, int BAR, typename Add>
-__device__ __forceinline__ void join_pieces(const KvAttnArgs& a, const KvWalk& w, int warp, uint32_t total, int* last, Add add) {
+// The pieces of the item that a CTA's piece belongs to: the CTA of the first one, their number.
+struct KvPieces {
+    int c, count;
+};
+__device__ __forceinline__ KvPieces kv_pieces(const KvAttnArgs& a, const KvWalk& w, uint32_t total) {
     const KvCut cut = kv_cut(a, total);
-    const int me = blockIdx.x;
-    const bool lead = warp == 0 && (threadIdx.x & 31) == 0;
     // the unit with which this piece began: of the run's first item the run's, else
     // what the run has left lies before the run's end
-    const uint32_t begin = w.first ? cut.at(me) - w.tile : cut.at(me + 1) - w.left, end = begin + (uint32_t)w.tiles;
-    const int c = cut.cta_of(begin), pieces = cut.cta_of(end - 1) - c + 1;
-    auto meet = [&]() { asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(32 * WARPS) : "memory"); };
-    auto arrive = [&](int* counter, int of) -> bool {
+    const uint32_t begin = w.first ? cut.at(blockIdx.x) - w.tile : cut.at(blockIdx.x + 1) - w.left, end = begin + (uint32_t)w.tiles;
+    const int c = cut.cta_of(begin);
+    return {c, cut.cta_of(end - 1) - c + 1};
+}
+
+// Called by the warps that have written a CTA's piece.  meet is a barrier of
+// theirs, lead one thread of them, joined their counters (kKvMaxCtas apart),
+// *last a word of shared memory; add(first, step, count, final) is add_pieces.
+template <typename Meet, typename Add>
+__device__ __forceinline__ void join_pieces(const KvPieces& of, int* joined, bool lead, int* last, Meet meet, Add add) {
+    auto arrive = [&](int* counter, int wanted) -> bool {
         meet();  // the CTA's writes ...
         if (lead) {
             // ... are seen before its arrival, and the other CTAs' after the last one's
             int before;
             asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-            *last = before == of - 1;
-            if (before == of - 1) *counter = 0;  // for the next call
+            *last = before == wanted - 1;
+            if (before == wanted - 1) *counter = 0;  // for the next call
         }
         meet();
         return *last != 0;
     };
-    if (pieces <= kJoin) {
-        if (arrive(a.joined + c, pieces)) add(a, w, warp, c, 0, 1, pieces, true);
+    if (of.count <= kJoin) {
+        if (arrive(joined + of.c, of.count)) add(0, 1, of.count, true);
         return;
     }
-    const int run = (me - c) / kJoin, size = min(kJoin, pieces - run * kJoin);
+    const int run = ((int)blockIdx.x - of.c) / kJoin, size = min(kJoin, of.count - run * kJoin);
     // A run's counter is that of its first CTA; an item that begins in that CTA has another.
-    if (!arrive(a.joined + kKvMaxCtas * (run ? 2 : 1) + c + run * kJoin, size)) return;
-    add(a, w, warp, c, run * kJoin, 1, size, false);
-    const int runs = (pieces + kJoin - 1) / kJoin;
-    if (arrive(a.joined + c, runs)) add(a, w, warp, c, 0, kJoin, runs, true);
+    if (!arrive(joined + kKvMaxCtas * (run ? 2 : 1) + of.c + run * kJoin, size)) return;
+    add(run * kJoin, 1, size, false);
+    const int runs = (of.count + kJoin - 1) / kJoin;
+    if (arrive(joined + of.c, runs)) add(0, kJoin, runs, true);
 }
 
 }  // namespace hs

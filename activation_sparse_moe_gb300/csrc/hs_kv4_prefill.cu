@@ -47,7 +47,8 @@ struct PfShared {
     uint32_t nan_any[kPfInfo];         // some value of the tile is NaN
     uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
     uint32_t tmem;
-    int join_last;
+    int join_last[2];   // by row tile
+    int direct[2][2];   // by end of the run (0: its first piece) and row tile: the item's other piece is there
 };
 
 // Shared-memory descriptor of a tile whose rows run along K (keys) and whose
@@ -100,9 +101,9 @@ __device__ __forceinline__ uint4 take_apart(uint32_t w, __half2 s, __half2 b) {
 
 // A call of its own: its registers are not the softmax's.
 template <int D>
-__device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int c, int first, int step, int count,
-                                              bool final) {
-    add_pieces<D, 8, 4, 2>(a, w, warp, c, first, step, count, final);
+__device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int warps, int row0, int row1, int c, int first,
+                                              int step, int count, bool final) {
+    add_pieces<D, 4, 2>(a, w, warp, warps, row0, row1, c, first, step, count, final);
 }
 
 template <int D>
@@ -419,7 +420,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         }
         while (w.left > 0) {
             const int cnt = kv_piece_tiles(w), nrows = rows_of(w), ctx = w.len - w.n;
-            const bool whole = cnt == w.tiles;
+            const bool whole = cnt == w.tiles, two = nrows > 128;
+            // An item's pieces are joined by row tile, by the warps of the row tile (the counters
+            // of the second lie 228 further on); by all eight where there is one row tile.
+            auto joined = [&]() { return a.joined + (two ? x * (kKvMaxCtas / 2) : 0); };
+            auto lead = [&]() { return lane == 0 && (two ? (warp & 3) == 0 : warp == 0); };
+            auto meet = [&]() {
+                if (!two)
+                    asm volatile("bar.sync 3, 256;" ::: "memory");
+                else if (x)
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
+                else
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+            };
+            KvPieces of{0, 1};
+            // Of an item's two pieces the second comes at the start of a run, the first at the end
+            // of one, when the other's sums have long been in memory: they are added on the way
+            // out, and this piece is never written (and read again, with both row tiles waiting).
+            auto other_is_there = [&]() { return of.count == 2 && (meet(), *(volatile int*)&sh.direct[w.tile == 0][two ? x : 0] != 0); };
             KvWalk& nx = coming[warp];  // the piece after this one
             {
                 KvWalk n = w;
@@ -433,6 +451,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 fetch_q(nx);
                 sc = convert_q();
             }
+            bool direct = false;
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
                 const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
@@ -513,18 +532,40 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.p_full + x);
                 }
+                if (!whole) {
+                    of = kv_pieces(a, w, cum[a.n_seqs]);
+                    if (of.count == 2 && lead()) {
+                        int there;
+                        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(joined() + of.c) : "memory");
+                        sh.direct[w.tile == 0][two ? x : 0] = there;
+                        if (there) joined()[of.c] = 0;  // for the next call
+                    }
+                }
                 // The next piece's first scores are worked out while this one is written.
                 const float next_sc = more ? convert_q() : 0.f;
                 if (!dead && !mbar_wait(sh.o_full + x, o_count++ & 1)) dead = true;
+                direct = other_is_there();
                 if (!dead) {
                     tc_fence_after();
                     see_nan(cnt - 1);
+                    const uint32_t at = (2 * blockIdx.x + (w.tile == 0 ? 1 : 0)) * (uint32_t)a.rows + r;
+                    // The other piece's row, and the weights of both: the operations of add_pieces,
+                    // so that the result is the same whoever comes last.
+                    const uint32_t other = (w.tile == 0 ? 2 * blockIdx.x + 2 : 2 * blockIdx.x - 1) * (uint32_t)a.rows;
+                    float mine = 1.f, its = 0.f;
+                    if (direct) {
+                        const float2 ml = valid ? __ldcg(a.part_ml + other + r) : make_float2(-1e30f, 0.f);
+                        const float top = fmaxf(m, ml.x);
+                        mine = ex2(m - top), its = ex2(ml.x - top);
+                        l = __fadd_rn(__fmul_rn(mine, l), __fmul_rn(its, ml.y));
+                    }
                     const float inv = l != 0.f ? 1.f / l : 0.f;
-                    const size_t at = (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * a.rows + r;
                     // 64 bytes of each of the warp's rows at a time, by way of a buffer (chunk j of
                     // row i at j ^ (i / 2 % 4): no two in one bank), so that four lanes write a row's
                     // 64 bytes together: a thread writing its own row took the load-store unit 4000
                     // cycles a piece.
+                    int ln = lane, wq = warp & 3;
+                    asm volatile("" : "+r"(ln), "+r"(wq));  // (what follows from them is not kept through the loop above)
                     uint8_t* buf = out_s + warp * 2048;
                     auto write64 = [&](const uint4 (&u)[4], uint8_t* base, bool part, int d) {
                         __syncwarp();
@@ -536,22 +577,56 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                             const int orow = i * 8 + (lane >> 2), qr = x * 128 + (warp & 3) * 32 + orow, qt = kv_row_token(a, qr);
                             const uint4 z = *reinterpret_cast<const uint4*>(buf + orow * 64 + (((lane & 3) ^ (orow >> 1 & 3)) << 4));
                             if (qr >= nrows) continue;
-                            uint8_t* dst = part ? base + ((at - r + qr) * D + d) * 4
+                            uint8_t* dst = part ? base + ((at - r + qr) * (uint32_t)D + d) * (size_t)4
                                                 : base + ((long long)qt * a.o_st + (long long)(qr - qt * a.group) * a.o_sh + d) * 2;
                             *reinterpret_cast<uint4*>(dst + (lane & 3) * 16) = z;
                         }
                     };
-                    uint8_t* out0 = reinterpret_cast<uint8_t*>(a.out + (long long)(w.row0 + w.r * a.tq) * a.o_st + (long long)w.head * a.group * a.o_sh);
-#pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
-                        float v[32];
-                        tmem_ld32(tl + 256 + x * 128 + d, v);
-                        if ((nan >> (d >> 6)) & 1u) {
+                    // The same with the other piece's sums, four channels a lane.
+                    float4 its_rows[4];  // the next 16 channels of the other piece
+                    auto fetch_its = [&](int d) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7fc00000u);
+                        for (int i = 0; i < 4; ++i) {
+                            const int qr = min(x * 128 + wq * 32 + i * 8 + (ln >> 2), nrows - 1);
+                            its_rows[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (other + qr) * (uint32_t)D + d) + (ln & 3));
                         }
-                        uint4 u[4];
-                        if (whole) {
+                    };
+                    auto add64 = [&](const uint4 (&u)[4], uint8_t* base, int d) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(buf + ln * 64 + ((j ^ (ln >> 1 & 3)) << 4)) = u[j];
+                        float4 y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[i] = its_rows[i];
+                        if (d + 16 < D) fetch_its(d + 16);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int orow = i * 8 + (ln >> 2), qr = x * 128 + wq * 32 + orow, qt = kv_row_token(a, qr);
+                            const float4 z = *reinterpret_cast<const float4*>(buf + orow * 64 + (((ln & 3) ^ (orow >> 1 & 3)) << 4));
+                            const float f = __shfl_sync(~0u, mine, orow), g = __shfl_sync(~0u, its, orow), n = __shfl_sync(~0u, inv, orow);
+                            const bool ahead = w.tile == 0;  // this piece's keys come first
+                            const float f0 = ahead ? f : g, f1 = ahead ? g : f;
+                            auto sum = [&](float u, float v) { return __fmaf_rn(f1, ahead ? v : u, __fmaf_rn(f0, ahead ? u : v, 0.f)) * n; };
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(sum(z.x, y[i].x), sum(z.y, y[i].y)),
+                                                 hi = __floats2bfloat162_rn(sum(z.z, y[i].z), sum(z.w, y[i].w));
+                            if (qr >= nrows) continue;
+                            uint8_t* dst = base + ((long long)qt * a.o_st + (long long)(qr - qt * a.group) * a.o_sh + d) * 2;
+                            *reinterpret_cast<uint2*>(dst + (ln & 3) * 8) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        }
+                    };
+                    uint8_t* out0 = reinterpret_cast<uint8_t*>(a.out + (long long)(w.row0 + w.r * a.tq) * a.o_st + (long long)w.head * a.group * a.o_sh);
+                    if (whole) {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 32) {
+                            float v[32];
+                            tmem_ld32(tl + 256 + x * 128 + d, v);
+                            if ((nan >> (d >> 6)) & 1u) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7fc00000u);
+                            }
+                            uint4 u[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t z[4];
@@ -564,26 +639,60 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                                 u[j] = make_uint4(z[0], z[1], z[2], z[3]);
                             }
                             write64(u, out0, false, d);
-                        } else {
+                        }
+                    } else if (direct) {
+                        fetch_its(0);
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            float v[16];
+                            tmem_ld16(tl + 256 + x * 128 + d, v);
+                            if ((nan >> (d >> 6)) & 1u) {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const int from = 16 * h + 8 * (j >> 1) + (j & 1);  // channels 0-3 or 4-7 of eight
-                                    u[j] = make_uint4(__float_as_uint(v[from]), __float_as_uint(v[from + 2]), __float_as_uint(v[from + 4]),
-                                                      __float_as_uint(v[from + 6]));
-                                }
-                                write64(u, reinterpret_cast<uint8_t*>(a.part_o), true, d + 16 * h);
+                                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(0x7fc00000u);
                             }
+                            uint4 u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int from = 8 * (j >> 1) + (j & 1);  // channels 0-3 or 4-7 of eight
+                                u[j] = make_uint4(__float_as_uint(v[from]), __float_as_uint(v[from + 2]), __float_as_uint(v[from + 4]),
+                                                  __float_as_uint(v[from + 6]));
+                            }
+                            add64(u, out0, d);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            float v[16];
+                            tmem_ld16(tl + 256 + x * 128 + d, v);
+                            if ((nan >> (d >> 6)) & 1u) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(0x7fc00000u);
+                            }
+                            uint4 u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int from = 8 * (j >> 1) + (j & 1);  // channels 0-3 or 4-7 of eight
+                                u[j] = make_uint4(__float_as_uint(v[from]), __float_as_uint(v[from + 2]), __float_as_uint(v[from + 4]),
+                                                  __float_as_uint(v[from + 6]));
+                            }
+                            write64(u, reinterpret_cast<uint8_t*>(a.part_o), true, d);
                         }
                     }
-                    if (valid && !whole) a.part_ml[at] = make_float2(m, l);
+                    if (valid && !whole && !direct) a.part_ml[at] = make_float2(m, l);
                     tc_fence_before();
                 }
                 sc = next_sc;
+            } else if (!whole) {
+                of = kv_pieces(a, w, cum[a.n_seqs]);
+                direct = other_is_there();
             }
             tiles += cnt;
-            if (!whole) join_pieces<8, 1>(a, w, warp, cum[a.n_seqs], &sh.join_last, add_pieces_apart<D>);
+            if (!whole && !direct) {
+                join_pieces(of, joined(), lead(), &sh.join_last[two ? x : 0], meet, [&](int first, int step, int count, bool final) {
+                    add_pieces_apart<D>(a, w, two ? warp & 3 : warp, two ? 4 : 8, two ? x * 128 : 0, two && !x ? 128 : nrows, of.c, first, step,
+                                        count, final);
+                });
+            }
             __syncwarp();
             w = nx;
             __syncwarp();
