@@ -6,6 +6,9 @@
 // run, and the runs' sums by the CTA whose run comes last: the order is that of
 // the keys either way, so the result does not depend on who comes last.  One
 // launch does everything; a second kernel for the sums cost 5 to 10 us a call.
+// A latency bounds this, not bytes: 152 pieces of 16 rows (1.2 MB) take about 8 us in
+// two rounds; 256 rows of two pieces 20,000 cycles, which is why the chunk kernel
+// adds a pair's second piece on its way out instead.
 #pragma once
 
 #include "hs_kv4_sched.cuh"

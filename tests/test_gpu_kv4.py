@@ -337,6 +337,23 @@ def test_attention_strides_streams_and_reuse_of_the_workspace():
     _close(b0, big.expected(0.09), 0.09)
 
 
+@pytest.mark.parametrize("ctx,new,hq,hkv,dim", [([900] * 5, [200] * 5, 16, 4, 128), ([1500, 40, 700], [1, 130, 333], 8, 2, 64),
+                                                ([3000] * 40, [1] * 40, 32, 8, 128), ([2000] * 9, [3] * 9, 32, 2, 128)])
+def test_joined_pieces_do_not_depend_on_who_comes_last(ctx, new, hq, hkv, dim):
+    """Work on another stream delays some CTAs, so that an item's pieces arrive in other orders."""
+    r = _kv4.Requests(77, ctx, new, hq, hkv, dim, 64)
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+    first = r.run(hs, 0.09, ws=ws)
+    _close(first, r.expected(0.09), 0.09)
+    side, a = torch.cuda.Stream(), torch.ones(2048, 2048, device="cuda")
+    for i in range(20):
+        if i % 2:
+            with torch.cuda.stream(side):
+                a @ a
+        assert torch.equal(first, r.run(hs, 0.09, ws=ws))
+    torch.cuda.synchronize()
+
+
 def test_rows_past_the_last_request_are_not_written_and_max_new_only_chooses():
     r = _kv4.Requests(31, [40, 500], [3, 2], 8, 2, 128, 64)
     q = torch.cat((r.q, torch.full((6, 8, 128), float("nan")).bfloat16())).cuda()
