@@ -25,6 +25,30 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ size_t piece_slot(int c, int i) { return i ? 2 * (size_t)(c + i) : 2 * (size_t)c + 1; }
 
+// Of a row whose KL lanes know the (maximum, sum) of its pieces, lane i those of
+// pieces i, i + KL, ...: the common maximum, the pieces' weights and the sum.
+template <int KL, int KP>
+__device__ __forceinline__ void weigh(float (&top)[KP], const float (&sum)[KP], int i, int count, float& m, float& l) {
+#pragma unroll
+    for (int o = KL / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    l = 0.f;
+#pragma unroll
+    for (int y = 0; y < KP; ++y) {
+        top[y] = i + y * KL < count ? ex2(top[y] - m) : 0.f;
+        l = fmaf(top[y], sum[y], l);
+    }
+#pragma unroll
+    for (int o = KL / 2; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8], float scale) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        u[e] = (uint32_t)f32_to_bf16_bits(v[2 * e] * scale) | ((uint32_t)f32_to_bf16_bits(v[2 * e + 1] * scale) << 16);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
 // Adds pieces first, first + step, ... (count of them, at most 32) of the item
 // that began in CTA c, their rows row0 <= row < row1: into out if `final`, else
 // into piece `first`.  Called by
@@ -40,7 +64,7 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
     // row `row` of piece i: fewer than 2^18 rows of the workspace (kKvWsRows)
     auto place = [&](int i, int row) { return (uint32_t)(piece_slot(c, first + min(i, count - 1) * step) * a.rows + row); };
     for (int s0 = warp; row0 + s0 * kR < row1; s0 += SETS * warps) {
-        float wt[SETS][kP], acc[SETS][8], m[SETS], l[SETS];
+        float wt[SETS][kP], part[SETS][kP], acc[SETS][8], m[SETS], l[SETS];
         float4 v[BATCH][SETS][2];
         int row[SETS];
         auto fetch = [&](int i0) {
@@ -61,23 +85,14 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
             for (int y = 0; y < kP; ++y) {
                 float2 ml = make_float2(-1e30f, 0.f);
                 if (i8 + y * kL < count) ml = __ldcg(a.part_ml + place(i8 + y * kL, row[x]));
-                wt[x][y] = ml.x, acc[x][y] = ml.y;
+                wt[x][y] = ml.x, part[x][y] = ml.y;
                 m[x] = fmaxf(m[x], ml.x);
             }
         }
         fetch(0);
 #pragma unroll
         for (int x = 0; x < SETS; ++x) {
-#pragma unroll
-            for (int o = kL / 2; o; o >>= 1) m[x] = fmaxf(m[x], __shfl_xor_sync(~0u, m[x], o));
-            l[x] = 0.f;
-#pragma unroll
-            for (int y = 0; y < kP; ++y) {
-                wt[x][y] = i8 + y * kL < count ? ex2(wt[x][y] - m[x]) : 0.f;
-                l[x] = fmaf(wt[x][y], acc[x][y], l[x]);
-            }
-#pragma unroll
-            for (int o = kL / 2; o; o >>= 1) l[x] += __shfl_xor_sync(~0u, l[x], o);
+            weigh<kL, kP>(wt[x], part[x], i8, count, m[x], l[x]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[x][e] = 0.f;
         }
@@ -102,14 +117,10 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
             if (row0 + (s0 + x * warps) * kR + sub >= row1) continue;
             if (final) {
                 const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
-                uint32_t u[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = (uint32_t)f32_to_bf16_bits(acc[x][2 * e] * inv) | ((uint32_t)f32_to_bf16_bits(acc[x][2 * e + 1] * inv) << 16);
                 const int tok = kv_row_token(a, row[x]);
                 *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
                                           (long long)(w.head * a.group + row[x] - tok * a.group) * a.o_sh + i8 * 8) =
-                    make_uint4(u[0], u[1], u[2], u[3]);
+                    pack_bf16x8(acc[x], inv);
             } else {
                 const uint32_t at = place(0, row[x]);
                 float4* dst = reinterpret_cast<float4*>(a.part_o + at * (uint32_t)D + i8 * 8);

@@ -41,13 +41,14 @@ struct PrefillCfg {
     static constexpr int kQBytes = 128 * D * 2;          // of a row tile
     static constexpr int kTileBytes = kPfKeys * D * 2;   // a K or V tile
     static constexpr int kPackedBytes = kPfKeys * (D / 2 + 4 * kNg);
-    static constexpr int kFixed = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes + 8 * 2048;
+    static constexpr int kPiecesRoom = 2 * kQBytes + kPfSlots * kTileBytes + kPfPacked * kPackedBytes;  // all before the output buffers
+    static constexpr int kFixed = kPiecesRoom + 8 * 2048;
     static constexpr int smem(int n_seqs) { return 1024 + kFixed + 1024 + (n_seqs + 1) * 4; }
 };
 
 struct PfShared {
     uint64_t packed_full[kPfPacked], packed_empty[kPfPacked], kv_full[kPfSlots], kv_empty[kPfSlots];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], pieces_full;
     uint32_t gone[kPfInfo];            // per key tile: blocks of 16 keys that are not there
     uint32_t nan_any[kPfInfo];         // some value of the tile is NaN
     uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
@@ -111,6 +112,77 @@ __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk&
     add_pieces<D, 4, 2>(a, w, warp, warps, row0, row1, c, first, step, count, final);
 }
 
+// The same by the 256 softmax threads of a CTA that has no work left: its
+// shared memory is free, and the pieces (at most kJoin of them) come in whole by
+// bulk copies.  A few loops of little code: that of add_pieces runs once a call, and
+// costs fetching it besides the rounds of loads (48 rows of five pieces: 9,400
+// cycles, here 5,800; 16 requests of three drafts 25.2 us, here 23.6).  The operations and their order are those of add_pieces.
+template <int D>
+__device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk& w, int c, int count, int rows) {
+    constexpr int kL = D / 8, kR = 32 / kL, kP = kJoin / kL, kAtOnce = 4;
+    const int tid = threadIdx.x, lane = tid & 31, sub = lane / kL, i8 = lane % kL;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* room = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* buffers = room + PrefillCfg<D>::kPiecesRoom;
+    float* weights = reinterpret_cast<float*>(buffers);  // [row][kJoin]
+    uint64_t* bar = &reinterpret_cast<PfShared*>(buffers + 8 * 2048)->pieces_full;
+    const uint32_t bytes = (uint32_t)(rows * D * 4);
+    float* inv = weights + 128 * kJoin;
+    if (tid == 224) {  // (of the idle row tile)
+        asm volatile("fence.proxy.async;" ::: "memory");  // the other CTAs' writes, seen by the arrival before
+        mbar_arrive_expect_tx(bar, bytes * (uint32_t)count);
+        for (int i = 0; i < count; ++i)
+            bulk_g2s(room + i * bytes, a.part_o + piece_slot(c, i) * a.rows * D, bytes, bar, policy_evict_first());
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int r0 = (tid >> 5) * kR; r0 < rows; r0 += kAtOnce * 8 * kR) {
+        float wt[kAtOnce][kP], part[kAtOnce][kP], m[kAtOnce], l;
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int row = min(r0 + x * 8 * kR + sub, rows - 1);
+            m[x] = -1e30f;
+#pragma unroll
+            for (int y = 0; y < kP; ++y) {
+                float2 ml = make_float2(-1e30f, 0.f);
+                if (i8 + y * kL < count) ml = __ldcg(a.part_ml + (uint32_t)(piece_slot(c, i8 + y * kL) * a.rows + row));
+                wt[x][y] = ml.x, part[x][y] = ml.y;
+                m[x] = fmaxf(m[x], ml.x);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int row = r0 + x * 8 * kR + sub;
+            if (r0 + x * 8 * kR >= rows) break;
+            weigh<kL, kP>(wt[x], part[x], i8, count, m[x], l);
+            if (row >= rows) continue;
+#pragma unroll
+            for (int y = 0; y < kP; ++y) weights[row * kJoin + i8 + y * kL] = wt[x][y];
+            if (i8 == 0) inv[row] = l != 0.f ? 1.f / l : 0.f;
+        }
+    }
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (!mbar_wait(bar, 0)) return;
+#pragma unroll 1
+    for (int at = tid; at < rows * kL; at += 256) {
+        const int row = at / kL, d = at % kL * 8, tok = kv_row_token(a, row);
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float f = weights[row * kJoin + i];
+            const float4* v = reinterpret_cast<const float4*>(room + i * bytes + (row * D + d) * 4);
+            const float4 v0 = v[0], v1 = v[1];
+            const float from[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, from[e], acc[e]);
+        }
+        *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
+                                  (long long)(w.head * a.group + row - tok * a.group) * a.o_sh + d) = pack_bf16x8(acc, inv[row]);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttnArgs a) {
     using C = PrefillCfg<D>;
@@ -134,6 +206,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         for (int i = 0; i < kPfSlots; ++i) mbar_init(sh.kv_full + i, kPfApart), mbar_init(sh.kv_empty + i, 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
+        mbar_init(&sh.pieces_full, 1);
         fence_mbar_init();
     }
     if (tid < kPfInfo) {
@@ -694,6 +767,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             tiles += cnt;
             if (!whole && !direct) {
                 join_pieces(of, joined(), lead(), &sh.join_last[two ? x : 0], meet, [&](int first, int step, int count, bool final) {
+                    const bool at_end = !two && nx.left == 0 && of.count <= kJoin;  // (no copy or product is under way then)
+                    if (at_end && count * rows_of(w) * D * 4 <= C::kPiecesRoom) {
+                        add_pieces_at_end<D>(a, w, of.c, count, rows_of(w));
+                        return;
+                    }
                     add_pieces_apart<D>(a, w, two ? warp & 3 : warp, two ? 4 : 8, two ? x * 128 : 0, two && !x ? 128 : nrows, of.c, first, step,
                                         count, final);
                 });
