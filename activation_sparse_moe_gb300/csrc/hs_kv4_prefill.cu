@@ -23,7 +23,7 @@
 // no second set of scores beside 2 x 128 columns of scores and outputs at head_dim 128), so
 // that a tile takes 3500 cycles for both; an item costs some 12,000 more: filling,
 // draining, writing.  A prompt of 4096 tokens (32 / 8 heads of 128 channels):
-// 149 us, 923 TFLOP/s, 48% of the measured bf16 peak; within long items 1340 TFLOP/s.
+// 147 us, 935 TFLOP/s, 49% of the measured bf16 peak; within long items 1340 TFLOP/s.
 #include "hs_kv4_join.cuh"
 #include "hs_tc.cuh"
 
@@ -48,11 +48,13 @@ struct PrefillCfg {
 
 struct PfShared {
     uint64_t packed_full[kPfPacked], packed_empty[kPfPacked], kv_full[kPfSlots], kv_empty[kPfSlots];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], pieces_full;
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
     uint32_t gone[kPfInfo];            // per key tile: blocks of 16 keys that are not there
     uint32_t nan_any[kPfInfo];         // some value of the tile is NaN
     uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
     uint32_t tmem;
+    // (Behind what every tile reads: before it, with those words elsewhere, chunks took 1% more.)
+    uint64_t pieces_full;
     int join_last[2];   // by row tile
     int direct[2][2];   // by end of the run (0: its first piece) and row tile: the item's other piece is there
 };
