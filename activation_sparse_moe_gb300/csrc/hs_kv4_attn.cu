@@ -586,12 +586,13 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     return HS_OK;
 }
 
-// Row tiles of 8, 16 or 32: the smallest that holds a request's rows.
+// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.
 template <int D>
 int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
     if (rows <= 8) return launch_decode<D, 1, 1, 4>(a, sms, s);
     if (rows <= 16) return launch_decode<D, 2, 1, 4>(a, sms, s);
-    return launch_decode<D, 2, 2, 4>(a, sms, s);
+    if (rows <= 32) return launch_decode<D, 2, 2, 4>(a, sms, s);
+    return launch_decode<D, 2, 4, 2>(a, sms, s);
 }
 
 }  // namespace hs
@@ -599,10 +600,14 @@ int launch_rows(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
 using namespace hs_host;
 
 // Rows of a request (new tokens x query heads of a kv head) from which the
-// chunk kernel is used.  This kernel against that one, us: 17 to 32 rows 38.9
-// and 43.5, 12.5 and 17.2, 114 and 128; 48 rows (16 requests, 32 / 2 heads, with
-// four row warps) 29.5 and 26.6.  Chunks of small batches from there on are within
-// 3 us either way (18.3 and 20.8; 13.4 and 14.6).
+// chunk kernel is used.  This kernel against that one, us: 32 rows, 16 requests
+// (32 / 2 heads) 18.2 and 20.7, one 15.8 and 26.0, 64 (32 / 8 heads) 104 and 134; 24 rows 37 and
+// 46.  With 48 rows, four row warps take the same codes apart, which costs where
+// there is much to read (16 requests, 32 / 8 heads: 56 and 41; one of 131,000
+// tokens 60 and 51) and does not where the start and the joins bound the call: one request of
+// 4096 tokens (32 / 2 heads) 22.8 and 29.1, four 25.0 and 29.2, eight of 1000 tokens 17.1 and
+// 19.2.  So up to 64 rows stay here if requests x kv heads are at most 16 and the
+// tables hold no more than 2^17 keys of them.
 constexpr int kPrefillRows = 33;
 
 // Counters of arrived pieces, (maximum, sum) pairs and partial sums of the widest launch.
@@ -656,7 +661,8 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.part_o = reinterpret_cast<float*>(w + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long need = std::max((long long)max_new, 1ll) * a.group;
-    if (need >= kPrefillRows) return hs_kv4_prefill(a, dim, sms, s);
+    const long long items = (long long)n_seqs * a.g.heads, keys = items * ((long long)a.width << a.g.page_log2);
+    if (need >= (items <= 16 && keys <= 1 << 17 ? 65 : kPrefillRows)) return hs_kv4_prefill(a, dim, sms, s);
     const int r = dim == 64 ? hs::launch_rows<64>(a, need, sms, s) : hs::launch_rows<128>(a, need, sms, s);
     return r != HS_OK ? r : launch_err();
 }
