@@ -10,9 +10,10 @@
 // group).  A code becomes an fp16 operand by masking alone: the four bits of
 // nibble 0 (of each half of a word) are the subnormal c * 2^-24 and those of
 // nibble 1 c * 2^-20, exact, five logic instructions for eight codes; the
-// powers of two go into q (per channel) and the output.  Query rows are scaled
-// by a power of two so that their largest channel is near 1: bf16 values then
-// lose nothing as fp16.
+// powers of two go into q (per channel) and the output.  Each query row is scaled
+// by the power of two that brings its largest channel near 1, whatever stands in
+// the others: bf16 values then lose nothing as fp16, unless they are 2^25 times
+// smaller than that channel.
 //
 // Bounds.  Instructions of the steps: taking 32 keys' codes apart, the products'
 // issue and the exponentials, about half the issue slots; the integer pipe is
@@ -217,14 +218,17 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         const int min_lim = ctx + tok0, max_lim = some ? ctx + tok1 : -1;
 
         // Query rows as the right operand of the first product (lane: row g, 16
-        // channels of each group), all scaled by one power of two that brings
-        // the largest channel near 1 (bf16 values down to 2^-28 of it stay exact).
+        // channels of each group), each scaled by the power of two that brings
+        // its largest channel near 1.  Channels of even nibbles come times 2^12, those
+        // of odd nibbles times 2^8: bf16 values of those keep all bits down to 2^-25 of
+        // the largest (even ones to 2^-29), and smaller ones move a score by less than
+        // 2^-33 of the largest channel's part.
         uint32_t Q[4 * NG][NQ][2];
-        float sq[NG][NQ][2], sc;
+        float sq[NG][NQ][2], sc[NQ][2];
         {
-            uint32_t top = 0;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
+                uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -233,15 +237,17 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         top = max(top, max(max((v[n][i][h].x << 16) & 0x7fffffffu, (v[n][i][h].y << 16) & 0x7fffffffu),
                                            max((v[n][i][h].z << 16) & 0x7fffffffu, (v[n][i][h].w << 16) & 0x7fffffffu)));
                     }
-            }
-            // f = 2^-e, 2^e <= largest < 2^(e+1); zeros and infinities keep f = 1
-            int e = (int)(warp_max_u32(top) >> 23);
-            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
-            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-            const float f8 = f * 4096.f, f4 = f * 256.f;  // the even nibbles stand for c * 2^-24, the odd ones for c * 2^-20
-            sc = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 4096.f;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));  // of row g
+                // f8 = 2^(12-e), 2^e <= largest < 2^(e+1); a row of zeros keeps 2^12.  The even
+                // nibbles stand for c * 2^-24, the odd ones for c * 2^-20.
+                int e = (int)(top >> 23);
+                const bool none = e >= kNoQuery;
+                e = e == 0 || none ? 0 : max(-110, e - 127);
+                const float f8 = none ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(139 - e) << 23), f4 = f8 * 0.0625f;
+                const float to_score = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 4096.f;
+                sc[n][0] = __shfl_sync(~0u, to_score, 8 * t);  // of rows 2t and 2t + 1
+                sc[n][1] = __shfl_sync(~0u, to_score, 8 * t + 4);
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
                     float sum = 0.f;
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t u[4] = {v[n][i][h].x, v[n][i][h].y, v[n][i][h].z, v[n][i][h].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sum += bf16_f32(u[j], 0) + bf16_f32(u[j], 1);
+                        for (int j = 0; j < 4; ++j) sum = fmaf(bf16_f32(u[j], 0), f8, fmaf(bf16_f32(u[j], 1), f8, sum));
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {  // nibbles (2j, 2j + 4) and (2j + 1, 2j + 5)
                             Q[(i * 2 + h) * 2 + j][n][0] = pack_half2(bf16_f32(u[j], 0) * f8, bf16_f32(u[j + 2], 0) * f8);
@@ -258,10 +264,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                     }
                     sum += __shfl_xor_sync(~0u, sum, 1);
                     sum += __shfl_xor_sync(~0u, sum, 2);
-                    sum *= f * (1.f / 4096.f);
-                    sq[i][n][0] = __shfl_sync(~0u, sum, 8 * t);      // of rows 2t and 2t + 1
+                    sum *= 1.f / 16777216.f;
+                    sq[i][n][0] = __shfl_sync(~0u, sum, 8 * t);
                     sq[i][n][1] = __shfl_sync(~0u, sum, 8 * t + 4);
                 }
+            }
         }
 
         // Lane: outputs of channels 64 i + 8 g + 2 u + (e / 2), rows 2t + e % 2.
@@ -363,7 +370,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grow |= fmaf(largest(n, e), sc, -m[n][e]) > kLazy;
+                for (int e = 0; e < 2; ++e) grow |= fmaf(largest(n, e), sc[n][e], -m[n][e]) > kLazy;
             if (__any_sync(~0u, grow || top > eb << 10)) {  // rare: a maximum passed the lag, or a scale the exponent
                 const uint32_t neb = max(eb, warp_max_u32(top) >> 10);
                 const float down = __uint_as_float((127u + eb - neb) << 23);
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         float x = largest(n, e);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-                        const float nm = fmaxf(m[n][e], x * sc), f = ex2(m[n][e] - nm);
+                        const float nm = fmaxf(m[n][e], x * sc[n][e]), f = ex2(m[n][e] - nm);
                         m[n][e] = nm;
                         l[n][e] *= f;
 #pragma unroll
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         float x[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            x[e] = ex2(fmaf(s[h][j][n][e], sc, -m[n][e]));
+                            x[e] = ex2(fmaf(s[h][j][n][e], sc[n][e], -m[n][e]));
                             l[n][e] += x[e];
                         }
 #pragma unroll

@@ -456,25 +456,30 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
             }
         };
-        // ... then put into fp16 in place, all scaled by the power of two that brings their
-        // largest channel to [2^8, 2^9): bf16 values down to 2^-22 of it stay exact, smaller
-        // ones move a score by less than 2^-33 of the largest.  Returns the scores' factor.
+        // ... then put into fp16 in place, each row scaled by the power of two that brings its
+        // largest channel to [2^8, 2^9), whatever stands in the others: bf16 values down to 2^-25
+        // of it stay exact, smaller ones move a score by less than 2^-33 of the largest channel's
+        // part.  A lane looks at its own row (eight lanes at eight places of the lines: no
+        // two in one bank).  Returns that row's factor of the scores.
         auto convert_q = [&]() -> float {
             cp_async_wait_all();
             __syncwarp();
+            const uint8_t* own = q_s + x * C::kQBytes + ((warp & 3) * 32 + lane) * 128;
             uint32_t top = 0;
 #pragma unroll 4
-            for (int i = 0; i < kB; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(q_lines + i * kAt * 128 + (c & 7) * 16);
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(own + (i >> 3) * (128 * 128) + (((i ^ lane) & 7) << 4));
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) top = max(top, max(u[j] & 0x7fff0000u, (u[j] << 16) & 0x7fff0000u));
             }
-            int e = (int)(warp_max_u32(top) >> 23);  // zeros and infinities keep the scale 1
-            e = e == 0 || e == 255 ? 0 : max(-110, min(110, e - 127));
-            const float f = __uint_as_float((uint32_t)(127 + 8 - e) << 23);
+            int e = (int)(top >> 23);
+            const bool none = e >= kNoQuery;
+            e = e == 0 || none ? 0 : max(-110, e - 127);  // a row of zeros keeps 2^8
+            const float row_f = none ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + 8 - e) << 23);
 #pragma unroll 4
             for (int i = 0; i < kB; ++i) {
+                const float f = __shfl_sync(~0u, row_f, i * kAt + sub);
                 uint8_t* line = q_lines + i * kAt * 128;
                 const uint4 v = *reinterpret_cast<const uint4*>(line + (c & 7) * 16);
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};

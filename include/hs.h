@@ -444,8 +444,10 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  *   scale       > 0 and finite;  window >= 0 (0: none)
  * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it.
  * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and
- * values (chunks) with fp16 queries scaled by a power of two, fp32 sums,
- * probabilities rounded to fp16 for the second product.
+ * values (chunks) with fp16 queries, each row scaled by a power of two of its
+ * own, fp32 sums, probabilities rounded to fp16 for the second product.  A
+ * query row that holds a NaN, an infinity or a value of 2^112 or more gives NaN
+ * where it sees a key, and no other row.
  * Deterministic.  Calls sharing one workspace must not overlap on the GPU.
  * The workspace must be ZERO-FILLED before its first use; each call leaves the
  * counters at its start at zero, so consecutive calls of any shapes and CUDA

@@ -316,6 +316,30 @@ def test_attention_query_with_one_large_channel(new, spike):
     assert (np.abs(r.run(hs, scale).float().cpu().double().numpy() - ref) <= bound * np.maximum(1, np.abs(ref))).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 7, 12, 40])
+def test_a_query_row_that_is_no_number_leaves_its_neighbours_alone(new, dim):
+    """Of each kv head's four query heads one holds a NaN, one an infinity or 2^112,
+    the others values of about 20 and 300 (past 2^16 under a common scale of 1):
+    the first two give NaN, the others what they give alone."""
+    r = _kv4.Requests(8, [200], [new], 8, 2, dim, 32)
+    kind = np.arange(8) % 4
+    q = r.q.float() * torch.from_numpy(np.array([1., 1., 20., 300.], np.float32)[kind])[None, :, None]
+    r.q = q.bfloat16()
+    scale = 0.003
+    ref = r.expected(scale)
+    q[:, kind == 0, 5] = float("nan")
+    q[:, kind == 1, 6] = float("inf")
+    q[::2, kind == 1, 6] = -2.0 ** 112
+    r.q = q.bfloat16()
+    got = r.run(hs, scale).float().cpu().double().numpy()
+    assert np.isnan(got[:, kind < 2]).all()
+    # as in test_attention_sizes_of_values, row by row
+    err_s = scale * dim ** 0.5 * np.array([20., 300.])[kind[kind > 1] - 2][None, :, None] * 2.0 ** -11
+    bound = 2.0 ** -8 * np.abs(ref[:, kind > 1]) + 6 * (2 * 2.0 ** -11 + 8 * err_s)
+    assert (np.abs(got - ref)[:, kind > 1] <= bound).all()
+
+
 def test_attention_strides_streams_and_reuse_of_the_workspace():
     r = _kv4.Requests(21, [700, 90], [2, 2], 16, 4, 128, 64)
     ref = r.expected(0.09)
