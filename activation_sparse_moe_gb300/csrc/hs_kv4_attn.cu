@@ -277,9 +277,13 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         // Exponent field of the largest value scale so far: probability * scale *
         // 2^(21 - eb) stays below 2^15.
         uint32_t eb = 0;
+        // Some row goes by another factor than its scores' own (kv_score_factor).  Those
+        // then stand in the second words of merge_ml, which are the warp's until the piece ends.
+        bool far = false;
+        float2* own_sc = merge_ml + warp * 8 * NQ + 2 * t;  // of rows 2t and 2t + 1
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            m[n][0] = m[n][1] = -1e30f;
+            m[n][0] = m[n][1] = kNoMax;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
@@ -375,6 +379,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                 const uint32_t neb = max(eb, warp_max_u32(top) >> 10);
                 const float down = __uint_as_float((127u + eb - neb) << 23);
                 eb = neb;
+                bool over = far;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -382,8 +387,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         float x = largest(n, e);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-                        const float nm = fmaxf(m[n][e], x * sc[n][e]), f = ex2(m[n][e] - nm);
+                        const float y = x * sc[n][e], nm = fmaxf(m[n][e], y), f = ex2(m[n][e] - nm);
                         m[n][e] = nm;
+                        over |= fabsf(y) >= kFarScore && y > kNoMax;  // (-infinity: the row sees no key of these)
                         l[n][e] *= f;
 #pragma unroll
                         for (int i = 0; i < NG; ++i) {
@@ -392,6 +398,23 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                             for (int u = 0; u < 4; ++u) O[i][u][n][e] *= f * down, O[i][u][n][2 + e] *= f * down;
                         }
                     }
+                if (__any_sync(~0u, over)) [[unlikely]] {  // scores far from any use: see kv_score_factor
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = largest(n, e);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+                            if (!far) own_sc[n * 8 + e].y = sc[n][e];  // (the same from a row's eight lanes)
+                            __syncwarp();
+                            if (m[n][e] == x * sc[n][e]) {
+                                sc[n][e] = kv_score_factor(x, own_sc[n * 8 + e].y);
+                                m[n][e] = x * sc[n][e];
+                            }
+                        }
+                    far = true;
+                }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -480,6 +503,13 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
                     for (int i = 0; i < NG; ++i) bs[i][n][e] += __shfl_xor_sync(~0u, bs[i][n][e], o);
                 }
+        if (far) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) m[n][e] = kv_whole_max(m[n][e], sc[n][e], own_sc[n * 8 + e].y);
+            __syncwarp();
+        }
         const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / 2^(21 - eb)
 #pragma unroll
         for (int i = 0; i < NG; ++i)
@@ -523,7 +553,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             using Vec = typename std::conditional<V == 4, float4, float2>::type;
             const int from = (row / (8 * NQ)) * KW * 8 * NQ + row % (8 * NQ);
             float2 ml[KW];
-            float top = -1e30f, sum = 0.f, acc[V];
+            float top = kNoMax, sum = 0.f, acc[V];
 #pragma unroll
             for (int i = 0; i < KW; ++i) {
                 ml[i] = merge_ml[from + i * 8 * NQ];

@@ -80,10 +80,10 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 #pragma unroll
         for (int x = 0; x < SETS; ++x) {
             row[x] = min(row0 + (s0 + x * warps) * kR + sub, row1 - 1);
-            m[x] = -1e30f;
+            m[x] = kNoMax;
 #pragma unroll
             for (int y = 0; y < kP; ++y) {
-                float2 ml = make_float2(-1e30f, 0.f);
+                float2 ml = make_float2(kNoMax, 0.f);
                 if (i8 + y * kL < count) ml = __ldcg(a.part_ml + place(i8 + y * kL, row[x]));
                 wt[x][y] = ml.x, part[x][y] = ml.y;
                 m[x] = fmaxf(m[x], ml.x);

@@ -143,10 +143,10 @@ __device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk
 #pragma unroll
         for (int x = 0; x < kAtOnce; ++x) {
             const int row = min(r0 + x * 8 * kR + sub, rows - 1);
-            m[x] = -1e30f;
+            m[x] = kNoMax;
 #pragma unroll
             for (int y = 0; y < kP; ++y) {
-                float2 ml = make_float2(-1e30f, 0.f);
+                float2 ml = make_float2(kNoMax, 0.f);
                 if (i8 + y * kL < count) ml = __ldcg(a.part_ml + (uint32_t)(piece_slot(c, i8 + y * kL) * a.rows + row));
                 wt[x][y] = ml.x, part[x][y] = ml.y;
                 m[x] = fmaxf(m[x], ml.x);
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
                 const int min_lim = -warp_max_s32(valid ? -lim : -0x7fffffff), max_lim = warp_max_s32(valid ? lim : -1);
 
-                float m = -1e30f, l = 0.f;
+                float m = kNoMax, l = 0.f;
+                const float own_sc = sc;  // (kv_score_factor)
                 uint32_t nan = 0;  // by group: the row sees a value that is NaN
                 auto see_nan = [&](int k) {  // of tile k of the piece
                     const int info = (tiles + k) % kPfInfo, key0 = (w.lo + w.tile + k) * kPfKeys;
@@ -580,8 +581,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     for (int i = 0; i < kPfKeys; i += 2) m4[(i >> 1) & 3] = fmaxf(m4[(i >> 1) & 3], fmaxf(v[i], v[i + 1]));
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (__any_sync(~0u, fmaf(mx, sc, -m) > kLazy)) {  // rare: raise the maximum and bring the sums to it
-                        const float nm = fmaxf(m, mx * sc), f = ex2(m - nm);
-                        m = nm;
+                        const float y = mx * sc, nm = fmaxf(m, y), f = ex2(m - nm);
+                        if (y > m && (sc != own_sc || fabsf(y) >= kFarScore)) {
+                            sc = kv_score_factor(mx, own_sc);
+                            m = mx * sc;
+                        } else {
+                            m = nm;
+                        }
                         l *= f;
                         if (k) {
 #pragma unroll 1
@@ -617,6 +623,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.p_full + x);
                 }
+                if (sc != own_sc) m = kv_whole_max(m, sc, own_sc);
                 if (!whole) {
                     of = kv_pieces(a, w, cum[a.n_seqs]);
                     if (of.count == 2 && lead()) {
@@ -639,7 +646,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     const uint32_t other = (w.tile == 0 ? 2 * blockIdx.x + 2 : 2 * blockIdx.x - 1) * (uint32_t)a.rows;
                     float mine = 1.f, its = 0.f;
                     if (direct) {
-                        const float2 ml = valid ? __ldcg(a.part_ml + other + r) : make_float2(-1e30f, 0.f);
+                        const float2 ml = valid ? __ldcg(a.part_ml + other + r) : make_float2(kNoMax, 0.f);
                         const float top = fmaxf(m, ml.x);
                         mine = ex2(m - top), its = ex2(ml.x - top);
                         l = __fadd_rn(__fmul_rn(mine, l), __fmul_rn(its, ml.y));

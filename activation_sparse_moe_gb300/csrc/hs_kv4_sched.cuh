@@ -15,6 +15,8 @@
 namespace hs {
 
 constexpr float kLazy = 8.f;     // a row's maximum may lag by a factor 2^8 before the sums are rescaled
+constexpr float kNoMax = -3e38f; // the maximum of a row that has seen no key
+constexpr float kFarScore = 2097152.f;  // 2^21, see kv_score_factor
 constexpr int kNoQuery = 127 + 112;  // exponent field of 2^112: a query row that reaches it, or holds no number, gives NaN
 constexpr int kKvMaxCtas = 456;  // three on each of 152 SMs
 constexpr int kKvWsRows = 2 * 152 * 256;  // rows of partial sums of the widest launch
@@ -137,6 +139,19 @@ __device__ __forceinline__ void kv_set_item(const KvAttnArgs& a, KvWalk& w) {
     const KvSpan s = kv_span(a, w.n, w.len, w.r);
     w.lo = s.lo, w.hi = s.hi, w.tiles = kv_span_tiles(s), w.units = w.tiles + a.pad;
 }
+
+// An exponent is one fused operation on a dot product, the scores' factor sc and
+// the row's maximum, which is rounded: from 2^24 on the exponents would be off by
+// whole units and the probabilities leave the fp16 range.  So a row whose
+// maximum is the dot product x, 2^21 and more times sc, goes by a power of two
+// that brings it to [2^20, 2^21): products and maximum are then exact, and what that levels
+// out (2^-20 of the scores) is of the size of their own rounding in fp32.
+__device__ __forceinline__ float kv_score_factor(float x, float sc) {
+    const int fx = (int)((__float_as_uint(x) >> 23) & 255u), fs = (int)((__float_as_uint(sc) >> 23) & 255u);
+    return fx + fs - 254 <= 20 ? sc : __uint_as_float((uint32_t)max(254 + 20 - fx, 1) << 23);
+}
+// A row's maximum as the joins take it: by the scores' own factor.
+__device__ __forceinline__ float kv_whole_max(float m, float sc, float own_sc) { return fminf(fmaxf(m / sc * own_sc, kNoMax), -kNoMax); }
 
 // The cut of the line: the first `more` of `active` CTAs take q + 1 units, the others q.
 struct KvCut {

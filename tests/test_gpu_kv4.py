@@ -340,6 +340,56 @@ def test_a_query_row_that_is_no_number_leaves_its_neighbours_alone(new, dim):
     assert (np.abs(got - ref)[:, kind > 1] <= bound).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 7, 12, 40])
+def test_query_rows_of_very_different_sizes(new, dim):
+    """Rows 2^30 times smaller than their neighbours keep all their bits: their
+    scores, of a few units at this scale, are those that they have alone."""
+    r = _kv4.Requests(9, [200], [new], 8, 2, dim, 32)
+    small = np.arange(8) % 4 > 1
+    size = np.where(small, 2.0 ** -30, 1.0).astype(np.float32)
+    r.q = (r.q.float() * torch.from_numpy(size)[None, :, None]).bfloat16()
+    scale = 0.09 * 2.0 ** 30
+    ref = r.expected(scale)
+    got = r.run(hs, scale).float().cpu().double().numpy()
+    assert np.isfinite(got).all()
+    err_s = 0.09 * dim ** 0.5 * 2.0 ** -11  # of the small rows; the others' softmax is one key's
+    bound = 2.0 ** -8 * np.abs(ref[:, small]) + 6 * (2 * 2.0 ** -11 + 8 * err_s)
+    assert (np.abs(got - ref)[:, small] <= bound).all()
+
+
+@pytest.mark.parametrize("scale", [1e3, 1e30])
+@pytest.mark.parametrize("sign", [0, -1])
+@pytest.mark.parametrize("new,hq,dim", [(1, 2, 64), (1, 8, 128), (3, 8, 128), (7, 8, 64), (12, 8, 128), (40, 8, 128), (40, 8, 64)])
+def test_scores_far_past_the_exponents_range(scale, sign, new, hq, dim):
+    """Scores of 1e9 and 1e36 units, of both signs or all negative: the softmax is
+    that of one key, and the output its value, wherever no other key comes near it."""
+    def edit(i, k, v):
+        if sign:
+            k[:] = -np.abs(k)
+    r = _kv4.Requests(10, [500], [new], hq, 2, dim, 16, k_size=30.0, edit=edit)
+    q = r.q.float() * 1e4
+    r.q = (q.abs() if sign else q).bfloat16()
+    got = r.run(hs, scale).float().cpu().double().numpy()
+    assert np.isfinite(got).all()
+    q, seen = r.q.double().numpy(), 0
+    for i in range(new):
+        n = r.len[0] - new + i + 1
+        for h in range(hq):
+            k, v = r.k[0][:n, h // (hq // 2)], r.v[0][:n, h // (hq // 2)]
+            s = k @ q[i, h]
+            # keys rounded to fp16 in chunks (2^-11 of each product) and fp32 sums (2^-20 of the products' sizes at most)
+            err = (np.abs(k) @ np.abs(q[i, h])).max() * (2.0 ** -11 + 2.0 ** -20)
+            order = np.argsort(s)
+            if s[order[-1]] - s[order[-2]] <= 2 * err:
+                continue
+            seen += 1
+            # the value, fp16-rounded in chunks, and its rounding to bf16
+            top = v[order[-1]]
+            assert (np.abs(got[i, h] - top) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(top) + 2.0 ** -12).all()
+    assert seen >= new * hq // 3
+
+
 def test_attention_strides_streams_and_reuse_of_the_workspace():
     r = _kv4.Requests(21, [700, 90], [2, 2], 16, 4, 128, 64)
     ref = r.expected(0.09)
