@@ -9,6 +9,7 @@ namespace hs {
 
 constexpr int kKvMaxSeqs = 4096;
 constexpr int kKvMaxTokens = 1 << 20;   // tokens of one append or read
+constexpr long long kKvMaxKeys = (1ll << 31) - (1 << 13);  // of a table's row: the loads look some 4000 keys ahead in 32 bits
 
 struct KvGeom {
     uint8_t* pool;

@@ -209,13 +209,14 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
     while (w.left > 0) {
         const int cnt = kv_piece_tiles(w);
         const int ctx = w.len - w.n;
-        // the warp's rows see no key past max_lim or before min_lim - back_keys, and all
-        // of those from max_lim - back_keys to min_lim
-        const int row0 = rt * 8 * NQ, back_keys = a.window ? a.window - 1 : 0x3fffffff;
+        // the warp's rows see no key past max_lim or before back_min, and all of those from
+        // back_max to min_lim
+        const int row0 = rt * 8 * NQ, back_keys = a.back;
         const int tok0 = w.r * a.tq + kv_row_token(a, row0);
         const int tok1 = min(w.r * a.tq + kv_row_token(a, min(row0 + 8 * NQ - 1, a.tq * a.group - 1)), w.n - 1);
         const bool some = row0 < a.tq * a.group && tok0 < w.n;
         const int min_lim = ctx + tok0, max_lim = some ? ctx + tok1 : -1;
+        const int back_min = max(min_lim, 0) - back_keys, back_max = max(max_lim, 0) - back_keys;  // (no position before 0: no overflow)
 
         // Query rows as the right operand of the first product (lane: row g, 16
         // channels of each group), each scaled by the power of two that brings
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                             if (MASKED) {
                                 const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + kv_row_token(a, row);
                                 const int key = key0 + 16 * h + 8 * j + kr;
-                                if (key > lim || key < lim - back_keys || ((none >> h) & 1u)) v = -INFINITY;
+                                if (key > lim || key < max(lim, 0) - back_keys || ((none >> h) & 1u)) v = -INFINITY;
                             }
                             s[h][j][n][e] = v;
                         }
@@ -480,9 +481,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             // sums; it still meets the others where they wait for it.
             if (phase < 2 && !mbar_wait(full + slot, phase)) phase |= 2;
             if (phase >= 2) continue;
-            if (none != 3u && key0 <= max_lim && key0 + kKvStep > min_lim - back_keys) {
+            if (none != 3u && key0 <= max_lim && key0 + kKvStep > back_min) {
                 const uint8_t* rec = ring + slot * C::kSlotBytes;
-                if (none || key0 + kKvStep - 1 > min_lim || key0 < max_lim - back_keys)
+                if (none || key0 + kKvStep - 1 > min_lim || key0 < back_max)
                     step32(std::true_type(), rec, key0, none);
                 else
                     step32(std::false_type(), rec, key0, none);
@@ -670,7 +671,7 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
         window < 0 || !(scale > 0.f) || scale > 1e30f)
         return HS_ERR_INVALID_ARG;
     if (n_q_heads < cache->n_kv_heads || n_q_heads % cache->n_kv_heads || n_q_heads / cache->n_kv_heads > 64 ||
-        n_seqs > hs::kKvMaxSeqs || (long long)table_width * cache->page_tokens >= (1ll << 31))
+        n_seqs > hs::kKvMaxSeqs || (long long)table_width * cache->page_tokens > hs::kKvMaxKeys)
         return HS_ERR_UNSUPPORTED_SHAPE;
     if (!al16(q) || !al16(out) || (q_st | q_sh | o_st | o_sh) & 7 || !al4(q_start) || !al4(seq_len) || !al4(table))
         return HS_ERR_MISALIGNED;
@@ -690,7 +691,7 @@ extern "C" int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q, lo
     a.width = table_width, a.n_seqs = n_seqs, a.n_tokens = n_tokens;
     a.group = n_q_heads / cache->n_kv_heads;
     a.group_inv = (65536u + (uint32_t)a.group - 1u) / (uint32_t)a.group;
-    a.window = window;
+    a.back = window ? window - 1 : INT32_MAX;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.joined = reinterpret_cast<int*>(w);
     w += round_up(3 * hs::kKvMaxCtas * 4, 256);

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         // ---- a row tile's queries, softmax and output, a thread a row
         const int x = warp >> 2, row = tid & 127, r = x * 128 + row;
         const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-        const int back_keys = a.window ? a.window - 1 : 0x3fffffff;
+        const int back_keys = a.back;  // taken off no position before 0: no overflow
         uint32_t tiles = 0, s_count = 0, o_count = 0;
         bool dead = false;
         // The warp's 32 rows of a piece's queries, a row by D / 8 lanes: fetched as they are
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     for (int i = 0; i < NG * 4; ++i)
                         for (uint32_t b = sh.nan_keys[info][i >> 2][i & 3]; b; b &= b - 1) {
                             const int key = key0 + (i & 3) * 32 + __ffs(b) - 1;
-                            if (key <= lim && key >= lim - back_keys) nan |= 1u << (i >> 2);
+                            if (key <= lim && key >= max(lim, 0) - back_keys) nan |= 1u << (i >> 2);
                         }
                 };
                 for (int k = 0; k < cnt && !dead; ++k) {
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     if (k == cnt - 1 && more) fetch_q(nx);  // the last scores are there: the queries' place is free
                     if (k) see_nan(k - 1);  // its values have been taken apart: its product is done
                     const uint32_t gone = sh.gone[(tiles + k) % kPfInfo];
-                    const bool masked = gone || key0 + kPfKeys - 1 > min_lim || key0 < max_lim - back_keys;
+                    const bool masked = gone || key0 + kPfKeys - 1 > min_lim || key0 < max(max_lim, 0) - back_keys;
                     float v[kPfKeys];
 #pragma unroll
                     for (int c = 0; c < kPfKeys / 32; ++c) tmem_ld32_async(tl + x * 128 + c * 32, v + c * 32);
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
 #pragma unroll
                         for (int i = 0; i < kPfKeys; ++i) {
                             const int key = key0 + i;
-                            if (key > lim || key < lim - back_keys || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
+                            if (key > lim || key < max(lim, 0) - back_keys || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
                         }
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

@@ -30,7 +30,8 @@ struct KvAttnArgs {
     const int* q_start;
     const int* seq_len;
     const int* table;
-    int width, n_seqs, n_tokens, group, window, rows, tq, min_units, pad, tile_log2;
+    int width, n_seqs, n_tokens, group, rows, tq, min_units, pad, tile_log2;
+    int back;            // a row at position p >= 0 sees the keys from p - back on: window - 1, or all of int
     uint32_t group_inv;  // ceil(2^16 / group)
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [2 * CTAs][rows][dim] partial sums
@@ -49,7 +50,7 @@ struct KvSpan {
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs& a, int n, int len, int r) {
     const int ctx = len - n, t0 = r * a.tq, t1 = min(n, t0 + a.tq) - 1;
     const int last = min(ctx + t1, len - 1);
-    const int first = a.window ? max(0, ctx + t0 - a.window + 1) : 0;
+    const int first = max(0, max(ctx + t0, 0) - a.back);
     KvSpan s;
     if (last < 0 || first > last) {
         s.lo = 0, s.hi = -1;

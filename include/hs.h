@@ -442,7 +442,8 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  *   max_new     the largest number of new tokens of a request, or more: it
  *               chooses the kernel, not the result
  *   scale       > 0 and finite;  window >= 0 (0: none)
- * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it.
+ * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it;
+ * table_width * page_tokens at most 2^31 - 2^13.
  * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and
  * values (chunks) with fp16 queries, each row scaled by a power of two of its
  * own, fp32 sums, probabilities rounded to fp16 for the second product.  A

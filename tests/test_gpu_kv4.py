@@ -268,6 +268,59 @@ def test_attention_rows_and_pages_that_are_not_there(new):
     _close(r.run(hs, 0.1), r.expected(0.1), 0.1)
 
 
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 1 << 30])
+@pytest.mark.parametrize("new,dim", [(3, 128), (5, 64), (100, 128)])
+def test_windows_of_any_size_and_rows_before_position_zero(new, dim, window):
+    """A window past every length hides nothing, in a row tile that holds rows at
+    negative positions too."""
+    r = _kv4.Requests(4, [0, 70], [new, new], 8, 2, dim, 32)
+    r.len[0] = new // 2
+    r.k[0], r.v[0] = r.k[0][:new // 2], r.v[0][:new // 2]
+    _close(r.run(hs, 0.1, window), r.expected(0.1), 0.1)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_contexts_past_two_to_the_thirty_without_a_window(new):
+    """2^30 + 2^16 cached tokens, all in two pages: the oldest 2^16 tokens stand in
+    one, whose keys lie nearer to the queries by as much as the others are more."""
+    page, dim, old = 64, 64, 1 << 10
+    length = (1 << 30) + (1 << 16) + 7
+    rng = np.random.default_rng(12)
+    q = _kv4.bf16(rng, (new, 1, dim))
+    u = q.double().numpy()[:, 0].mean(0)
+    u *= 1 / np.abs(u).max()
+    q = torch.from_numpy(u[None, None] + rng.normal(0, 0.02, (new, 1, dim))).bfloat16()
+    scale, k, v = 0.125, rng.normal(0, 0.2, (2 * page, 1, dim)), rng.normal(0, 1, (2 * page, 1, dim))
+    k[:page, 0] += u * (14 * np.log(2) / scale / (u @ u))
+    v[:page] += 2
+    v[page:] -= 2
+    k, v = (torch.from_numpy(x.astype(np.float32)).bfloat16() for x in (k, v))
+    pool, c = _cache(2, page, 1, dim)
+    slots = torch.arange(2 * page, device="cuda")
+    hs.hs_kv4_append(c, k.cuda(), v.cuda(), slots, 2 * page)
+    table = torch.ones((1, -(-length // page)), dtype=torch.int32, device="cuda")
+    table[0, :old] = 0
+    out = torch.empty_like(q, device="cuda")
+    ws = torch.zeros(hs.hs_kv4_attention_workspace_size(c, 1, 1), dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    hs.hs_kv4_attention(c, q.cuda(), i32([0, new]), i32([length]), table, 1, new, scale, 0, out, ws)
+    torch.cuda.synchronize()
+    assert hs.hs_device_status() == hs.HS_OK
+    kk, vv, qq = _kv4.values(k.float().numpy())[:, 0], _kv4.values(v.float().numpy())[:, 0], q.double().numpy()[:, 0]
+    ref = np.zeros((new, 1, dim))
+    for i in range(new):
+        seen = length - new + i + 1
+        pages, rest = divmod(seen, page)
+        times = np.concatenate((np.full(page, old), pages - old + (np.arange(page) < rest))).astype(float)
+        s = kk @ qq[i] * scale
+        e = times * np.exp(s - s.max())
+        assert 0.2 < e[:page].sum() / e.sum() < 0.8
+        ref[i, 0] = e / e.sum() @ vv
+    # roundings as in _close, and 2^30 / 16 / 152 products added in turn, each sum cut off at 2^-23 of it at worst
+    bound = np.abs(ref) * 2.0 ** -8 + 6 * (2.0 ** -11 * 8.4 + (1 << 30) / 16 / 152 * 2.0 ** -23)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
 @pytest.mark.parametrize("new", [1, 3, 70])
 def test_nan_in_hidden_places_does_not_spread(new):
     """NaN keys and values behind the causal border or before the window reach

@@ -114,6 +114,16 @@ def test_attention_refusals(lib):
         assert hs.hs_kv4_attention_workspace_size(*bad) == 0
 
 
+def test_attention_refuses_tables_whose_keys_leave_no_room_in_32_bits(lib):
+    need = hs.hs_kv4_attention_workspace_size(_cache(page=16, heads=1), 1, 1)
+
+    def call(width):
+        return lib.hs_kv4_attention(C.byref(_cache(page=16, heads=1)), A, 128, 128, A, A, A, width, 1, 0, 1, 1, 0.1, 0, A, 128, 128,
+                                    A, need, None)
+    assert call((1 << 27) - (1 << 9)) == hs.HS_OK                    # (no token: no launch)
+    assert call((1 << 27) - (1 << 9) + 1) == call((1 << 27) - 1) == hs.HS_ERR_UNSUPPORTED_SHAPE
+
+
 def test_binding_wants_contiguous_channels(lib):
     import torch
     k = torch.zeros(4, 2, 256).bfloat16()[:, :, ::2]
