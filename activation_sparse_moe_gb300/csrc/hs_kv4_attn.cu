@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                             float y[2];
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const bool hide = MASKED && x[e] == 0.f;  // a key that the row does not see may hold a NaN
+                                const bool hide = MASKED && s[h][j][n][e] == -INFINITY;  // a key that the row does not see may hold a NaN
                                 bs[i][n][e] = hide ? bs[i][n][e] : fmaf(x[e], p[i].y, bs[i][n][e]);
                                 y[e] = hide ? 0.f : x[e] * p[i].x;
                             }

@@ -337,6 +337,26 @@ def test_nan_in_hidden_places_does_not_spread(new):
         _close(torch.from_numpy(got[:-1]), ref[:-1], 0.1)
 
 
+@pytest.mark.parametrize("new", [1, 3, 70])
+@pytest.mark.parametrize("far", [0, 40])
+@pytest.mark.parametrize("where", [3, 199])
+def test_a_visible_nan_value_reaches_its_rows_however_unlikely_its_key(new, far, where):
+    """A value is NaN, in a step that all rows see whole or in the one where the rows'
+    borders begin; with far > 0 its key's probability vanishes in fp32.  Every row sees
+    it, and is NaN in its 64 channels and in them alone."""
+    def edit(i, k, v):
+        k[:] = np.abs(k)
+        if far:
+            k[where] = -far
+        v[where, :, 64:] = np.nan
+    r = _kv4.Requests(13, [200], [new], 4, 2, 128, 16, edit=edit)
+    r.q = r.q.abs()
+    got = r.run(hs, 0.1).float().cpu().double().numpy()
+    assert np.isnan(got[..., 64:]).all()
+    r.v[0] = np.nan_to_num(r.v[0])
+    _close(torch.from_numpy(got[..., :64]), r.expected(0.1)[..., :64], 0.1)
+
+
 @pytest.mark.parametrize("k_size,v_size,q_size", [(30., 1., 1.), (1., 300., 1.), (1., 1e-4, 1.), (1e-3, 1., 1e4), (1., 1., 1e-20)])
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_sizes_of_values(k_size, v_size, q_size, new):
