@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                 const bool none = e >= kNoQuery;
                 e = e == 0 || none ? 0 : max(-110, e - 127);
                 const float f8 = none ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(139 - e) << 23), f4 = f8 * 0.0625f;
-                const float to_score = a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 4096.f;
+                const float to_score = kv_score_range(a.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * 4096.f);
                 sc[n][0] = __shfl_sync(~0u, to_score, 8 * t);  // of rows 2t and 2t + 1
                 sc[n][1] = __shfl_sync(~0u, to_score, 8 * t + 4);
 #pragma unroll

@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sh.q_full + x);
-            return a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23);
+            return kv_score_range(a.scale_log2 * __uint_as_float((uint32_t)(127 - 8 + e) << 23));
         };
         float sc = 0.f;
         if (w.left > 0 && x * 128 < rows_of(w)) {

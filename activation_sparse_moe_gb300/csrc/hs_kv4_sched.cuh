@@ -151,6 +151,8 @@ __device__ __forceinline__ float kv_score_factor(float x, float sc) {
     const int fx = (int)((__float_as_uint(x) >> 23) & 255u), fs = (int)((__float_as_uint(sc) >> 23) & 255u);
     return fx + fs - 254 <= 20 ? sc : __uint_as_float((uint32_t)max(254 + 20 - fx, 1) << 23);
 }
+// Kept off 0 and infinity, which make NaN of a hidden key (0 times -infinity) or of a product that is 0.
+__device__ __forceinline__ float kv_score_range(float sc) { return fminf(fmaxf(sc, 1.2e-38f), 1e38f); }
 // A row's maximum as the joins take it: by the scores' own factor.
 __device__ __forceinline__ float kv_whole_max(float m, float sc, float own_sc) { return fminf(fmaxf(m / sc * own_sc, kNoMax), -kNoMax); }
 

@@ -441,7 +441,8 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  *   table_dev   [n_seqs][table_width]; a length past table_width pages is cut
  *   max_new     the largest number of new tokens of a request, or more: it
  *               chooses the kernel, not the result
- *   scale       > 0 and finite;  window >= 0 (0: none)
+ *   scale       > 0, at most 10^30 (scores past the fp32 range say nothing);
+ *   window      >= 0 (0: none)
  * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it;
  * table_width * page_tokens at most 2^31 - 2^13.
  * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and

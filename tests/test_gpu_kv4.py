@@ -463,6 +463,22 @@ def test_scores_far_past_the_exponents_range(scale, sign, new, hq, dim):
     assert seen >= new * hq // 3
 
 
+@pytest.mark.parametrize("scale,q_size", [(1e-30, 1e-20), (1e-38, 1e-30), (1e30, 3e4), (1e30, 1e5)])
+@pytest.mark.parametrize("new", [1, 3, 12, 40])
+def test_scales_at_the_ends_of_their_range(scale, q_size, new):
+    """Scores of nothing: the mean of the visible values, hidden keys and absent rows
+    apart.  Scores of -10^36 and more, one key far above the others: its value."""
+    def edit(i, k, v):
+        k[:] = -10 - np.abs(k)
+        k[17] = -0.5
+    r = _kv4.Requests(14, [90, 30], [new, 2], 8, 2, 128, 32, edit=edit)
+    r.q = ((r.q.float().abs() + 0.5) * q_size).bfloat16()
+    ref = r.expected(scale)
+    got = r.run(hs, scale).float().cpu().double().numpy()
+    # probabilities rounded to fp16 (2^-11) before their product with codes of values up to 6 wide, values too in chunks
+    assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + 6 * 2 * 2.0 ** -11).all()
+
+
 def test_attention_strides_streams_and_reuse_of_the_workspace():
     r = _kv4.Requests(21, [700, 90], [2, 2], 16, 4, 128, 64)
     ref = r.expected(0.09)
