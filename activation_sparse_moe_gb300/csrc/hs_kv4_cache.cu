@@ -397,6 +397,22 @@ extern "C" int hs_kv4_plan(const int* cached, const int* fresh, int n_seqs, int 
     const void* p8[] = {counters_in, counters_out, slot};
     for (const void* p : p8)
         if ((uintptr_t)p & 7u) return HS_ERR_MISALIGNED;
+    // What the call writes overlaps nothing else: every CTA reads the lengths, the old
+    // table and the ring while others write.  Only the table may be updated in place.
+    const long long n = n_seqs, cells = n * table_width;
+    struct Range {
+        const void* p;
+        long long bytes;
+    } const ranges[] = {{table_out, cells * 4}, {ring, n_pages * 4ll}, {seq_len, n * 4}, {q_start, (n + 1) * 4}, {slot, max_tokens * 8ll},
+                        {position, max_tokens * 4ll}, {counters_out, 16}, {short_out, 4},  // written up to here
+                        {table_in, cells * 4}, {cached, n * 4}, {fresh, n * 4}, {counters_in, 16}};
+    for (int i = 0; i < 8; ++i)
+        for (int j = i + 1; j < 12; ++j) {
+            const Range &x = ranges[i], &y = ranges[j];
+            if (!x.p || !y.p || (i == 0 && j == 8 && x.p == y.p)) continue;
+            const uintptr_t a = (uintptr_t)x.p, b = (uintptr_t)y.p;
+            if (a < b + (uintptr_t)y.bytes && b < a + (uintptr_t)x.bytes) return HS_ERR_INVALID_ARG;
+        }
     const int smem = (4 * n_seqs + 2) * (int)sizeof(int);
     if (smem > 48 * 1024) {
         const int st = set_smem_attr((const void*)hs::kv4_plan_kernel, smem);

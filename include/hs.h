@@ -391,12 +391,15 @@ size_t hs_kv4_pool_bytes(const hs_kv4_cache* cache);
  *   q_start_dev    [n_seqs + 1] first new token of each request, and the total
  *   slot_dev       [max_tokens] slots of the new tokens, -1 past the total
  *   position_dev   [max_tokens] their positions, -1 past the total; or NULL
- *   counters_out_dev [2]; must not be counters_in_dev
+ *   counters_out_dev [2]
  *   short_dev      [1]: 0, or the number of pages missing (in the ring, or past
  *                  table_width) plus tokens over max_tokens.  Then the step is
  *                  refused as a whole: no request gets a page or a token
  *                  (q_start all 0, slots -1, seq_len = cached_len); ended
  *                  requests still give their pages back.
+ * Of what the call writes (the ring among it) nothing may overlap anything else
+ * (HS_ERR_INVALID_ARG), table_out_dev as table_in_dev apart: the next step's
+ * lengths and counters are other buffers than this one's, or copies.
  * n_seqs 1..4096; n_seqs * table_width, max_tokens and n_pages below 2^30,
  * table_width * page_tokens below 2^31. */
 int hs_kv4_plan(const int* cached_len_dev, const int* new_len_dev, int n_seqs, int page_tokens, int n_pages,

@@ -56,6 +56,30 @@ def test_plan_refusals(lib):
         assert call(**{f"a{i}": A + 4}) == hs.HS_ERR_MISALIGNED
 
 
+def test_plan_refuses_outputs_that_overlap(lib):
+    """4 requests, 8 entries a row, 100 pages, 64 tokens; each buffer 4096 bytes
+    from the next.  The lengths updated in place would be read after they were written."""
+    names = "cached new n page pages table_in width ring counters_in tokens table_out seq_len q_start slot position counters_out short stream"
+    names = names.split()
+    size = dict(cached=16, new=16, table_in=128, ring=400, counters_in=16, table_out=128, seq_len=16, q_start=20, slot=512, position=256,
+                counters_out=16, short=4)
+    written = ("ring", "table_out", "seq_len", "q_start", "slot", "position", "counters_out", "short")
+    ok = {x: A + 4096 * i for i, x in enumerate(size)}
+
+    def call(**kw):
+        a = {**dict(n=4, page=64, pages=100, width=8, tokens=64, stream=None), **ok, **kw}
+        return lib.hs_kv4_plan(*(a[x] for x in names))
+    for x in written:
+        for y in size:
+            if y == x or {x, y} == {"table_in", "table_out"}:
+                continue
+            wide = 8  # both ends: y's last bytes and x's first ones, and the other way round
+            for at in (ok[x], ok[x] + (size[x] - 1) // wide * wide, ok[x] - (size[y] - 1) // wide * wide):
+                assert call(**{y: at}) == hs.HS_ERR_INVALID_ARG, (x, y, at - ok[x])
+    for at in (4, 124, -124):
+        assert call(table_out=ok["table_in"] + at) == hs.HS_ERR_INVALID_ARG
+
+
 def _bad_caches():
     yield _cache(pool=None), hs.HS_ERR_INVALID_ARG
     yield _cache(pool=A + 8), hs.HS_ERR_MISALIGNED
