@@ -4,10 +4,10 @@
 
 #include <cuda_runtime.h>
 #include <cstring>
-#include <mutex>
 
 #include "hs.h"
 #include "hs_kernels.cuh"
+#include "hs_smem_attr.h"
 
 namespace hs_host {
 
@@ -31,25 +31,6 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-// Raises a kernel's dynamic shared memory limit once per (kernel, device, size):
-// the attribute call is kept out of the per-call path (and out of stream capture
-// after the first eager call).
-inline int set_smem_attr(const void* fn, int bytes) {
-    struct Entry { const void* fn; int dev; int bytes; };
-    static Entry done[64];
-    static int n_done = 0;
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return HS_ERR_CUDA;
-    for (int i = 0; i < n_done; ++i)
-        if (done[i].fn == fn && done[i].dev == dev && done[i].bytes >= bytes) return HS_OK;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return HS_ERR_CUDA;
-    if (n_done < 64) done[n_done++] = Entry{fn, dev, bytes};
-    return HS_OK;
 }
 
 inline int check_expert(const hs_expert& e, int hidden, int neurons_expected) {

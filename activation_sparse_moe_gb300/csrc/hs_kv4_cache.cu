@@ -415,7 +415,7 @@ extern "C" int hs_kv4_plan(const int* cached, const int* fresh, int n_seqs, int 
         }
     const int smem = (4 * n_seqs + 2) * (int)sizeof(int);
     if (smem > 48 * 1024) {
-        const int st = set_smem_attr((const void*)hs::kv4_plan_kernel, smem);
+        const int st = set_smem_attr((const void*)hs::kv4_plan_kernel, (4 * hs::kKvMaxSeqs + 2) * (int)sizeof(int));
         if (st != HS_OK) return st;
     }
     hs::PlanArgs a = {cached, fresh,      n_seqs,    page_tokens == 16 ? 4 : page_tokens == 32 ? 5 : 6, n_pages, table_width,
