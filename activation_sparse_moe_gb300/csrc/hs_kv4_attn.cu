@@ -600,6 +600,15 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         w = coming;
         __syncwarp();
     }
+    // After a wait gave up no step was taken and no copy asked for: from `slot`, whose
+    // copies that wait was for, to in_slot (all of the ring where they are the same) they
+    // may still be under way, and the shared memory is the next CTA's.
+    if (phase >= 2) {
+        do {
+            mbar_wait(full + slot, phase & 1);
+            if (++slot == C::kSlots) slot = 0, phase ^= 1;
+        } while (slot != in_slot);
+    }
 }
 
 template <int D, int NQ, int RT, int KW>

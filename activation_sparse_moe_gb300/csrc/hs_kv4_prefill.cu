@@ -54,7 +54,7 @@ struct PfShared {
     uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
     uint32_t tmem;
     // (Behind what every tile reads: before it, with those words elsewhere, chunks took 1% more.)
-    uint64_t pieces_full;
+    uint64_t pieces_full, products_done;
     int join_last[2];   // by row tile
     int direct[2][2];   // by end of the run (0: its first piece) and row tile: the item's other piece is there
 };
@@ -164,7 +164,10 @@ __device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk
         }
     }
     asm volatile("bar.sync 3, 256;" ::: "memory");
-    if (!mbar_wait(bar, 0)) return;
+    if (!mbar_wait(bar, 0)) {
+        mbar_wait(bar, 0);  // once more: the copies under way write into this CTA's shared memory
+        return;
+    }
 #pragma unroll 1
     for (int at = tid; at < rows * kL; at += 256) {
         const int row = at / kL, d = at % kL * 8, tok = kv_row_token(a, row);
@@ -209,6 +212,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         for (int i = 0; i < 2; ++i)
             mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
         mbar_init(&sh.pieces_full, 1);
+        mbar_init(&sh.products_done, 1);
         fence_mbar_init();
     }
     if (tid < kPfInfo) {
@@ -284,6 +288,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 }
             }
         }
+        // Where a wait gave up, here or in the warps that use the copies, the last ones may
+        // still be under way; the CTA stays until they have come.
+        for (uint32_t i = f > kPfPacked ? f - kPfPacked : 0; i < f; ++i) mbar_wait(sh.packed_full + i % kPfPacked, (i / kPfPacked) & 1);
     } else if (warp == 13) {
         // ---- matrix products, issued by one lane
         constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kPfKeys);
@@ -350,6 +357,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             }
             next_piece();
         }
+        // The products read shared memory and write tensor memory, which is given back below.
+        if (elect_one()) umma_commit(&sh.products_done);
+        __syncwarp();
+        mbar_wait(&sh.products_done, 0);
     } else {
         // ---- codes taken apart into swizzled fp16 tiles
         const int idx = (warp < 12 ? warp - 8 : warp - 10) * 32 + lane;  // of 192
