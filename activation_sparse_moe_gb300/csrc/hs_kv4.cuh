@@ -36,6 +36,20 @@ __device__ __forceinline__ void bulk_g2s_to(uint32_t dst, const void* src, uint3
         : "memory");
 }
 
+// mbar_wait by a whole warp: it gives up as one, where its lanes would run out of
+// patience one by one and come to its next vote or shuffle in parts.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) [[likely]] return true;
+    const unsigned long long t0 = clock64();
+    while (!__all_sync(~0u, mbar_try_wait(bar, parity))) {
+        if (__any_sync(~0u, clock64() - t0 > kWaitLimitCycles)) {
+            atomicOr(&g_status, 1u);
+            return false;
+        }
+    }
+    return true;
+}
+
 // True in one lane of the (converged) warp; the compiler then knows the branch
 // to be taken by one thread, and keeps the operands in uniform registers.
 __device__ __forceinline__ bool elect_one() {

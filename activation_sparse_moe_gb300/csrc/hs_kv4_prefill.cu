@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 const unsigned mask = __ballot_sync(~0u, here);
                 for (int v = 0; v < 2; ++v, ++f) {
                     const int st = f % kPfPacked;
-                    if (f >= kPfPacked && !mbar_wait(sh.packed_empty + st, (f / kPfPacked + 1) & 1)) {
+                    if (f >= kPfPacked && !warp_wait(sh.packed_empty + st, (f / kPfPacked + 1) & 1)) {
                         dead = true;
                         break;
                     }
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         const uint32_t q_at = smem_u32(q_s), kv_at = smem_u32(kv_s);
         uint32_t slot = 0, phase = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};  // slot: of the next K tile
         bool dead = false;
-        auto wait = [&](uint64_t* bar, uint32_t parity) { dead |= !__all_sync(~0u, mbar_wait(bar, parity)); };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { dead |= !warp_wait(bar, parity); };
         while (w.left > 0 && !dead) {
             const int cnt = (int)warp_max_u32((uint32_t)kv_piece_tiles(w));
             const bool two = warp_max_u32((uint32_t)rows_of(w)) > 128u;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 const int key0 = (w.lo + w.tile + k) * kPfKeys, info = tiles % kPfInfo;
                 for (int v = 0; v < 2; ++v, ++f) {
                     const int st = f % kPfPacked, slot = f % kPfSlots;
-                    if (!mbar_wait(sh.packed_full + st, (f / kPfPacked) & 1)) {
+                    if (!warp_wait(sh.packed_full + st, (f / kPfPacked) & 1)) {
                         dead = true;
                         break;
                     }
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                             }
                         }
                     }
-                    if (f >= kPfSlots && !mbar_wait(sh.kv_empty + slot, (f / kPfSlots + 1) & 1)) {
+                    if (f >= kPfSlots && !warp_wait(sh.kv_empty + slot, (f / kPfSlots + 1) & 1)) {
                         dead = true;
                         break;
                     }
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 };
                 for (int k = 0; k < cnt && !dead; ++k) {
                     const int key0 = (w.lo + w.tile + k) * kPfKeys;
-                    if (!mbar_wait(sh.s_full + x, s_count++ & 1)) {
+                    if (!warp_wait(sh.s_full + x, s_count++ & 1)) {
                         dead = true;
                         break;
                     }
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 }
                 // The next piece's first scores are worked out while this one is written.
                 const float next_sc = more ? convert_q() : 0.f;
-                if (!dead && !mbar_wait(sh.o_full + x, o_count++ & 1)) dead = true;
+                if (!dead && !warp_wait(sh.o_full + x, o_count++ & 1)) dead = true;
                 direct = other_is_there();
                 if (!dead) {
                     tc_fence_after();

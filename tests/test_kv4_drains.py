@@ -116,3 +116,18 @@ def test_every_wait_is_bounded(name):
     src = _squeeze(name)
     assert "mbarrier.try_wait" not in src and "mbarrier.test_wait" not in src  # only through mbar_wait, which gives up
     assert not re.search(r"while \(!mbar_(try_wait|test)", src)
+
+
+def test_a_warp_gives_up_as_one():
+    """Lanes run out of patience one by one; a warp in which some have and some have
+    not would meet its next vote or shuffle in parts and hang there.  So what a wait
+    returns decides only by way of a vote; the ones at a warp's end decide nothing."""
+    wait = _squeeze("hs_kv4.cuh").split("bool warp_wait(")[1].split("True in one lane")[0]
+    assert wait.count("mbar_try_wait(") == wait.count("__all_sync(~0u, mbar_try_wait(bar, parity))") == 2
+    assert "if (__any_sync(~0u, clock64() - t0 > kWaitLimitCycles)) { atomicOr(&g_status, 1u); return false; }" in wait
+    for name, decided in (("hs_kv4_attn.cu", 0), ("hs_kv4_prefill.cu", 1)):
+        src = _squeeze(name)
+        uses = [m.start() for m in re.finditer(r"\bmbar_wait\(", src)]
+        assert uses
+        # a statement of its own, but for the one of add_pieces_at_end, which returns at once
+        assert sum(1 for at in uses if not re.search(r"[;{})] $", src[:at])) == decided, name
