@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(const AppendArgs a) {
                 }
             }
             if (g0 + j * a.r.abreast >= u.end || u.slot < 0) continue;
+            // Two stores: of tokens with one slot the codes of one and the pair of the other may stay
+            // (one owner a slot would take a search of the slots, or a lock a group).
             reinterpret_cast<uint32_t*>(codes)[lane8] = word;
             if (lane8 == 0) *reinterpret_cast<uint32_t*>(pair) = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
         }

@@ -412,8 +412,10 @@ int hs_kv4_plan(const int* cached_len_dev, const int* new_len_dev, int n_seqs, i
  * code = clamp(rint((x - bias) / scale), 0, 15) (0 where scale = 0), each step
  * in fp32, round to nearest even, as hs_requant_down_rowscale.  A group that
  * holds a NaN or a value of 65536 or more (past the fp16 range) reads back as
- * NaN.  A slot outside the pool (such as -1) is skipped.  Two
- * tokens with the same slot leave one of the two in it, group by group.
+ * NaN.  A slot outside the pool (such as -1) is skipped.  A slot may
+ * stand once among the tokens (hs_kv4_plan gives none twice): what a slot given
+ * to tokens of different values holds afterwards is undefined, for codes and
+ * pairs are written by themselves; other slots are not touched by it.
  *   k_bf16_dev, v_bf16_dev  bf16, token t and head h at t * stride_token +
  *     h * stride_head elements (K and V each their own strides), channels
  *     contiguous; 16-byte aligned, strides multiples of 8

@@ -148,6 +148,30 @@ def test_append_writes_the_definition_bit_for_bit_and_read_returns_it(t, hkv, di
         assert torch.equal(torch.isnan(b), torch.isnan(f))
 
 
+def test_append_of_a_slot_given_twice_touches_no_other():
+    """What such a slot holds is undefined where its tokens differ; where they are
+    equal it holds them, and every other slot holds its own token bit for bit."""
+    page, hkv, dim, t = 16, 3, 128, 400
+    rng = np.random.default_rng(5)
+    pool, c = _cache(32, page, hkv, dim)
+    k, v = _kv4.bf16(rng, (t, hkv, dim)), _kv4.bf16(rng, (t, hkv, dim))
+    slots = rng.permutation(32 * page)[:t]
+    slots[100:200] = slots[7]                       # 101 tokens of different values
+    slots[200:250], k[200:250], v[200:250] = slots[8], k[8], v[8]
+    hs.hs_kv4_append(c, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda(), t)
+    keep = np.r_[0:7, 8:100, 250:t]
+    want = np.full(pool.shape, 0xFF, np.uint8)
+    _kv4.fill_pool(want, page, dim, slots[keep], k[keep].float().numpy(), v[keep].float().numpy())
+    got = pool.cpu().numpy()
+    p, o = divmod(int(slots[7]), page)
+    for a in (got, want):
+        half, pairs = page * dim // 2, page * dim // 16
+        for x in (0, 1):
+            a[p, :, x * half + o * (dim // 2):x * half + (o + 1) * (dim // 2)] = 0
+            a[p, :, 2 * half + x * pairs + o * (dim // 16):2 * half + x * pairs + (o + 1) * (dim // 16)] = 0
+    assert np.array_equal(got, want)
+
+
 def test_append_skips_slots_outside_the_pool_and_zero_tokens():
     pool, c = _cache(3, 16, 2, 64)
     k = torch.full((4, 2, 64), float("nan"), device="cuda").bfloat16()

@@ -87,6 +87,30 @@ def _bad_caches():
         yield _cache(**bad), hs.HS_ERR_UNSUPPORTED_SHAPE
 
 
+def test_plan_gives_no_slot_twice_and_the_header_asks_for_that():
+    """The append of a slot given twice is undefined: the plan must not ask for it."""
+    rng = np.random.default_rng(6)
+    for _ in range(20):
+        n, page, width = int(rng.integers(1, 30)), int(rng.choice([16, 32, 64])), 12
+        cached = rng.integers(0, 4 * page, n)
+        new = rng.integers(-1, 5 * page, n)
+        have = -(-cached // page)
+        need = int(sum(-(-(c + f) // page) - h for c, f, h in zip(cached, new, have) if f >= 0))
+        pages = rng.permutation(int(have.sum()) + need + 3).astype(np.int32)
+        table = np.full((n, width), -1, np.int32)
+        at = 0
+        for i in range(n):
+            table[i, :have[i]] = pages[at:at + have[i]]
+            at += have[i]
+        ring = np.concatenate((pages[at:], np.full(at, -1, np.int32)))
+        r = _kv4.plan(cached, new, page, len(pages), table, ring, [0, len(pages) - at], int(new.clip(0).sum()) + 1)
+        slots = [s for s in r["slot"] if s >= 0]
+        assert r["short"] == 0 and len(set(slots)) == len(slots) == int(new.clip(0).sum())
+    text = " ".join(open(hs.HEADER).read().replace("\n *", " ").split())
+    assert "what a slot given to tokens of different values holds afterwards is undefined" in text
+    assert "leave one of the two in it" not in text
+
+
 def test_append_and_read_refusals(lib):
     def app(c, k=A, ks=256, kh=128, v=A, vs=256, vh=128, s=A, n=4):
         return lib.hs_kv4_append(C.byref(c) if c else None, k, ks, kh, v, vs, vh, s, n, None)
