@@ -289,19 +289,12 @@ def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
 
 
 # The key/value cache's calls are made for every layer of every token, so their
-# marshalling is kept short: pointers and strides straight from the tensors.
-def hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, table_width, ring, counters_in,
-                max_tokens, table_out, seq_len, q_start, slot, position, counters_out, short, stream=None):
-    st = lib().hs_kv4_plan(
-        cached_len.data_ptr(), new_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width,
-        ring.data_ptr(), counters_in.data_ptr(), max_tokens, table_out.data_ptr(), seq_len.data_ptr(),
-        q_start.data_ptr(), slot.data_ptr(), _p(position), counters_out.data_ptr(), short.data_ptr(),
-        _kv4_stream(stream))
-    if st:
-        raise HsError("hs_kv4_plan", st)
-
-
-_current = None  # torch's own lookups of the current device and its raw stream
+# marshalling is kept short (as called they take as long as the smallest steps do
+# on the GPU): pointers and strides straight from the tensors, and one look at
+# what the pointers would not tell the library: shapes against the cache and the
+# sizes, the slots' type, rows that do not follow one another.
+_current = None   # torch's own lookups of the current device and its raw stream
+_i64 = None       # torch.int64
 
 
 def _kv4_stream(stream):
@@ -315,20 +308,62 @@ def _kv4_stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _kv4_refuse(fn):
+    """The first call of a process looks at the slots' type before it is known: True to look again."""
+    global _i64
+    if _i64 is not None:
+        raise HsError(fn, HS_ERR_INVALID_ARG)
+    import torch
+    _i64 = torch.int64
+    return True
+
+
+def hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, table_width, ring, counters_in,
+                max_tokens, table_out, seq_len, q_start, slot, position, counters_out, short, stream=None):
+    """Tensors of the header's types and sizes, each contiguous; position may be None."""
+    if not (table_in.is_contiguous() and table_out.is_contiguous() and slot.dtype is _i64):
+        if _kv4_refuse("hs_kv4_plan"):
+            return hs_kv4_plan(cached_len, new_len, n_seqs, page_tokens, n_pages, table_in, table_width, ring, counters_in, max_tokens,
+                               table_out, seq_len, q_start, slot, position, counters_out, short, stream)
+    st = (_lib or lib()).hs_kv4_plan(
+        cached_len.data_ptr(), new_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width,
+        ring.data_ptr(), counters_in.data_ptr(), max_tokens, table_out.data_ptr(), seq_len.data_ptr(),
+        q_start.data_ptr(), slot.data_ptr(), None if position is None else position.data_ptr(), counters_out.data_ptr(),
+        short.data_ptr(), _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv4_plan", st)
+
+
 def hs_kv4_append(cache: hs_kv4_cache, k, v, slots, n_tokens, stream=None):
-    """k, v: bf16 [tokens][kv heads][head_dim], any token and head strides."""
-    (kt, kh, kc), (vt, vh, vc) = k.stride(), v.stride()
-    if kc != 1 or vc != 1:
-        raise HsError("hs_kv4_append", HS_ERR_INVALID_ARG)
-    st = lib().hs_kv4_append(cache.ref, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), n_tokens,
-                             _kv4_stream(stream))
+    """k, v: bf16 [tokens][kv heads][head_dim], any token and head strides;
+    slots: int64, contiguous; n_tokens of each at least."""
+    (kt, kh, kc), (vt, vh, vc), shape = k.stride(), v.stride(), k.shape
+    rows, heads, dim = shape
+    if (kc != 1 or vc != 1 or dim != cache.head_dim or heads != cache.n_kv_heads or rows < n_tokens or v.shape != shape
+            or slots.dtype is not _i64 or not slots.is_contiguous() or slots.numel() < n_tokens):
+        if _kv4_refuse("hs_kv4_append"):
+            return hs_kv4_append(cache, k, v, slots, n_tokens, stream)
+    st = (_lib or lib()).hs_kv4_append(cache, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), n_tokens,
+                                       _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv4_append", st)
 
 
 def hs_kv4_read(cache: hs_kv4_cache, slots, n_tokens, k_bf16=None, v_bf16=None, k_f32=None, v_f32=None, stream=None):
-    st = lib().hs_kv4_read(cache.ref, slots.data_ptr(), n_tokens, _p(k_bf16), _p(v_bf16), _p(k_f32), _p(v_f32),
-                           _kv4_stream(stream))
+    """slots: int64, contiguous; outputs contiguous, n_tokens rows of [kv heads][head_dim] at least."""
+    n = n_tokens * cache.n_kv_heads * cache.head_dim
+    if (slots.dtype is not _i64 or not slots.is_contiguous() or slots.numel() < n_tokens
+            or (k_bf16 is not None and (k_bf16.numel() < n or not k_bf16.is_contiguous()))
+            or (v_bf16 is not None and (v_bf16.numel() < n or not v_bf16.is_contiguous()))
+            or (k_f32 is not None and (k_f32.numel() < n or not k_f32.is_contiguous()))
+            or (v_f32 is not None and (v_f32.numel() < n or not v_f32.is_contiguous()))):
+        if _kv4_refuse("hs_kv4_read"):
+            return hs_kv4_read(cache, slots, n_tokens, k_bf16, v_bf16, k_f32, v_f32, stream)
+    st = (_lib or lib()).hs_kv4_read(
+        cache, slots.data_ptr(), n_tokens, k_bf16 if k_bf16 is None else k_bf16.data_ptr(),
+        v_bf16 if v_bf16 is None else v_bf16.data_ptr(), k_f32 if k_f32 is None else k_f32.data_ptr(),
+        v_f32 if v_f32 is None else v_f32.data_ptr(),
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv4_read", st)
 
@@ -340,17 +375,20 @@ def hs_kv4_attention_workspace_size(cache: hs_kv4_cache, n_seqs, n_q_heads) -> i
 def hs_kv4_attention(cache: hs_kv4_cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out,
                      workspace=None, workspace_bytes=None, stream=None):
     """q, out: bf16 [tokens][query heads][head_dim], any token and head
-    strides; table: int32 [n_seqs][table_width] contiguous."""
-    (qt, qh, qc), (ot, oh, oc) = q.stride(), out.stride()
-    if qc != 1 or oc != 1:
+    strides; table: int32 [n_seqs][table_width] contiguous; q_start and seq_len:
+    int32, contiguous, n_seqs + 1 and n_seqs at least."""
+    (qt, qh, qc), (ot, oh, oc), shape, (rows, width) = q.stride(), out.stride(), q.shape, table.shape
+    tokens, heads, dim = shape
+    if (qc != 1 or oc != 1 or dim != cache.head_dim or out.shape != shape or rows < n_seqs or not table.is_contiguous()
+            or q_start.numel() <= n_seqs or seq_len.numel() < n_seqs):
         raise HsError("hs_kv4_attention", HS_ERR_INVALID_ARG)
     if workspace is None:
         ws, nb = None, 0
     else:
         ws, nb = workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes
-    tokens, heads, _ = q.shape
-    st = lib().hs_kv4_attention(
-        cache.ref, q.data_ptr(), qt, qh, q_start.data_ptr(), seq_len.data_ptr(), table.data_ptr(), table.shape[1],
-        n_seqs, tokens, heads, max_new, scale, window, out.data_ptr(), ot, oh, ws, nb, _kv4_stream(stream))
+    st = (_lib or lib()).hs_kv4_attention(
+        cache, q.data_ptr(), qt, qh, q_start.data_ptr(), seq_len.data_ptr(), table.data_ptr(), width,
+        n_seqs, tokens, heads, max_new, scale, window, out.data_ptr(), ot, oh, ws, nb,
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv4_attention", st)

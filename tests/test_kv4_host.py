@@ -179,6 +179,40 @@ def test_binding_wants_contiguous_channels(lib):
         hs.hs_kv4_append(_cache(), k, k, 0, 4)
 
 
+def test_binding_refuses_tensors_that_do_not_fit(lib):
+    """What the pointers do not tell the library: each of these was launched on
+    other data than the tensors hold.  (A call that the binding passes on ends on the CPU
+    in HS_ERR_CUDA at the launch; here none may get there.)"""
+    import torch
+    b16, i32, i64, f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+    c = _cache(pool=A, n_pages=8, page=64, heads=2, dim=128)
+    z = lambda *s, t=b16: torch.zeros(s, dtype=t)  # noqa: E731
+
+    def refused(f, base, bads):
+        for name, values in bads.items():
+            for bad in values:
+                with pytest.raises(hs.HsError) as e:
+                    f(**{**base, name: bad})
+                assert e.value.status == hs.HS_ERR_INVALID_ARG, (name, bad.shape if hasattr(bad, "shape") else bad)
+    slots = [z(4, t=i32), z(3, t=i64), z(8, t=i64)[::2]]
+    refused(hs.hs_kv4_append, dict(cache=c, k=z(4, 2, 128), v=z(4, 2, 128), slots=z(4, t=i64), n_tokens=4, stream=0),
+            dict(k=[z(4, 2, 64), z(4, 1, 128), z(3, 2, 128), z(4, 2, 256)[:, :, ::2]], v=[z(4, 2, 64), z(4, 1, 128), z(3, 2, 128)],
+                 slots=slots, n_tokens=[5]))
+    refused(hs.hs_kv4_read, dict(cache=c, slots=z(4, t=i64), n_tokens=4, k_bf16=z(4, 2, 128), v_bf16=z(4, 2, 128),
+                                 k_f32=z(4, 2, 128, t=f32), v_f32=z(4, 2, 128, t=f32), stream=0),
+            dict(slots=slots, k_bf16=[z(3, 2, 128)], v_bf16=[z(4, 2, 256)[:, :, :128]], k_f32=[z(4, 2, 64, t=f32)],
+                 v_f32=[z(8, 2, 128, t=f32)[::2]]))
+    refused(hs.hs_kv4_attention, dict(cache=c, q=z(4, 8, 128), q_start=z(4, t=i32), seq_len=z(3, t=i32), table=z(3, 16, t=i32), n_seqs=3,
+                                      max_new=2, scale=0.1, window=0, out=z(4, 8, 128), workspace=z(1, t=torch.uint8),
+                                      workspace_bytes=1 << 30, stream=0),
+            dict(q=[z(4, 8, 64), z(3, 8, 128), z(4, 4, 128), z(4, 8, 256)[:, :, ::2]], out=[z(4, 8, 64), z(3, 8, 128)],
+                 q_start=[z(3, t=i32)], seq_len=[z(2, t=i32)], table=[z(3, 32, t=i32)[:, :16], z(2, 16, t=i32), z(16, 3, t=i32).T]))
+    plan = dict(cached_len=z(4, t=i32), new_len=z(4, t=i32), n_seqs=4, page_tokens=64, n_pages=100, table_in=z(4, 8, t=i32),
+                table_width=8, ring=z(100, t=i32), counters_in=z(2, t=i64), max_tokens=64, table_out=z(4, 8, t=i32), seq_len=z(4, t=i32),
+                q_start=z(5, t=i32), slot=z(64, t=i64), position=z(64, t=i32), counters_out=z(2, t=i64), short=z(1, t=i32), stream=0)
+    refused(hs.hs_kv4_plan, plan, dict(table_in=[z(4, 16, t=i32)[:, :8]], table_out=[z(4, 16, t=i32)[:, :8]], slot=[z(64, t=i32)]))
+
+
 # ------------------------------------------------ pins of the restatement
 def test_quantiser_by_hand():
     x = np.zeros((1, 64), np.float32)
