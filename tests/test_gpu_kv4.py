@@ -148,6 +148,29 @@ def test_append_writes_the_definition_bit_for_bit_and_read_returns_it(t, hkv, di
         assert torch.equal(torch.isnan(b), torch.isnan(f))
 
 
+@pytest.mark.parametrize("t,hkv,dim,page", [(21, 33, 128, 16), (9, 65, 64, 32), (5, 256, 128, 16), (3, 129, 64, 16)])
+def test_append_and_read_of_many_heads(t, hkv, dim, page):
+    """More than 64 groups a row: several CTAs along it."""
+    rng = np.random.default_rng(hkv)
+    pool, c = _cache(4, page, hkv, dim)
+    k, v = _hard_rows(rng, t, hkv, dim), _hard_rows(rng, t, hkv, dim)
+    slots = rng.permutation(4 * page)[:t]
+    sl = torch.from_numpy(slots).cuda()
+    hs.hs_kv4_append(c, k.cuda(), v.cuda(), sl, t)
+    want = np.full(pool.shape, 0xFF, np.uint8)
+    _kv4.fill_pool(want, page, dim, slots, k.float().numpy(), v.float().numpy())
+    half, got = page * dim // 2, pool.cpu().numpy()
+    assert np.array_equal(got[..., :2 * half], want[..., :2 * half])
+    gp, wp = (np.ascontiguousarray(a[..., 2 * half:]).view(np.float16) for a in (got, want))
+    assert np.array_equal(gp, wp, equal_nan=True)
+    kf, vf = (torch.empty((t, hkv, dim), dtype=torch.float32, device="cuda") for _ in range(2))
+    vb = torch.empty((t, hkv, dim), dtype=torch.bfloat16, device="cuda")
+    hs.hs_kv4_read(c, sl, t, k_f32=kf, v_f32=vf, v_bf16=vb)
+    for x, f in ((k, kf), (v, vf)):
+        assert np.array_equal(f.cpu().numpy(), _kv4.values(x.float().numpy()).astype(np.float32), equal_nan=True)
+    assert torch.equal(vb.isnan(), vf.isnan()) and torch.equal(vb[~vb.isnan()], vf.bfloat16()[~vb.isnan()])
+
+
 def test_append_of_a_slot_given_twice_touches_no_other():
     """What such a slot holds is undefined where its tokens differ; where they are
     equal it holds them, and every other slot holds its own token bit for bit."""
@@ -256,6 +279,35 @@ def test_attention(case, window):
     scale = dim ** -0.5
     out = r.run(hs, scale, window)
     _close(out, r.expected(scale, window), scale)
+
+
+ROW_SHAPES = [  # new, hq, hkv: rows of a kv head at the ends of each row tile of the few-row kernel
+    (9, 2, 2), (2, 9, 1), (3, 16, 4), (4, 8, 2), (2, 16, 2),          # 9, 18, 12, 16, 16
+    (1, 17, 1), (17, 1, 1), (4, 8, 1), (8, 16, 4), (5, 24, 4), (3, 20, 2),  # 17, 17, 32, 32, 30, 30
+    (3, 11, 1), (12, 8, 2), (1, 64, 1), (64, 2, 2),                   # 33, 48, 64, 64: four row warps in calls this small
+]
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 64), (128, 16), (128, 32), (128, 64)])
+@pytest.mark.parametrize("case", range(len(ROW_SHAPES)))
+@pytest.mark.parametrize("window", [0, 1, 50, 333])
+def test_attention_of_each_row_tile(case, dim, page, window):
+    new, hq, hkv = ROW_SHAPES[case]
+    r = _kv4.Requests(case + dim + page, [400, 0, 65], [new, new, min(new, 2)], hq, hkv, dim, page)
+    scale = dim ** -0.5
+    _close(r.run(hs, scale, window), r.expected(scale, window), scale)
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (24, 24, 64), (16, 2, 64)])
+@pytest.mark.parametrize("bound", [None, 600])
+def test_prompts_and_single_tokens_in_one_call(hq, hkv, dim, bound):
+    """A step as the plan makes it: decoding requests, prompts, a request that waits; max_new
+    is the step's own or a bound."""
+    cached = [200, 0, 77, 1000, 0, 31, 64, 5, 0, 512]
+    new = [1, 300, 1, 1, 7, 0, 1, 130, 1, 1]
+    r = _kv4.Requests(hq, cached, new, hq, hkv, dim, 32)
+    scale = dim ** -0.5
+    _close(r.run(hs, scale, max_new=bound), r.expected(scale), scale)
 
 
 @pytest.mark.parametrize("n", [32, 33, 64, 100, 127, 128, 129, 300])
