@@ -479,8 +479,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             const uint32_t none = (gone >> (2 * slot)) & 3u;
             // A wait that gives up (the error word is set) ends this warp's loads and
             // sums; it still meets the others where they wait for it.
-            if (phase < 2 && !warp_wait(full + slot, phase)) phase |= 2;
-            if (phase >= 2) continue;
+            if (phase >= 2) break;
+            if (!warp_wait(full + slot, phase)) {
+                phase |= 2;
+                break;
+            }
             if (none != 3u && key0 <= max_lim && key0 + kKvStep > back_min) {
                 const uint8_t* rec = ring + slot * C::kSlotBytes;
                 if (none || key0 + kKvStep - 1 > min_lim || key0 < back_max)
