@@ -551,6 +551,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             if (x * 128 < nrows) {
                 const bool valid = r < nrows;
                 const int lim = ctx + w.r * a.tq + kv_row_token(a, r);
+                const int low = max(lim, 0) - back_keys;  // the row's first key
                 const int min_lim = -warp_max_s32(valid ? -lim : -0x7fffffff), max_lim = warp_max_s32(valid ? lim : -1);
 
                 float m = kNoMax, l = 0.f;
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
 #pragma unroll
                         for (int i = 0; i < kPfKeys; ++i) {
                             const int key = key0 + i;
-                            if (key > lim || key < max(lim, 0) - back_keys || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
+                            if (key > lim || key < low || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
                         }
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
