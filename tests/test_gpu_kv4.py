@@ -298,6 +298,18 @@ def test_attention_of_each_row_tile(case, dim, page, window):
     _close(r.run(hs, scale, window), r.expected(scale, window), scale)
 
 
+@pytest.mark.parametrize("hq,long", [(2, 1), (40, 1), (2, 70)])
+def test_attention_of_4096_requests(hq, long):
+    """The most requests there may be, in the few-row kernel and in the chunk kernel (40 query
+    heads of one kv head; 70 tokens); a third of them has no new token."""
+    rng = np.random.default_rng(hq + long)
+    cached = [int(x) for x in rng.integers(0, 20, 4096)]
+    new = [int(x) for x in rng.integers(0, 3, 4096).clip(0, 1)]
+    new[0], new[4095], new[2000] = 1, 1, long
+    r = _kv4.Requests(hq, cached, new, hq, 1, 64, 16)
+    _close(r.run(hs, 0.2), r.expected(0.2), 0.2)
+
+
 @pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (24, 24, 64), (16, 2, 64)])
 @pytest.mark.parametrize("bound", [None, 600])
 def test_prompts_and_single_tokens_in_one_call(hq, hkv, dim, bound):
