@@ -18,8 +18,8 @@
 // Bounds.  Instructions of the steps: taking 32 keys' codes apart, the products'
 // issue and the exponentials, about half the issue slots; the integer pipe is
 // the busiest.  64 decode requests of up to 8192 tokens (32 / 8 heads of 128
-// channels, 316 MB of rows): 67 us, 4.7 TB/s, 70% of the copy bandwidth.  One of
-// 131,071 tokens (32 / 2 heads): 24.6 us, of which the steps take 9.5 and the
+// channels, 316 MB of rows): 68 us, 4.7 TB/s, 69% of the copy bandwidth.  One of
+// 131,071 tokens (32 / 2 heads): 24.8 us, of which the steps take 9.5 and the
 // joins of 152 pieces a head about 8.
 #include <type_traits>
 
@@ -657,7 +657,8 @@ using namespace hs_host;
 // tokens 60 and 51) and does not where the start and the joins bound the call: one request of
 // 4096 tokens (32 / 2 heads) 22.8 and 29.1, four 25.0 and 29.2, eight of 1000 tokens 17.1 and
 // 19.2.  So up to 64 rows stay here if requests x kv heads are at most 16 and the
-// tables hold no more than 2^17 keys of them.
+// tables hold no more than 2^17 keys of them.  The host knows the tables' width only, not
+// the lengths: short requests in tables made for long contexts go to the chunk kernel.
 constexpr int kPrefillRows = 33;
 
 // Counters of arrived pieces, (maximum, sum) pairs and partial sums of the widest launch.

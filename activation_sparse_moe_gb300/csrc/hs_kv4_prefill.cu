@@ -23,7 +23,7 @@
 // no second set of scores beside 2 x 128 columns of scores and outputs at head_dim 128), so
 // that a tile takes 3500 cycles for both; an item costs some 12,000 more: filling,
 // draining, writing.  A prompt of 4096 tokens (32 / 8 heads of 128 channels):
-// 147 us, 935 TFLOP/s, 49% of the measured bf16 peak; within long items 1340 TFLOP/s.
+// 148 us, 926 TFLOP/s, 48% of the measured bf16 peak; within long items 1340 TFLOP/s.
 #include "hs_kv4_join.cuh"
 #include "hs_tc.cuh"
 
@@ -118,7 +118,8 @@ __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk&
 // shared memory is free, and the pieces (at most kJoin of them) come in whole by
 // bulk copies.  A few loops of little code: that of add_pieces runs once a call, and
 // costs fetching it besides the rounds of loads (48 rows of five pieces: 9,400
-// cycles, here 5,800; 16 requests of three drafts 25.2 us, here 23.6).  The operations and their order are those of add_pieces.
+// cycles, here 5,800; 16 requests of three drafts gained 1.6 of 25.2 us).  The
+// operations and their order are those of add_pieces.
 template <int D>
 __device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk& w, int c, int count, int rows) {
     constexpr int kL = D / 8, kR = 32 / kL, kP = kJoin / kL, kAtOnce = 4;

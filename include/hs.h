@@ -445,17 +445,22 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  *   q_start_dev [n_seqs + 1] ascending, seq_len_dev [n_seqs]
  *   table_dev   [n_seqs][table_width]; a length past table_width pages is cut
  *   max_new     the largest number of new tokens of a request, or more: it
- *               chooses the kernel, not the result
+ *               chooses the kernel, and with it the roundings, not the result
  *   scale       > 0, at most 10^30 (scores past the fp32 range say nothing);
  *   window      >= 0 (0: none)
  * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it;
- * table_width * page_tokens at most 2^31 - 2^13.
+ * table_width * page_tokens at most 2^31 - 2^13; the work (kv heads x row tiles x
+ * key tiles, by n_tokens, max_new and table_width) below 2^32 tiles.
  * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and
  * values (chunks) with fp16 queries, each row scaled by a power of two of its
  * own, fp32 sums, probabilities rounded to fp16 for the second product.  A
  * query row that holds a NaN, an infinity or a value of 2^112 or more gives NaN
  * where it sees a key, and no other row.
+ * Scores are held to fp32 at any size; past 2^21 (of their base-2 logarithms) a
+ * row's are levelled to 2^-20 of the largest.
  * Deterministic.  Calls sharing one workspace must not overlap on the GPU.
+ * Its size (40.5 MB at 128 channels, 21 MB at 64) is that of the widest launch,
+ * whatever n_seqs and n_q_heads: one workspace serves every call of a cache.
  * The workspace must be ZERO-FILLED before its first use; each call leaves the
  * counters at its start at zero, so consecutive calls of any shapes and CUDA
  * graph replays need no clearing in between.  A workspace that another entry
