@@ -17,7 +17,7 @@ namespace hs {
 constexpr float kLazy = 8.f;     // a row's maximum may lag by a factor 2^8 before the sums are rescaled
 constexpr float kNoMax = -3e38f; // the maximum of a row that has seen no key
 constexpr float kFarScore = 2097152.f;  // 2^21, see kv_score_factor
-constexpr int kNoQuery = 127 + 112;  // exponent field of 2^112: a query row that reaches it, or holds no number, gives NaN
+constexpr int kNoQuery = 255;    // exponent field of infinities and NaN: a query row that holds one gives NaN
 constexpr int kKvMaxCtas = 456;  // three on each of 152 SMs
 constexpr int kKvWsRows = 2 * 152 * 256;  // rows of partial sums of the widest launch
 

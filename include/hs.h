@@ -454,8 +454,8 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  * Arithmetic: products of exact codes (single tokens) or fp16-rounded keys and
  * values (chunks) with fp16 queries, each row scaled by a power of two of its
  * own, fp32 sums, probabilities rounded to fp16 for the second product.  A
- * query row that holds a NaN, an infinity or a value of 2^112 or more gives NaN
- * where it sees a key, and no other row.
+ * query row that holds a NaN or an infinity gives NaN where it sees a key, and
+ * no other row.
  * Scores are held to fp32 at any size; past 2^21 (of their base-2 logarithms) a
  * row's are levelled to 2^-20 of the largest.
  * Deterministic.  Calls sharing one workspace must not overlap on the GPU.

@@ -480,8 +480,8 @@ def test_attention_query_with_one_large_channel(new, spike):
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("new", [1, 3, 7, 12, 40])
 def test_a_query_row_that_is_no_number_leaves_its_neighbours_alone(new, dim):
-    """Of each kv head's four query heads one holds a NaN, one an infinity or 2^112,
-    the others values of about 20 and 300 (past 2^16 under a common scale of 1):
+    """Of each kv head's four query heads one holds a NaN, one an infinity, the
+    others values of about 20 and 300 (past 2^16 under a common scale of 1):
     the first two give NaN, the others what they give alone."""
     r = _kv4.Requests(8, [200], [new], 8, 2, dim, 32)
     kind = np.arange(8) % 4
@@ -491,7 +491,7 @@ def test_a_query_row_that_is_no_number_leaves_its_neighbours_alone(new, dim):
     ref = r.expected(scale)
     q[:, kind == 0, 5] = float("nan")
     q[:, kind == 1, 6] = float("inf")
-    q[::2, kind == 1, 6] = -2.0 ** 112
+    q[::2, kind == 1, 6] = -float("inf")
     r.q = q.bfloat16()
     got = r.run(hs, scale).float().cpu().double().numpy()
     assert np.isnan(got[:, kind < 2]).all()
@@ -565,6 +565,16 @@ def test_scales_at_the_ends_of_their_range(scale, q_size, new):
     got = r.run(hs, scale).float().cpu().double().numpy()
     # probabilities rounded to fp16 (2^-11) before their product with codes of values up to 6 wide, values too in chunks
     assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + 6 * 2 * 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("exponent", [-95, 105, 113, 120])
+@pytest.mark.parametrize("new,dim", [(1, 128), (3, 64), (12, 128), (40, 128), (40, 64)])
+def test_queries_of_any_exponent(exponent, new, dim):
+    """Queries of 2^exponent with a scale that makes their scores the usual ones."""
+    r = _kv4.Requests(15, [300, 20], [new, 1], 8, 2, dim, 64)
+    r.q = (r.q.float() * 2.0 ** exponent).bfloat16()
+    scale = dim ** -0.5 * 2.0 ** -exponent
+    _close(r.run(hs, scale), r.expected(scale), scale)
 
 
 def test_attention_strides_streams_and_reuse_of_the_workspace():
