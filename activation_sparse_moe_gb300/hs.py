@@ -105,6 +105,16 @@ _SIGS = {
     "hs_kv4_attention": (C.c_int, [C.POINTER(hs_kv4_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float,
                                    C.c_int, C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hs_kv_pages_workspace_size": (C.c_size_t, [C.c_int]),
+    "hs_kv_fork": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p,
+                             C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                             C.c_void_p, C.c_void_p, C.c_void_p]),
+    "hs_kv_copy_pages": (C.c_int, [C.c_void_p, C.c_int, C.c_longlong, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p]),
+    "hs_kv_release": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
+                                C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hs_kv_compact": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                                C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                C.c_size_t, C.c_void_p]),
 }
 
 
@@ -392,3 +402,97 @@ def hs_kv4_attention(cache: hs_kv4_cache, q, q_start, seq_len, table, n_seqs, ma
         _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv4_attention", st)
+
+
+# Pages shared, copied, given back and moved.  The pointers do not tell the
+# library how long the tensors behind them are, so each is looked at here.
+def _kv_fits(fn, t32, t64, sizes):
+    """t32: int32 tensors, t64: int64 ones, contiguous, of at least the sizes beside them."""
+    import torch
+    for tensors, dtype in ((t32, torch.int32), (t64, torch.int64)):
+        for t, n in tensors:
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
+                raise HsError(fn, HS_ERR_INVALID_ARG)
+    if min(sizes) < 0:
+        raise HsError(fn, HS_ERR_INVALID_ARG)
+
+
+class make_kv_pools:
+    """The pools of a model's layers for hs_kv_copy_pages: device tensors, which
+    are kept, all of one size."""
+
+    def __init__(self, pools):
+        pools = list(pools)
+        if not pools or any(not p.is_contiguous() or p.nbytes != pools[0].nbytes for p in pools):
+            raise HsError("make_kv_pools", HS_ERR_INVALID_ARG)
+        self.tensors, self.nbytes = pools, pools[0].nbytes
+        self.c = (C.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
+
+
+def hs_kv_pages_workspace_size(n_pages) -> int:
+    return lib().hs_kv_pages_workspace_size(n_pages)
+
+
+def hs_kv_fork(parent, child, length, n_forks, cached_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared, ring,
+               counters_in, table_out, len_out, copy_src, copy_dst, counters_out, short, stream=None):
+    """Tensors of the header's types and sizes, each contiguous."""
+    cells = n_seqs * table_width
+    _kv_fits("hs_kv_fork", ((parent, n_forks), (child, n_forks), (length, n_forks), (cached_len, n_seqs), (table_in, cells),
+                            (shared, n_pages), (ring, n_pages), (table_out, cells), (len_out, n_seqs), (copy_src, n_forks),
+                            (copy_dst, n_forks), (short, 1)), ((counters_in, 2), (counters_out, 2)), (n_forks, n_seqs, n_pages, table_width))
+    st = lib().hs_kv_fork(parent.data_ptr(), child.data_ptr(), length.data_ptr(), n_forks, cached_len.data_ptr(), n_seqs, page_tokens,
+                          n_pages, table_in.data_ptr(), table_width, shared.data_ptr(), ring.data_ptr(), counters_in.data_ptr(),
+                          table_out.data_ptr(), len_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), counters_out.data_ptr(),
+                          short.data_ptr(), _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv_fork", st)
+
+
+def hs_kv_copy_pages(pools, page_bytes, n_pages, src, dst, n_copies, stream=None):
+    """pools: make_kv_pools of the layers' pools, or the tensors themselves."""
+    if not isinstance(pools, make_kv_pools):
+        pools = make_kv_pools(pools)
+    if pools.nbytes < n_pages * page_bytes:
+        raise HsError("hs_kv_copy_pages", HS_ERR_INVALID_ARG)
+    _kv_fits("hs_kv_copy_pages", ((src, n_copies), (dst, n_copies)), (), (0,))
+    st = lib().hs_kv_copy_pages(pools.c, len(pools.tensors), page_bytes, n_pages, src.data_ptr(), dst.data_ptr(), n_copies,
+                                _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv_copy_pages", st)
+
+
+def hs_kv_release(cached_len, keep_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared, ring, counters_in, table_out,
+                  len_out, counters_out, workspace=None, workspace_bytes=None, stream=None):
+    """Tensors of the header's types and sizes, each contiguous; table_out may be table_in."""
+    cells = n_seqs * table_width
+    _kv_fits("hs_kv_release", ((cached_len, n_seqs), (keep_len, n_seqs), (table_in, cells), (shared, n_pages), (ring, n_pages),
+                               (table_out, cells), (len_out, n_seqs)), ((counters_in, 2), (counters_out, 2)),
+             (n_seqs, n_pages, table_width))
+    ws, nb = _kv_workspace(workspace, workspace_bytes)
+    st = lib().hs_kv_release(cached_len.data_ptr(), keep_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width,
+                             shared.data_ptr(), ring.data_ptr(), counters_in.data_ptr(), table_out.data_ptr(), len_out.data_ptr(),
+                             counters_out.data_ptr(), ws, nb, _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv_release", st)
+
+
+def hs_kv_compact(cached_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared_in, ring, counters_in, max_copies, table_out,
+                  shared_out, copy_src, copy_dst, counters_out, short, workspace=None, workspace_bytes=None, stream=None):
+    """Tensors of the header's types and sizes, each contiguous; table_out and shared_out may be the inputs."""
+    cells = n_seqs * table_width
+    _kv_fits("hs_kv_compact", ((cached_len, n_seqs), (table_in, cells), (shared_in, n_pages), (ring, n_pages), (table_out, cells),
+                               (shared_out, n_pages), (copy_src, max_copies), (copy_dst, max_copies), (short, 1)),
+             ((counters_in, 2), (counters_out, 2)), (n_seqs, n_pages, table_width, max_copies))
+    ws, nb = _kv_workspace(workspace, workspace_bytes)
+    st = lib().hs_kv_compact(cached_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width, shared_in.data_ptr(),
+                             ring.data_ptr(), counters_in.data_ptr(), max_copies, table_out.data_ptr(), shared_out.data_ptr(),
+                             copy_src.data_ptr(), copy_dst.data_ptr(), counters_out.data_ptr(), short.data_ptr(), ws, nb,
+                             _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv_compact", st)
+
+
+def _kv_workspace(workspace, workspace_bytes):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes

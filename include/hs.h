@@ -472,6 +472,109 @@ int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q_bf16_dev, long
                      int window, uint16_t* out_bf16_dev, long long out_stride_token, long long out_stride_head,
                      void* workspace_dev, size_t workspace_bytes, hs_stream_t stream);
 
+/* ------------------------------------------------------ pages of a cache
+ * What happens to a cache's pages besides hs_kv4_plan: requests that begin with
+ * the same tokens (several samples of a prompt, a prompt kept for the next
+ * request), requests that are cut back or end, and a pool whose pages in use lie
+ * scattered.  The calls work on block tables, the ring of free pages and the
+ * counters of hs_kv4_plan, and are good for a cache of any format: a page is a
+ * number, and for hs_kv_copy_pages page_bytes bytes at page * page_bytes of a pool.
+ *
+ * shared_dev [n_pages] counts a page's owners beyond the first.  It starts as
+ * zeros; a page in the ring has the count 0, and hs_kv4_plan, which takes pages
+ * from the ring, needs no counts.  But it gives an ended request's pages to the
+ * ring whatever their count is: where requests share pages, those that end or are
+ * cut back go through hs_kv_release.  A page that is shared is not to be written:
+ * hs_kv_fork gives a child its own copy of a page that it shares in part, and a
+ * request that is to go on from an earlier token of a shared page is forked at
+ * that token into an empty row.
+ *
+ * Lengths are tokens, negative ones count as 0.  Of what a call writes, nothing
+ * may overlap anything else (HS_ERR_INVALID_ARG) but an output that its
+ * description lets be an input.  n_seqs 1..4096; page_tokens 16, 32 or 64;
+ * n_seqs * table_width and n_pages below 2^30, table_width * page_tokens below
+ * 2^31.  Deterministic. */
+
+/* Bytes of the workspace of hs_kv_release and hs_kv_compact; 0 for n_pages out of
+ * range.  The workspace must be ZERO-FILLED before its first use by either; each
+ * call leaves it so that the next one of the same n_pages, of either kind, and CUDA
+ * graph replays need no clearing.  Calls sharing one must not overlap on the GPU. */
+size_t hs_kv_pages_workspace_size(int n_pages);
+
+/* Rows of child_dev begin with the first length_dev tokens of the rows of
+ * parent_dev: the child's table lists the parent's pages that these tokens fill
+ * (each gets one owner more) and, if a part of a page is left, a page from the
+ * front of the ring, in the order of the forks, into which that page is to be
+ * copied (hs_kv_copy_pages with the pairs of this call, once in every pool).
+ *   parent_dev, child_dev, length_dev [n_forks]
+ *   cached_len_dev [n_seqs];  table_in_dev [n_seqs][table_width];  ring_dev [n_pages]
+ *   table_out_dev  all rows, -1 past a child's pages; it may be table_in_dev
+ *   shared_dev     [n_pages], in and out
+ *   len_out_dev    [n_seqs] the rows' lengths afterwards
+ *   copy_src_dev, copy_dst_dev [n_forks]; -1 where a child ends with a full page
+ *   counters_out_dev [2]
+ *   short_dev      [1]: 0, or the number of pages that the ring lacks for all forks
+ *                  plus that of the forks that cannot be: a row outside the table,
+ *                  a parent that is its own child, a length that is negative, or more
+ *                  than the parent holds or a row takes, a child that holds tokens
+ *                  or that another fork names too.  Then no fork is done (tables,
+ *                  lengths, counts and counters as before, pairs -1).
+ * A page of the parent outside the pool is listed as it is and has no count.
+ * n_forks 1..4096. */
+int hs_kv_fork(const int* parent_dev, const int* child_dev, const int* length_dev, int n_forks, const int* cached_len_dev, int n_seqs,
+               int page_tokens, int n_pages, const int* table_in_dev, int table_width, int* shared_dev, const int* ring_dev,
+               const long long* counters_in_dev, int* table_out_dev, int* len_out_dev, int* copy_src_dev, int* copy_dst_dev,
+               long long* counters_out_dev, int* short_dev, hs_stream_t stream);
+
+/* Copies page src_dev[i] to page dst_dev[i], i < n_copies, in each of n_pools pools
+ * (those of a model's layers; pools is a host array of device pointers, read during
+ * the call).  A pair that names a page outside the pool (such as -1) is skipped.
+ * Pairs are copied at the same time: a page that is the target of one pair and in
+ * another one too holds undefined bytes afterwards (the pairs of hs_kv_fork and
+ * hs_kv_compact have none).
+ *   pools 16-byte aligned, each n_pages * page_bytes bytes, at most 64 of them
+ *   page_bytes a multiple of 16, at most 2^30: bytes of a page over all kv heads,
+ *              the pool's bytes / n_pages
+ * n_copies 0..2^30 - 1. */
+int hs_kv_copy_pages(void* const* pools, int n_pools, long long page_bytes, int n_pages, const int* src_dev, const int* dst_dev,
+                     int n_copies, hs_stream_t stream);
+
+/* Cuts each row back to its first keep_len tokens (0: the request ends; as many as
+ * it holds or more: nothing happens).  A page that a row gives up loses an owner; one
+ * that had none beyond the row goes to the end of the ring.  The pages of one call
+ * go there in ascending order.
+ *   cached_len_dev, keep_len_dev [n_seqs];  table_in_dev [n_seqs][table_width]
+ *   shared_dev, ring_dev [n_pages], in and out
+ *   table_out_dev  -1 past a row's pages; it may be table_in_dev, whose entries past
+ *                  the pages that a row keeps are then all set to -1
+ *   len_out_dev    [n_seqs] min(cached, keep)
+ *   counters_out_dev [2] */
+int hs_kv_release(const int* cached_len_dev, const int* keep_len_dev, int n_seqs, int page_tokens, int n_pages,
+                  const int* table_in_dev, int table_width, int* shared_dev, int* ring_dev, const long long* counters_in_dev,
+                  int* table_out_dev, int* len_out_dev, long long* counters_out_dev, void* workspace_dev, size_t workspace_bytes,
+                  hs_stream_t stream);
+
+/* Moves the pages in use to the front of the pool.  Of the n pages that the rows
+ * list for their tokens, those numbered n and more go, in ascending order, into the
+ * free pages below n, in ascending order (hs_kv_copy_pages with the pairs of this
+ * call, once in every pool); every page from n on is then free and stands in the
+ * ring, n first.  A page that no row lists becomes free, whatever its count was.
+ *   cached_len_dev [n_seqs];  table_in_dev [n_seqs][table_width];  shared_in_dev [n_pages]
+ *   ring_dev       [n_pages] in and out: entries 0 up to n_pages - n are written
+ *   table_out_dev  -1 past a row's pages; entries outside the pool as they are; it may
+ *                  be table_in_dev
+ *   shared_out_dev [n_pages] the counts of the pages as they are then numbered, 0 for
+ *                  free ones; it may be shared_in_dev
+ *   copy_src_dev, copy_dst_dev [max_copies]; -1 past the moves (n_pages / 2 always do)
+ *   counters_out_dev [2]: 0 and the number of free pages
+ *   short_dev      [1]: 0, or the number of moves over max_copies.  Then nothing is done
+ *                  (tables, counts, ring and counters as before, pairs -1).
+ * max_copies 1..2^30 - 1. */
+int hs_kv_compact(const int* cached_len_dev, int n_seqs, int page_tokens, int n_pages, const int* table_in_dev, int table_width,
+                  const int* shared_in_dev, int* ring_dev, const long long* counters_in_dev, int max_copies, int* table_out_dev,
+                  int* shared_out_dev, int* copy_src_dev, int* copy_dst_dev, long long* counters_out_dev, int* short_dev,
+                  void* workspace_dev, size_t workspace_bytes, hs_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
