@@ -523,6 +523,7 @@ extern "C" const char* hs_status_string(int status) {
 }
 
 unsigned hs_kv4_take_status();  // of the key/value cache attention (hs_kv4_attn.cu)
+unsigned hs_kv8_take_status();  // (hs_kv8_attn.cu)
 
 extern "C" int hs_device_status(int* status) {
     if (!status) return HS_ERR_INVALID_ARG;
@@ -533,6 +534,7 @@ extern "C" int hs_device_status(int* status) {
     v |= hs_batch_take_status();
     v |= hs_prefill_take_status();
     v |= hs_kv4_take_status();
+    v |= hs_kv8_take_status();
     *status = v ? HS_ERR_TIMEOUT : HS_OK;
     return HS_OK;
 }

@@ -69,6 +69,11 @@ class hs_kv4_cache(C.Structure):
         return r
 
 
+class hs_kv8_cache(C.Structure):
+    _fields_ = hs_kv4_cache._fields_
+    ref = hs_kv4_cache.ref
+
+
 _lib = None
 
 _SIGS = {
@@ -103,6 +108,15 @@ _SIGS = {
                               C.c_void_p, C.c_void_p]),
     "hs_kv4_attention_workspace_size": (C.c_size_t, [C.POINTER(hs_kv4_cache), C.c_int, C.c_int]),
     "hs_kv4_attention": (C.c_int, [C.POINTER(hs_kv4_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float,
+                                   C.c_int, C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "hs_kv8_pool_bytes": (C.c_size_t, [C.POINTER(hs_kv8_cache)]),
+    "hs_kv8_append": (C.c_int, [C.POINTER(hs_kv8_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
+                                C.c_longlong, C.c_longlong, C.c_void_p, C.c_int, C.c_void_p]),
+    "hs_kv8_read": (C.c_int, [C.POINTER(hs_kv8_cache), C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
+                              C.c_void_p, C.c_void_p]),
+    "hs_kv8_attention_workspace_size": (C.c_size_t, [C.POINTER(hs_kv8_cache), C.c_int, C.c_int]),
+    "hs_kv8_attention": (C.c_int, [C.POINTER(hs_kv8_cache), C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_float,
                                    C.c_int, C.c_void_p, C.c_longlong, C.c_longlong, C.c_void_p, C.c_size_t, C.c_void_p]),
     "hs_kv_pages_workspace_size": (C.c_size_t, [C.c_int]),
@@ -305,6 +319,7 @@ def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
 # sizes, the slots' type, rows that do not follow one another.
 _current = None   # torch's own lookups of the current device and its raw stream
 _i64 = None       # torch.int64
+_b16 = None       # torch.bfloat16
 
 
 def _kv4_stream(stream):
@@ -319,12 +334,12 @@ def _kv4_stream(stream):
 
 
 def _kv4_refuse(fn):
-    """The first call of a process looks at the slots' type before it is known: True to look again."""
-    global _i64
+    """The first call of a process looks at the tensors' types before they are known: True to look again."""
+    global _i64, _b16
     if _i64 is not None:
         raise HsError(fn, HS_ERR_INVALID_ARG)
     import torch
-    _i64 = torch.int64
+    _i64, _b16 = torch.int64, torch.bfloat16
     return True
 
 
@@ -402,6 +417,75 @@ def hs_kv4_attention(cache: hs_kv4_cache, q, q_start, seq_len, table, n_seqs, ma
         _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv4_attention", st)
+
+
+def make_kv8_cache(pool, n_pages, page_tokens, n_kv_heads, head_dim) -> hs_kv8_cache:
+    """Descriptor of an 8-bit key/value cache, as make_kv4_cache."""
+    return hs_kv8_cache(_p(pool), n_pages, page_tokens, n_kv_heads, head_dim)
+
+
+def hs_kv8_pool_bytes(cache: hs_kv8_cache) -> int:
+    return lib().hs_kv8_pool_bytes(cache.ref)
+
+
+def hs_kv8_append(cache: hs_kv8_cache, k, v, slots, n_tokens, stream=None):
+    """As hs_kv4_append; the tokens of a block of 16 next to one another."""
+    (kt, kh, kc), (vt, vh, vc), shape = k.stride(), v.stride(), k.shape
+    rows, heads, dim = shape
+    if (kc != 1 or vc != 1 or dim != cache.head_dim or heads != cache.n_kv_heads or rows < n_tokens or v.shape != shape
+            or slots.dtype is not _i64 or not slots.is_contiguous() or slots.numel() < n_tokens or k.dtype is not _b16
+            or v.dtype is not _b16):
+        if _kv4_refuse("hs_kv8_append"):
+            return hs_kv8_append(cache, k, v, slots, n_tokens, stream)
+    st = (_lib or lib()).hs_kv8_append(cache, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), n_tokens,
+                                       _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv8_append", st)
+
+
+def hs_kv8_read(cache: hs_kv8_cache, slots, n_tokens, k_bf16=None, v_bf16=None, k_f32=None, v_f32=None, stream=None):
+    """As hs_kv4_read."""
+    n = n_tokens * cache.n_kv_heads * cache.head_dim
+    if (slots.dtype is not _i64 or not slots.is_contiguous() or slots.numel() < n_tokens
+            or (k_bf16 is not None and (k_bf16.numel() < n or not k_bf16.is_contiguous()))
+            or (v_bf16 is not None and (v_bf16.numel() < n or not v_bf16.is_contiguous()))
+            or (k_f32 is not None and (k_f32.numel() < n or not k_f32.is_contiguous()))
+            or (v_f32 is not None and (v_f32.numel() < n or not v_f32.is_contiguous()))):
+        if _kv4_refuse("hs_kv8_read"):
+            return hs_kv8_read(cache, slots, n_tokens, k_bf16, v_bf16, k_f32, v_f32, stream)
+    st = (_lib or lib()).hs_kv8_read(
+        cache, slots.data_ptr(), n_tokens, k_bf16 if k_bf16 is None else k_bf16.data_ptr(),
+        v_bf16 if v_bf16 is None else v_bf16.data_ptr(), k_f32 if k_f32 is None else k_f32.data_ptr(),
+        v_f32 if v_f32 is None else v_f32.data_ptr(),
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv8_read", st)
+
+
+def hs_kv8_attention_workspace_size(cache: hs_kv8_cache, n_seqs, n_q_heads) -> int:
+    return lib().hs_kv8_attention_workspace_size(cache.ref, n_seqs, n_q_heads)
+
+
+def hs_kv8_attention(cache: hs_kv8_cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out,
+                     workspace=None, workspace_bytes=None, stream=None):
+    """As hs_kv4_attention."""
+    (qt, qh, qc), (ot, oh, oc), shape, (rows, width) = q.stride(), out.stride(), q.shape, table.shape
+    tokens, heads, dim = shape
+    if (qc != 1 or oc != 1 or dim != cache.head_dim or out.shape != shape or rows < n_seqs or not table.is_contiguous()
+            or q_start.numel() <= n_seqs or seq_len.numel() < n_seqs or q.dtype is not _b16 or out.dtype is not _b16):
+        if _kv4_refuse("hs_kv8_attention"):
+            return hs_kv8_attention(cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out, workspace, workspace_bytes,
+                                    stream)
+    if workspace is None:
+        ws, nb = None, 0
+    else:
+        ws, nb = workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes
+    st = (_lib or lib()).hs_kv8_attention(
+        cache, q.data_ptr(), qt, qh, q_start.data_ptr(), seq_len.data_ptr(), table.data_ptr(), width,
+        n_seqs, tokens, heads, max_new, scale, window, out.data_ptr(), ot, oh, ws, nb,
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
+    if st:
+        raise HsError("hs_kv8_attention", st)
 
 
 # Pages shared, copied, given back and moved.  The pointers do not tell the

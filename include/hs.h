@@ -472,6 +472,71 @@ int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q_bf16_dev, long
                      int window, uint16_t* out_bf16_dev, long long out_stride_token, long long out_stride_head,
                      void* workspace_dev, size_t workspace_bytes, hs_stream_t stream);
 
+/* ------------------------------------------------- 8-bit key/value cache
+ * The same cache in 8 bits, for layers that 4 bits serve too coarsely: e4m3 codes
+ * with one scale for 16 tokens of a kv head, K and V each their own.  It takes the
+ * block tables, slots and pages of hs_kv4_plan and the calls on pages below as the
+ * 4-bit cache does, whose conventions hold here where nothing else is said.
+ *
+ * Pool layout: [n_pages][n_kv_heads][record], one record a (page, kv head):
+ *   K codes [page_tokens][head_dim], V codes [page_tokens][head_dim],
+ *   scales [page_tokens/16][4] words: K scale, V scale (fp32), two words of 0
+ * A channel stands for scale * code, code one byte of e4m3 (NaN 0x7f), scale a power
+ * of two from 2^-15 to 2^7: every value held is exact in fp16 and in bf16.  Of the codes of
+ * a token at offset o of its page the 16 bytes of channels 16 c to 16 c + 15 stand at
+ * byte 16 (c ^ turn), turn = (2 (o & 3)) ^ (o & 4) for 128 channels and o & 2 for 64
+ * (the kernels then read keys and channels from shared memory without bank conflicts). */
+typedef struct {
+    void* pool;        /* device, 16-byte aligned, hs_kv8_pool_bytes bytes */
+    int   n_pages;     /* >= 1 */
+    int   page_tokens; /* 16, 32 or 64 */
+    int   n_kv_heads;  /* 1..256 */
+    int   head_dim;    /* 64 or 128 */
+} hs_kv8_cache;
+
+/* Bytes of the pool; 0 for sizes outside the ranges above.  (pool is not read.) */
+size_t hs_kv8_pool_bytes(const hs_kv8_cache* cache);
+
+/* Writes the keys and values of n_tokens tokens into their slots.  A block (16
+ * tokens of a page whose first offset is a multiple of 16) has one scale 2^e: the
+ * smallest, -15 <= e <= 7, at which the largest magnitude among its new tokens is at
+ * most 448 * 2^e, but never less than the one it has, if it holds older tokens.  Those
+ * are the ones in front of the first new one; where the scale grows, they are rounded
+ * again at the new one (their codes move towards zero by powers of two: what was not
+ * below 2^-6 of the new scale stays exact).  A block whose first token is new begins
+ * anew, whatever stood there.
+ *   code = e4m3(x / 2^e), round to nearest, ties to even
+ * A group of 64 channels of a token that holds a NaN or a magnitude past 57344
+ * (448 * 2^7) reads back as NaN and says nothing about the scale.  A slot outside the
+ * pool (such as -1) is skipped.
+ * The tokens of one block stand next to one another in slot_dev, in any order, each
+ * slot once (hs_kv4_plan gives them so): what a block then holds whose tokens stand
+ * apart, or a slot given twice, is undefined; other blocks are not touched by it.
+ * Arguments as hs_kv4_append. */
+int hs_kv8_append(const hs_kv8_cache* cache, const uint16_t* k_bf16_dev, long long k_stride_token, long long k_stride_head,
+                  const uint16_t* v_bf16_dev, long long v_stride_token, long long v_stride_head, const long long* slot_dev,
+                  int n_tokens, hs_stream_t stream);
+
+/* Reads n_tokens slots back, scale * code (exact in either type); otherwise as
+ * hs_kv4_read. */
+int hs_kv8_read(const hs_kv8_cache* cache, const long long* slot_dev, int n_tokens, uint16_t* k_bf16_dev, uint16_t* v_bf16_dev,
+                float* k_f32_dev, float* v_f32_dev, hs_stream_t stream);
+
+/* Causal attention of each request's new tokens over its cached ones: all of
+ * hs_kv4_attention's arguments, limits and rules, over the 8-bit cache.  A value that is
+ * NaN makes NaN only its channels of the rows that see it.
+ * Arithmetic: keys and values exact in fp16, with queries in fp16, each row scaled by a
+ * power of two of its own, fp32 sums, probabilities (times the value's scale, for
+ * single tokens) rounded to fp16 for the second product.
+ * The workspace is one of hs_kv4_attention's kind and may be shared with it, if
+ * it is large enough for both and the calls do not overlap. */
+size_t hs_kv8_attention_workspace_size(const hs_kv8_cache* cache, int n_seqs, int n_q_heads);
+int hs_kv8_attention(const hs_kv8_cache* cache, const uint16_t* q_bf16_dev, long long q_stride_token, long long q_stride_head,
+                     const int* q_start_dev, const int* seq_len_dev, const int* table_dev, int table_width, int n_seqs,
+                     int n_tokens, int n_q_heads, int max_new, float scale, int window, uint16_t* out_bf16_dev,
+                     long long out_stride_token, long long out_stride_head, void* workspace_dev, size_t workspace_bytes,
+                     hs_stream_t stream);
+
 /* ------------------------------------------------------ pages of a cache
  * What happens to a cache's pages besides hs_kv4_plan: requests that begin with
  * the same tokens (several samples of a prompt, a prompt kept for the next
