@@ -80,9 +80,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
     return r;
 }
-// Bit 7 of each byte that is a NaN code.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
 // A call of its own: its registers are not the softmax's.
 template <int D>
 __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk& w, int warp, int warps, int row0, int row1, int c, int first,
@@ -341,46 +338,41 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
         __syncwarp();
         mbar_wait(&sh.products_done, 0);
     } else {
-        // ---- codes converted into swizzled fp16 tiles
+        // ---- codes converted into swizzled fp16 tiles, 16 channels of a key at a time
+        // Eight lanes that work together take four chunks of two keys k and k ^ 3: their codes
+        // stand turned into different banks, and the chunks that they store in a line's
+        // even and odd places.  A thread's keys are a multiple of eight apart, so its places
+        // in the tiles are too.
         const int idx = (warp < 12 ? warp - 8 : warp - 10) * 32 + lane;  // of 192
+        constexpr int kItems = kPfHalf * D / 16, kMine = (kItems + 32 * kPfApart - 1) / (32 * kPfApart), kApart = 32 * kPfApart * 16 / D;
+        static_assert(kApart % 8 == 0, "keys of a thread");
+        const int rest = NG == 1 ? idx >> 3 : idx >> 4, c = NG == 1 ? idx & 3 : (idx & 3) | (idx >> 1 & 4);
+        const int first = (rest >> 1) << 2 | ((rest & 1) ^ (idx & 4 ? 3 : 0));  // its first key in a half
+        const uint8_t* read_at = packed_s + first * D + ((c ^ kv8_turn<D>(first)) << 4);
+        uint8_t* write_at = kv_s + (c >> 2) * (kPfKeys * 128) + first * 128 + ((((c & 3) * 2) ^ (first & 7)) << 4);
+        const int other = first & 1 ? -16 : 16;  // to the chunk's second half
         uint32_t f = 0, tiles = 0;
         bool dead = false;
         for (; w.left > 0 && !dead; next_piece()) {
-            const int cnt = kv_piece_tiles(w);
-            for (int k = 0; k < cnt && !dead; ++k, ++tiles) {
-                const int key0 = (w.lo + w.tile + k) * kPfKeys, info = tiles % kPfInfo;
+            const int cnt = kv_piece_tiles(w), len = w.len;
+            int key0 = (w.lo + w.tile) * kPfKeys;
+            for (int k = 0; k < cnt && !dead; ++k, ++tiles, key0 += kPfKeys) {
+                const int info = tiles % kPfInfo;
                 for (int part = 0; part < 4; ++part, ++f) {
                     const int st = f % kPfPacked, slot = (f >> 1) % kPfSlots, v = part >> 1, half = part & 1;
                     if (!warp_wait(sh.packed_full + st, (f / kPfPacked) & 1)) {
                         dead = true;
                         break;
                     }
-                    // 16 channels of a key at a time, into registers while the tile's place may
-                    // still be in use.  Eight lanes that work together take four chunks of two keys k
-                    // and k ^ 3: their codes stand turned into different banks, and the
-                    // chunks that they store in a line's even and odd places.
-                    constexpr int kItems = kPfHalf * D / 16, kMine = (kItems + 32 * kPfApart - 1) / (32 * kPfApart);
+                    // into registers while the tile's place may still be in use
                     const uint32_t gone = sh.gone[info];
-                    const uint8_t* from = packed_s + st * C::kPackedBytes;
-                    auto key_of = [](int id) {  // in the half
-                        const int r = NG == 1 ? id >> 3 : id >> 4;
-                        return (r >> 1) << 2 | ((r & 1) ^ (id & 4 ? 3 : 0));
-                    };
-                    auto chunk_of = [](int id) { return NG == 1 ? id & 3 : (id & 3) | (id >> 1 & 4); };
                     uint4 q[kMine];
                     float scale[kMine];
-                    uint32_t nan = 0;
 #pragma unroll
                     for (int i = 0; i < kMine; ++i) {
-                        const int id = idx + i * 32 * kPfApart;
-                        const int key = key_of(id), c = chunk_of(id), in_tile = half * kPfHalf + key;
-                        if (kItems % (32 * kPfApart) == 0 || id < kItems) {
-                            q[i] = *reinterpret_cast<const uint4*>(from + key * D + ((c ^ kv8_turn<D>(key)) << 4));
-                            scale[i] = reinterpret_cast<const float*>(from + kPfHalf * D + (key & ~15))[v];
-                            // what lies behind the last key, or in a page that is not there, may be anything
-                            if (key0 + in_tile >= w.len || (gone >> (in_tile >> 4)) & 1u) q[i] = make_uint4(0, 0, 0, 0), scale[i] = 1.f;
-                            if (v) nan |= nan_bytes(q[i].x) | nan_bytes(q[i].y) | nan_bytes(q[i].z) | nan_bytes(q[i].w);
-                        }
+                        if ((i + 1) * 32 * kPfApart > kItems && idx + i * 32 * kPfApart >= kItems) continue;
+                        q[i] = *reinterpret_cast<const uint4*>(read_at + st * C::kPackedBytes + i * kApart * D);
+                        scale[i] = reinterpret_cast<const float*>(packed_s + st * C::kPackedBytes + kPfHalf * D + ((first + i * kApart) & ~15))[v];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.packed_empty + st);
@@ -389,12 +381,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-                    if (nan) {  // a NaN value must not meet the zero probability of a row that does not see it
+                    if (gone || key0 + kPfKeys > len) {  // what lies behind the last key, or in a page that is not there, may be anything
 #pragma unroll
                         for (int i = 0; i < kMine; ++i) {
-                            const int id = idx + i * 32 * kPfApart;
-                            const int c = chunk_of(id), in_tile = half * kPfHalf + key_of(id);
-                            if (id < kItems && (nan_bytes(q[i].x) | nan_bytes(q[i].y) | nan_bytes(q[i].z) | nan_bytes(q[i].w))) {
+                            const int in_tile = half * kPfHalf + first + i * kApart;
+                            if (key0 + in_tile >= len || (gone >> (in_tile >> 4 & 7)) & 1u) q[i] = make_uint4(0, 0, 0, 0), scale[i] = 1.f;
+                        }
+                    }
+                    if (v) {  // a NaN value must not meet the zero probability of a row that does not see it
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) {
+                            if ((i + 1) * 32 * kPfApart > kItems && idx + i * 32 * kPfApart >= kItems) continue;
+                            if ((q[i].x & 0x7fu) == 0x7fu) [[unlikely]] {  // (it stands in all 64 codes of a group)
+                                const int in_tile = half * kPfHalf + first + i * kApart;
                                 atomicOr(&sh.nan_keys[info][c >> 2][in_tile >> 5], 1u << (in_tile & 31));
                                 sh.nan_any[info] = 1;
                                 q[i] = make_uint4(0, 0, 0, 0);
@@ -405,23 +404,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                         dead = true;
                         break;
                     }
-                    uint8_t* to = kv_s + slot * C::kTileBytes;
+                    uint8_t* to = write_at + slot * C::kTileBytes + half * (kPfHalf * 128);
 #pragma unroll
                     for (int i = 0; i < kMine; ++i) {
-                        const int id = idx + i * 32 * kPfApart;
-                        const int key = key_of(id), c = chunk_of(id);
-                        if (kItems % (32 * kPfApart) == 0 || id < kItems) {
-                            const __half2 sc = __float2half2_rn(scale[i]);
-                            uint8_t* line = to + (c >> 2) * (kPfKeys * 128) + (half * kPfHalf + key) * 128;
-                            const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                        if ((i + 1) * 32 * kPfApart > kItems && idx + i * 32 * kPfApart >= kItems) continue;
+                        const __half2 sc = __float2half2_rn(scale[i]);
+                        const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                uint32_t r[4];
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t r[4];
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    r[y] = as_u32(__hmul2(as_h2(e4m3x2_half2((uint16_t)(words[2 * x + (y >> 1)] >> (16 * (y & 1))))), sc));
-                                *reinterpret_cast<uint4*>(line + ((((c & 3) * 2 + x) ^ (key & 7)) << 4)) = make_uint4(r[0], r[1], r[2], r[3]);
-                            }
+                            for (int y = 0; y < 4; ++y)
+                                r[y] = as_u32(__hmul2(as_h2(e4m3x2_half2((uint16_t)(words[2 * x + (y >> 1)] >> (16 * (y & 1))))), sc));
+                            *reinterpret_cast<uint4*>(to + i * kApart * 128 + x * other) = make_uint4(r[0], r[1], r[2], r[3]);
                         }
                     }
                     if (half) {

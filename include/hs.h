@@ -481,8 +481,9 @@ int hs_kv4_attention(const hs_kv4_cache* cache, const uint16_t* q_bf16_dev, long
  * Pool layout: [n_pages][n_kv_heads][record], one record a (page, kv head):
  *   K codes [page_tokens][head_dim], V codes [page_tokens][head_dim],
  *   scales [page_tokens/16][4] words: K scale, V scale (fp32), two words of 0
- * A channel stands for scale * code, code one byte of e4m3 (NaN 0x7f), scale a power
- * of two from 2^-15 to 2^7: every value held is exact in fp16 and in bf16.  Of the codes of
+ * A channel stands for scale * code, code one byte of e4m3, scale a power of two from
+ * 2^-15 to 2^7: every value held is exact in fp16 and in bf16.  NaN (0x7f) stands in all
+ * codes of a group of 64 channels or in none.  Of the codes of
  * a token at offset o of its page the 16 bytes of channels 16 c to 16 c + 15 stand at
  * byte 16 (c ^ turn), turn = (2 (o & 3)) ^ (o & 4) for 128 channels and o & 2 for 64
  * (the kernels then read keys and channels from shared memory without bank conflicts). */
@@ -523,8 +524,7 @@ int hs_kv8_read(const hs_kv8_cache* cache, const long long* slot_dev, int n_toke
                 float* k_f32_dev, float* v_f32_dev, hs_stream_t stream);
 
 /* Causal attention of each request's new tokens over its cached ones: all of
- * hs_kv4_attention's arguments, limits and rules, over the 8-bit cache.  A value that is
- * NaN makes NaN only its channels of the rows that see it.
+ * hs_kv4_attention's arguments, limits and rules, over the 8-bit cache.
  * Arithmetic: keys and values exact in fp16, with queries in fp16, each row scaled by a
  * power of two of its own, fp32 sums, probabilities (times the value's scale, for
  * single tokens) rounded to fp16 for the second product.
