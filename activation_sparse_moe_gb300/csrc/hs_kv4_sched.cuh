@@ -31,6 +31,7 @@ struct KvAttnArgs {
     const int* seq_len;
     const int* table;
     int width, n_seqs, n_tokens, group, rows, tq, min_units, pad, tile_log2;
+    uint32_t short_line, short_ctas;  // a line of at most so many units goes to at most so many CTAs (0: no such line)
     int back;            // a row at position p >= 0 sees the keys from p - back on: window - 1, or all of int
     uint32_t group_inv;  // ceil(2^16 / group)
     float scale_log2;    // scale * log2(e)
@@ -168,6 +169,7 @@ struct KvCut {
 __device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, uint32_t total) {
     KvCut c;
     c.active = max(1u, min(gridDim.x, total / (uint32_t)a.min_units));
+    if (total <= a.short_line) c.active = min(c.active, a.short_ctas);
     c.q = total / c.active;
     c.more = total - c.q * c.active;
     return c;

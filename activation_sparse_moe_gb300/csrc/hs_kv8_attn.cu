@@ -12,8 +12,8 @@
 // score by less than 2^-33 of the largest channel's part.
 #include <type_traits>
 
-#include "hs_kv4_join.cuh"
 #include "hs_kv8.cuh"
+#include "hs_kv8_join.cuh"
 
 namespace hs {
 
@@ -47,7 +47,7 @@ __device__ __forceinline__ float bf16_f32(uint32_t w, int hi) { return __uint_as
 template <int D, int NQ, int RT, int KW>
 struct Decode8Cfg {
     static constexpr int kNg = D / 64;
-    static constexpr int kCtas = RT > 1 ? 1 : 2;      // resident on an SM
+    static constexpr int kCtas = RT * KW > 4 ? 1 : 2;  // resident on an SM
     static constexpr int kSlots = D == 128 ? 2 : 3;  // steps of a warp's ring
     static constexpr int kSlotBytes = kv8_record_bytes(kKvStep, D);
     static constexpr int kWarps = RT * KW;
@@ -87,12 +87,17 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
     // (every lane writes the same): looked at once an item, and registers are short.
     __shared__ KvWalk walks[C::kWarps], ahead[C::kWarps], comings[C::kWarps];
     __shared__ int join_last;
-    static_assert(C::kWarps * C::kSlots <= 32, "barriers");
+    static_assert(C::kWarps * C::kSlots < 32, "barriers");  // the last one is the joins'
+    uint32_t joins = 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rt = warp / KW, kw = warp % KW, g = lane >> 2, t = lane & 3;  // fragment row or column, and pair
 
     if (tid < C::kWarps * C::kSlots) {
         mbar_init(bars + tid, 1);
+        fence_mbar_init();
+    }
+    if (tid == 31) {
+        mbar_init(bars + 31, 1);
         fence_mbar_init();
     }
     pdl_wait();
@@ -565,8 +570,13 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         if (!whole) {
             const KvPieces of = kv_pieces(a, w, total);
-            auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory"); };
-            join_pieces(of, a.joined, tid == 0, &join_last, meet, [&](int first, int step, int count, bool final) {
+            auto meet = []() { asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory"); };
+            join_pieces_in_runs(of, a.joined, tid == 0, &join_last, meet, [&](int first, int step, int count, bool final) {
+                // (no copy is under way then, but where a wait gave up)
+                if (coming.left == 0 && join_bytes<D>(count, rows) <= C::kRingBytes + C::kMergeBytes) {
+                    add_pieces_at_end<D, 32 * C::kWarps>(a, w, smem, bars + 31, joins++ & 1, of.c, first, step, count, rows, final, meet);
+                    return;
+                }
                 add_pieces<D, C::kJoinSets, 8 / C::kJoinSets>(a, w, warp, C::kWarps, 0, rows, of.c, first, step, count, final);
             });
         }
@@ -595,8 +605,15 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tq = C::kRows / a.group;
     a.min_units = 2;
     a.tile_log2 = 6;
-    // An item's own time in tiles.
-    a.pad = RT == 1 ? 6 : 4;
+    a.pad = RT == 1 ? 6 : 8;
+    // Up to 16 pieces of an item are joined in one round, more in two, which costs as much as eight
+    // warps take for some ten tiles: few and short items are cut in 12 (one request of 4096 tokens with
+    // two kv heads 11.8 instead of 13.1 us, two of 8000 13.2 instead of 13.8).
+    if (KW == 8) {
+        const uint32_t items = (uint32_t)a.n_seqs * (uint32_t)a.g.heads;
+        a.short_line = items * (uint32_t)(a.pad + 128);
+        a.short_ctas = 12 * items;
+    }
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
@@ -605,10 +622,15 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
     return HS_OK;
 }
 
-// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.
+// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.  Sixteen rows
+// of few items are shared by eight warps along the keys, one CTA an SM in place of two: half
+// as many pieces to join, and room to join 16 of them in shared memory.  us, against four: one request of
+// 131,071 tokens (32 / 2 heads) 24.6 and 27.3, one of 4096 11.8 and 15.2, eight of 2000 11.0 and
+// 14.1; but 16 of 4000 17.8 and 16.1, and up to 128 keys, where nothing is cut, 6.3 and 6.0.
 template <int D>
 int launch_rows8(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
     if (rows <= 8) return launch_decode8<D, 1, 1, 4>(a, sms, s);
+    if (rows <= 16 && a.n_seqs * a.g.heads <= 16 && a.width << a.g.page_log2 > 128) return launch_decode8<D, 2, 1, 8>(a, sms, s);
     if (rows <= 16) return launch_decode8<D, 2, 1, 4>(a, sms, s);
     if (rows <= 32) return launch_decode8<D, 2, 2, 4>(a, sms, s);
     return launch_decode8<D, 2, 4, 2>(a, sms, s);

@@ -628,7 +628,10 @@ def test_attention_strides_streams_and_reuse_of_the_workspace():
                                                 ([3000] * 40, [1] * 40, 32, 8, 128), ([2000] * 9, [3] * 9, 32, 2, 128),
                                                 # one row tile: joins in shared memory (few pieces), from memory (many)
                                                 ([1500] * 14, [3] * 14, 32, 2, 128), ([3000] * 6, [40] * 6, 4, 4, 64),
-                                                ([700, 0, 65], [40, 128, 1], 8, 8, 128), ([20000], [9], 16, 4, 64)])
+                                                ([700, 0, 65], [40, 128, 1], 8, 8, 128), ([20000], [9], 16, 4, 64),
+                                                # sixteen rows on eight warps: two rounds, one round, items that a CTA begins and ends
+                                                ([40000], [1], 32, 2, 128), ([9000], [4], 8, 2, 64), ([5000, 30], [1, 1], 16, 1, 128),
+                                                ([15000, 200, 9000], [2, 1, 2], 16, 2, 128), ([3000] * 7, [1] * 7, 32, 2, 64)])
 def test_joined_pieces_do_not_depend_on_who_comes_last(ctx, new, hq, hkv, dim):
     """Work on another stream delays some CTAs, so that an item's pieces arrive in other orders."""
     r = _kv8.Requests(77, ctx, new, hq, hkv, dim, 64)
