@@ -17,6 +17,8 @@ struct Kv8AppendArgs {
 // has grown (rarely), and rounds the new rows, which it keeps in registers: they are read
 // once.  D / 8 lanes take a row, 16 bytes of it each.  What is past 57344 or NaN is found by
 // comparing bf16 bits.
+constexpr uint32_t kLargest = 0x4760u;  // 57344 in bf16
+
 template <int D>
 __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) {
     constexpr int kL = D / 8, kR = 32 / kL, kIts = kKv8Block / kR;  // lanes a row, rows at a time, turns for 16 rows
@@ -27,6 +29,13 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     pdl_trigger();
     const int t0 = seg * a.span;
     if (t0 >= a.n) return;
+    const uint16_t* x = (kv ? a.x[1] : a.x[0]) + (long long)head * (kv ? a.sh[1] : a.sh[0]);
+    const long long st = kv ? a.st[1] : a.st[0];
+    // The rows' addresses are known before the slots are: they come into L2 meanwhile.
+    if (D == 128 ? lane < 2 * a.span : lane < a.span) {
+        const int t = t0 + (D == 128 ? lane >> 1 : lane);
+        if (t < a.n) prefetch_l2(x + t * st + (D == 128 ? (lane & 1) * 64 : 0));
+    }
     auto block_at = [&](int t, long long& s) -> long long {
         s = t >= 0 && t < a.n ? a.slot[t] : -1;
         return s >= 0 && s < a.g.slots ? s >> 4 : -1;
@@ -36,8 +45,7 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
     long long before = __shfl_up_sync(~0u, mine, 1);
     if (lane == 0) before = block_at(t0 - 1, unused);
     unsigned runs = __ballot_sync(~0u, lane < a.span && mine >= 0 && mine != before);
-    const uint16_t* x = (kv ? a.x[1] : a.x[0]) + (long long)head * (kv ? a.sh[1] : a.sh[0]) + c8 * 8;
-    const long long st = kv ? a.st[1] : a.st[0];
+    x += c8 * 8;
     const int P = 1 << a.g.page_log2;
     for (; runs; runs &= runs - 1) {
         const int l = __ffs(runs) - 1;
@@ -45,9 +53,7 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
         const unsigned same = __ballot_sync(~0u, mine == block) >> l;
         const int count = min(~same ? __ffs(~same) - 1 : 32, kKv8Block);
         const int first = (int)warp_min_u32(lane >= l && lane < l + count ? (uint32_t)slot & 15u : 16u);
-        // the rows, and the largest magnitude of those groups of 64 that can be held
-        uint4 v[kIts];
-        uint32_t bad = 0, top = 0;
+        uint4 v[kIts];  // the rows (absent ones as zeros)
 #pragma unroll
         for (int i = 0; i < kIts; ++i) {
             const int j = i * kR + sub;
@@ -59,17 +65,25 @@ __global__ void __launch_bounds__(128) kv8_append_kernel(const Kv8AppendArgs a) 
         float* scale = reinterpret_cast<float*>(rec + 2 * P * D + base) + kv;
         int e_old = kKv8Low;
         if (first > 0) e_old = min(max((int)(__float_as_uint(*scale) >> 23) - 127, kKv8Low), kKv8High);
+        // the largest magnitude of all rows; only if that cannot be held, group by group of 64
+        uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < kIts; ++i) {
-            if (i * kR >= count) break;
-            uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+        for (int i = 0; i < kIts; ++i)
+            most = __vmaxu2(most, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        uint32_t top = warp_max_u32(max(most & 0xffffu, most >> 16)), bad = 0;
+        if (top > kLargest) {  // past 57344, or NaN
+            top = 0;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(~0u, m, o));
-            m = max(m & 0xffffu, m >> 16);
-            if (m > 0x4760u) bad |= 1u << i;  // past 57344, or NaN
-            else top = max(top, m);
+            for (int i = 0; i < kIts; ++i) {
+                uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(~0u, m, o));
+                m = max(m & 0xffffu, m >> 16);
+                if (m > kLargest) bad |= 1u << i;
+                else top = max(top, m);
+            }
+            top = warp_max_u32(top);
         }
-        top = warp_max_u32(top);
         // the smallest e with top <= 448 * 2^e = 1.75 * 2^(e + 8)
         int e = max((int)(top >> 7) - 127 - 8 + ((top & 127u) > 96u ? 1 : 0), kKv8Low);
         e = max(e, e_old);
@@ -125,61 +139,51 @@ struct Kv8ReadArgs {
     float* f32[2];
 };
 
-constexpr int kRead8Ahead = 2;
-
-// A thread takes eight channels of a key and those of its value, and as many of
-// another token's half a grid on, so that four loads are in flight.
+// A thread takes eight channels of a key and those of its value.  (Sixteen write
+// their 32 bytes in two halves, 16 bytes of every sector at a time.)
 template <int D>
 __global__ void __launch_bounds__(256) kv8_read_kernel(const Kv8ReadArgs a) {
     constexpr int kL = D / 8;
     pdl_wait();
     pdl_trigger();
     const int P = 1 << a.g.page_log2;
-    const long long all = (long long)a.n * a.per, step = (long long)gridDim.x * blockDim.x;
-    uint2 w[kRead8Ahead][2];
-    float2 s[kRead8Ahead];
-    long long at[kRead8Ahead];
-#pragma unroll
-    for (int i = 0; i < kRead8Ahead; ++i) {
-        at[i] = (long long)blockIdx.x * blockDim.x + threadIdx.x + i * step;
-        w[i][0] = w[i][1] = make_uint2(0, 0);
-        s[i] = make_float2(0.f, 0.f);
-        if (at[i] >= all) continue;
-        const uint32_t t = (uint32_t)(at[i] / (uint32_t)a.per), rest = (uint32_t)(at[i] - (long long)t * a.per), head = rest / kL, c8 = rest % kL;
-        const long long slot = a.slot[t];
-        if (slot < 0 || slot >= a.g.slots) continue;
+    const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (at >= (long long)a.n * a.per) return;
+    const uint32_t t = (uint32_t)at / (uint32_t)a.per, rest = (uint32_t)at - t * (uint32_t)a.per, head = rest / kL, c8 = rest % kL;  // (below 2^32)
+    uint2 w[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+    float2 s = make_float2(0.f, 0.f);
+    const long long slot = a.slot[t];
+    if (slot >= 0 && slot < a.g.slots) {
         const uint8_t* rec = kv_record(a.g, (int)(slot >> a.g.page_log2), (int)head);
         const int o = (int)slot & (P - 1);
         const uint8_t* code = rec + o * D + (((int)(c8 >> 1) ^ kv8_turn<D>(o)) << 4) + (c8 & 1) * 8;
-        w[i][0] = *reinterpret_cast<const uint2*>(code);
-        w[i][1] = *reinterpret_cast<const uint2*>(code + P * D);
-        s[i] = *reinterpret_cast<const float2*>(rec + 2 * P * D + (o & ~15));
+        w[0] = *reinterpret_cast<const uint2*>(code);
+        w[1] = *reinterpret_cast<const uint2*>(code + P * D);
+        s = *reinterpret_cast<const float2*>(rec + 2 * P * D + (o & ~15));
     }
 #pragma unroll
-    for (int i = 0; i < kRead8Ahead; ++i) {
-        if (at[i] >= all) continue;
+    for (int kv = 0; kv < 2; ++kv) {
+        const __half2 scale = __float2half2_rn(kv ? s.y : s.x);  // (exact, and so are the products)
+        float2 x[4];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            float x[8];
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t h = e4m3x2_half2((uint16_t)((k < 2 ? w[kv].x : w[kv].y) >> (16 * (k & 1))));
+            x[k] = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h), scale));
+        }
+        uint16_t* b16 = kv ? a.b16[1] : a.b16[0];
+        float* f32 = kv ? a.f32[1] : a.f32[0];
+        if (b16) {
+            uint32_t z[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t u = k < 2 ? w[i][kv].x : w[i][kv].y;
-                const float2 p = half2_to_float2(e4m3x2_half2((uint16_t)(u >> (16 * (k & 1)))));
-                x[2 * k] = p.x * (kv ? s[i].y : s[i].x);
-                x[2 * k + 1] = p.y * (kv ? s[i].y : s[i].x);
+                const __nv_bfloat162 y = __float22bfloat162_rn(x[k]);
+                z[k] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            uint16_t* b16 = kv ? a.b16[1] : a.b16[0];
-            float* f32 = kv ? a.f32[1] : a.f32[0];
-            if (b16) {
-                uint32_t z[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) z[k] = (uint32_t)f32_to_bf16_bits(x[2 * k]) | (uint32_t)f32_to_bf16_bits(x[2 * k + 1]) << 16;
-                *reinterpret_cast<uint4*>(b16 + at[i] * 8) = make_uint4(z[0], z[1], z[2], z[3]);
-            }
-            if (f32) {
-                *reinterpret_cast<float4*>(f32 + at[i] * 8) = make_float4(x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<float4*>(f32 + at[i] * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
-            }
+            *reinterpret_cast<uint4*>(b16 + at * 8) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        if (f32) {
+            *reinterpret_cast<float4*>(f32 + at * 8) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+            *reinterpret_cast<float4*>(f32 + at * 8 + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
         }
     }
 }
@@ -226,7 +230,7 @@ extern "C" int hs_kv8_read(const hs_kv8_cache* cache, const long long* slot, int
     if (!n_tokens) return HS_OK;
     const int per = cache->n_kv_heads * cache->head_dim / 8;
     hs::Kv8ReadArgs a = {kv8_geom(cache), slot, n_tokens, per, {k16, v16}, {k32, v32}};
-    const long long threads = ((long long)n_tokens * per + hs::kRead8Ahead - 1) / hs::kRead8Ahead;
+    const long long threads = (long long)n_tokens * per;  // at most 2^32
     auto kern = cache->head_dim == 64 ? hs::kv8_read_kernel<64> : hs::kv8_read_kernel<128>;
     if (launch_pdl(kern, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;

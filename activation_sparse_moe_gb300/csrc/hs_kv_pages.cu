@@ -12,18 +12,33 @@ namespace hs {
 constexpr int kPageThreads = 256, kPageWarps = kPageThreads / 32;
 constexpr int kMaxPools = 64;
 
-// What release and compact keep between their steps.  The arrivals and the bits are
+// What release and compact keep between their steps.  The arrivals and the marks are
 // zero between calls; the rest is written before it is read.
 struct PageScratch {
     int* arrived;     // CTAs that are done with their rows
     int* totals;      // compact: used pages, those of them below that number, moves, refused
-    uint32_t* bits;   // [words] a bit a page: release: to be given back; compact: used
-    int* before;      // [words] compact: used pages before a word's first
+    uint8_t* mark;    // [n_pages] 1: release: to be given back; compact: used (bytes, for a store each; bits would take atomics)
+    int* before;      // [words] compact: used pages before the first of 32
     int* move_of;     // [n_pages] compact: the move that takes a page away
     int* moved;       // [n_pages / 2] compact: a move's count of owners
 };
 
 __host__ __device__ inline int page_words(int n_pages) { return (n_pages + 31) >> 5; }
+
+// The marks of 64 pages (four times 16 bytes, past the pool zeros) as two words of bits.
+__device__ __forceinline__ void marks64(const uint8_t* mark, uint32_t (&word)[2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        word[k] = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(mark) + 2 * k + j);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) word[k] |= ((u[i] | u[i] >> 7 | u[i] >> 14 | u[i] >> 21) & 15u) << (16 * j + 4 * i);
+        }
+    }
+}
 
 struct PageRows {
     const int* cached;
@@ -170,12 +185,12 @@ __global__ void __launch_bounds__(kPageThreads) kv_fork_kernel(const ForkArgs a)
 struct CopyArgs {
     uint8_t* pool[kMaxPools];
     int pools, n_pages, n, segments;
-    uint32_t page_bytes;
+    uint32_t page_bytes, segment;  // of a page; that a CTA copies of it
     const int *src, *dst;
 };
 
-constexpr int kCopyThreads = 128, kCopyAhead = 4;
-constexpr uint32_t kSegment = kCopyThreads * kCopyAhead * 16;  // bytes that a CTA copies at a time
+constexpr int kCopyThreads = 128, kCopyAhead = 5;
+constexpr uint32_t kSegment = kCopyThreads * kCopyAhead * 16;  // bytes that a CTA copies at a time, at most
 
 // A CTA takes one segment of the pages of one pool, and every gridDim.x-th pair: it
 // reads 128 of its pairs at a time and keeps those that are ones, so that a long list
@@ -203,19 +218,19 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const CopyArgs a)
         __syncthreads();
         for (int y = blockIdx.y; y < a.pools * a.segments; y += gridDim.y) {
             uint8_t* pool = a.pool[y / a.segments];
-            const uint32_t from = (uint32_t)(y % a.segments) * kSegment + (uint32_t)tid * 16;
+            const uint32_t first = (uint32_t)(y % a.segments) * a.segment, end = min(first + a.segment, a.page_bytes), from = first + (uint32_t)tid * 16;
             for (int j = 0; j < count; ++j) {
                 const uint8_t* src = pool + (size_t)todo[j].x * a.page_bytes;
                 uint8_t* dst = pool + (size_t)todo[j].y * a.page_bytes;
                 uint4 v[kCopyAhead];
 #pragma unroll
                 for (int k = 0; k < kCopyAhead; ++k)
-                    if (from + k * kCopyThreads * 16 < a.page_bytes)
-                        v[k] = *reinterpret_cast<const uint4*>(src + from + k * kCopyThreads * 16);
+                    if (from + k * kCopyThreads * 16 < end)
+                        v[k] = __ldcs(reinterpret_cast<const uint4*>(src + from + k * kCopyThreads * 16));
 #pragma unroll
                 for (int k = 0; k < kCopyAhead; ++k)
-                    if (from + k * kCopyThreads * 16 < a.page_bytes)
-                        *reinterpret_cast<uint4*>(dst + from + k * kCopyThreads * 16) = v[k];
+                    if (from + k * kCopyThreads * 16 < end)
+                        __stcs(reinterpret_cast<uint4*>(dst + from + k * kCopyThreads * 16), v[k]);
             }
         }
         __syncthreads();
@@ -254,40 +269,39 @@ __global__ void __launch_bounds__(kPageThreads) kv_release_kernel(const ReleaseA
             if (!(in_place && c < stay)) dst[c] = c < stay ? page : -1;
             if (c >= stay && a.r.there(page) && atomicSub(a.shared + page, 1) <= 0) {
                 atomicAdd(a.shared + page, 1);
-                atomicOr(a.s.bits + (page >> 5), 1u << (page & 31));
+                a.s.mark[page] = 1;
             }
         }
     }
     if (!last_to_arrive(a.s.arrived)) return;
+    __shared__ uint2 found[kPageThreads * 2];  // of 32 pages: those to be given back, and how many come before them
     const long long tail = a.counters_in[1];
     const uint32_t tail_m = ring_at(tail, a.r.n_pages), np = (uint32_t)a.r.n_pages;
     const int words = page_words(a.r.n_pages);
     uint32_t done = 0;
-    for (int w0 = 0; w0 < words; w0 += kPageThreads * 4) {  // a thread four words that follow one another
-        uint32_t v[4];
-        int mine = 0, all;
+    for (int w0 = 0; w0 < words; w0 += kPageThreads * 2) {  // a thread 64 pages that follow one another
+        uint32_t v[2] = {0, 0};
+        const int w = w0 + tid * 2;
+        int all;
+        if (w < words) {
+            uint8_t* mark = a.s.mark + (size_t)w * 32;
+            marks64(mark, v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int w = w0 + tid * 4 + k;
-            v[k] = w < words ? __ldcg(a.s.bits + w) : 0u;
-            if (v[k]) a.s.bits[w] = 0;
-            mine += __popc(v[k]);
+            for (int j = 0; j < 4; ++j)
+                if (v[j >> 1]) reinterpret_cast<uint4*>(mark)[j] = make_uint4(0, 0, 0, 0);
         }
-        int at = block_scan(mine, all);
+        const int at = block_scan(__popc(v[0]) + __popc(v[1]), all);
         if (!all) continue;
-        // a word at a time by the whole warp: its pages' places follow one another
-        for (unsigned some = __ballot_sync(~0u, mine != 0); some; some &= some - 1) {
-            const int l = __ffs(some) - 1;
-            uint32_t to = tail_m + (done + (uint32_t)__shfl_sync(~0u, at, l)) % np;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t word = __shfl_sync(~0u, v[k], l);
-                if ((word >> lane) & 1u)
-                    a.ring[(to + (uint32_t)__popc(word & ((1u << lane) - 1))) % np] = (w0 + ((warp << 5) + l) * 4 + k) * 32 + lane;
-                to += (uint32_t)__popc(word);
-            }
+        found[tid * 2] = make_uint2(v[0], (uint32_t)at);
+        found[tid * 2 + 1] = make_uint2(v[1], (uint32_t)(at + __popc(v[0])));
+        __syncthreads();
+        for (int x = warp; x < min(kPageThreads * 2, words - w0); x += kPageWarps) {  // a page a lane
+            const uint2 y = found[x];
+            uint32_t to = tail_m + done + y.y + (uint32_t)__popc(y.x & ((1u << lane) - 1));  // (at most n_pages on)
+            if (to >= np) to -= np;
+            if ((y.x >> lane) & 1u) a.ring[to] = (w0 + x) * 32 + lane;
         }
-        done += (uint32_t)all;
+        done += (uint32_t)all;  // (`found` is written again behind the next scan's barriers)
     }
     if (tid == 0) {
         a.counters_out[0] = a.counters_in[0];
@@ -309,8 +323,8 @@ struct CompactArgs {
     PageScratch s;
 };
 
-// First of three launches: the pages that the rows list, a bit each; the CTA that comes
-// last counts them word by word.
+// First of three launches: the pages that the rows list are marked; the CTA that comes
+// last counts them by thirty-two.
 __global__ void __launch_bounds__(kPageThreads) kv_compact_mark_kernel(const CompactArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -321,34 +335,30 @@ __global__ void __launch_bounds__(kPageThreads) kv_compact_mark_kernel(const Com
 #pragma unroll 4
         for (int c = lane; c < held; c += 32) {
             const int page = src[c];
-            if (a.r.there(page)) atomicOr(a.s.bits + (page >> 5), 1u << (page & 31));
+            if (a.r.there(page)) a.s.mark[page] = 1;
         }
     }
     if (!last_to_arrive(a.s.arrived)) return;
     const int words = page_words(a.r.n_pages);
     int used = 0;
-    for (int w0 = 0; w0 < words; w0 += kPageThreads * 4) {
-        uint32_t v[4];
-        int mine = 0, all;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int w = w0 + tid * 4 + k;
-            v[k] = w < words ? __ldcg(a.s.bits + w) : 0u;
-            mine += __popc(v[k]);
-        }
-        int at = used + block_scan(mine, all);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int w = w0 + tid * 4 + k;
-            if (w < words) a.s.before[w] = at;
-            at += __popc(v[k]);
-        }
+    for (int w0 = 0; w0 < words; w0 += kPageThreads * 2) {
+        uint32_t v[2] = {0, 0};
+        const int w = w0 + tid * 2;
+        int all;
+        if (w < words) marks64(a.s.mark + (size_t)w * 32, v);
+        const int at = used + block_scan(__popc(v[0]) + __popc(v[1]), all);
+        if (w < words) a.s.before[w] = at;
+        if (w + 1 < words) a.s.before[w + 1] = at + __popc(v[0]);
         used += all;
     }
     __syncthreads();
     if (tid == 0) {
         int below = used;  // used pages among the first `used` ones
-        if (used < a.r.n_pages) below = a.s.before[used >> 5] + __popc(__ldcg(a.s.bits + (used >> 5)) & ((1u << (used & 31)) - 1));
+        if (used < a.r.n_pages) {
+            uint32_t v[2];
+            marks64(a.s.mark + (size_t)(used >> 6) * 64, v);
+            below = a.s.before[used >> 5] + __popc(v[used >> 5 & 1] & ((1u << (used & 31)) - 1));
+        }
         const int moves = used - below, over = max(moves - a.max_copies, 0);
         a.s.totals[0] = used, a.s.totals[1] = below, a.s.totals[2] = over ? 0 : moves, a.s.totals[3] = over;
         a.counters_out[0] = over ? a.counters_in[0] : 0;
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(kPageThreads) kv_compact_mark_kernel(const Com
     }
 }
 
-// Second: a warp a word.  The k-th used page past the first `used` ones goes into the
+// Second: a warp 32 pages.  The k-th used page past the first `used` ones goes into the
 // k-th free one among them.
 __global__ void __launch_bounds__(kPageThreads) kv_compact_list_kernel(const CompactArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -367,12 +377,11 @@ __global__ void __launch_bounds__(kPageThreads) kv_compact_list_kernel(const Com
     const bool ok = a.s.totals[3] == 0;
     const int words = page_words(a.r.n_pages);
     for (int w = blockIdx.x * kPageWarps + warp; w < words; w += gridDim.x * kPageWarps) {
-        const uint32_t word = a.s.bits[w];
-        const int page = w * 32 + lane, rank = a.s.before[w] + __popc(word & ((1u << lane) - 1));
-        __syncwarp();
-        if (lane == 0) a.s.bits[w] = 0;  // for the next call
+        const int page = w * 32 + lane;
+        const bool live = a.s.mark[page] != 0;  // (of whole words: past the pool 0)
+        const int rank = a.s.before[w] + __popc(__ballot_sync(~0u, live) & ((1u << lane) - 1));
         if (page >= a.r.n_pages) continue;
-        const bool live = (word >> lane) & 1u;
+        if (live) a.s.mark[page] = 0;  // for the next call
         const int owners = a.shared_in[page];
         if (!ok) {
             a.shared_out[page] = owners;
@@ -463,16 +472,17 @@ hs::PageRows rows_of(const int* cached, int n, int page_tokens, int n_pages, int
 }
 
 size_t scratch_bytes(int n_pages, uint8_t* base, hs::PageScratch* s) {
-    const size_t words = round_up((size_t)hs::page_words(n_pages) * 4, 256), pages = round_up((size_t)n_pages * 4, 256);
+    const size_t marks = round_up((size_t)n_pages, 256), words = round_up((size_t)hs::page_words(n_pages) * 4, 256),
+                 pages = round_up((size_t)n_pages * 4, 256);
     if (s) {
         s->arrived = reinterpret_cast<int*>(base);
         s->totals = s->arrived + 4;
-        s->bits = reinterpret_cast<uint32_t*>(base + 256);
-        s->before = reinterpret_cast<int*>(base + 256 + words);
-        s->move_of = reinterpret_cast<int*>(base + 256 + 2 * words);
-        s->moved = reinterpret_cast<int*>(base + 256 + 2 * words + pages);
+        s->mark = base + 256;
+        s->before = reinterpret_cast<int*>(base + 256 + marks);
+        s->move_of = reinterpret_cast<int*>(base + 256 + marks + words);
+        s->moved = reinterpret_cast<int*>(base + 256 + marks + words + pages);
     }
-    return 256 + 2 * words + 2 * pages;
+    return 256 + marks + words + 2 * pages;
 }
 
 // CTAs for rows a warp each, up to two on an SM.
@@ -527,8 +537,9 @@ extern "C" int hs_kv_copy_pages(void* const* pools, int n_pools, long long page_
     a.pools = n_pools, a.n_pages = n_pages, a.n = n_copies, a.src = src, a.dst = dst;
     a.page_bytes = (uint32_t)page_bytes;
     a.segments = (int)((page_bytes + hs::kSegment - 1) / hs::kSegment);
+    a.segment = (uint32_t)round_up((size_t)(page_bytes + a.segments - 1) / a.segments, 16);
     const int y = (int)std::min((long long)n_pools * a.segments, 65535ll);
-    const int x = std::max(1, std::min(n_copies, sms * 16 / y));
+    const int x = std::max(1, std::min(n_copies, sms * 64 / y));
     if (launch_pdl(hs::kv_copy_kernel, dim3(x, y), dim3(hs::kCopyThreads), 0, reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
         return HS_ERR_CUDA;
     return launch_err();

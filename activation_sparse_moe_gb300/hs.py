@@ -319,7 +319,7 @@ def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
 # sizes, the slots' type, rows that do not follow one another.
 _current = None   # torch's own lookups of the current device and its raw stream
 _i64 = None       # torch.int64
-_b16 = None       # torch.bfloat16
+_i32 = _b16 = None  # and its int32 and bfloat16
 
 
 def _kv4_stream(stream):
@@ -335,11 +335,11 @@ def _kv4_stream(stream):
 
 def _kv4_refuse(fn):
     """The first call of a process looks at the tensors' types before they are known: True to look again."""
-    global _i64, _b16
+    global _i64, _i32, _b16
     if _i64 is not None:
         raise HsError(fn, HS_ERR_INVALID_ARG)
     import torch
-    _i64, _b16 = torch.int64, torch.bfloat16
+    _i64, _i32, _b16 = torch.int64, torch.int32, torch.bfloat16
     return True
 
 
@@ -489,18 +489,8 @@ def hs_kv8_attention(cache: hs_kv8_cache, q, q_start, seq_len, table, n_seqs, ma
 
 
 # Pages shared, copied, given back and moved.  The pointers do not tell the
-# library how long the tensors behind them are, so each is looked at here.
-def _kv_fits(fn, t32, t64, sizes):
-    """t32: int32 tensors, t64: int64 ones, contiguous, of at least the sizes beside them."""
-    import torch
-    for tensors, dtype in ((t32, torch.int32), (t64, torch.int64)):
-        for t, n in tensors:
-            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n:
-                raise HsError(fn, HS_ERR_INVALID_ARG)
-    if min(sizes) < 0:
-        raise HsError(fn, HS_ERR_INVALID_ARG)
-
-
+# library how long the tensors behind them are, nor their types, so each is
+# looked at here, in one expression: a loop over them costs as much as the call.
 class make_kv_pools:
     """The pools of a model's layers for hs_kv_copy_pages: device tensors, which
     are kept, all of one size."""
@@ -509,7 +499,7 @@ class make_kv_pools:
         pools = list(pools)
         if not pools or any(not p.is_contiguous() or p.nbytes != pools[0].nbytes for p in pools):
             raise HsError("make_kv_pools", HS_ERR_INVALID_ARG)
-        self.tensors, self.nbytes = pools, pools[0].nbytes
+        self.tensors, self.nbytes, self.n = pools, pools[0].nbytes, len(pools)
         self.c = (C.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
 
 
@@ -519,15 +509,26 @@ def hs_kv_pages_workspace_size(n_pages) -> int:
 
 def hs_kv_fork(parent, child, length, n_forks, cached_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared, ring,
                counters_in, table_out, len_out, copy_src, copy_dst, counters_out, short, stream=None):
-    """Tensors of the header's types and sizes, each contiguous."""
+    """Tensors of the header's types and sizes, each contiguous; table_out may be table_in."""
     cells = n_seqs * table_width
-    _kv_fits("hs_kv_fork", ((parent, n_forks), (child, n_forks), (length, n_forks), (cached_len, n_seqs), (table_in, cells),
-                            (shared, n_pages), (ring, n_pages), (table_out, cells), (len_out, n_seqs), (copy_src, n_forks),
-                            (copy_dst, n_forks), (short, 1)), ((counters_in, 2), (counters_out, 2)), (n_forks, n_seqs, n_pages, table_width))
-    st = lib().hs_kv_fork(parent.data_ptr(), child.data_ptr(), length.data_ptr(), n_forks, cached_len.data_ptr(), n_seqs, page_tokens,
-                          n_pages, table_in.data_ptr(), table_width, shared.data_ptr(), ring.data_ptr(), counters_in.data_ptr(),
-                          table_out.data_ptr(), len_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), counters_out.data_ptr(),
-                          short.data_ptr(), _kv4_stream(stream))
+    if not (parent.dtype is child.dtype is length.dtype is cached_len.dtype is table_in.dtype is shared.dtype is ring.dtype
+            is table_out.dtype is len_out.dtype is copy_src.dtype is copy_dst.dtype is short.dtype is _i32
+            and counters_in.dtype is counters_out.dtype is _i64
+            and parent.is_contiguous() and child.is_contiguous() and length.is_contiguous() and cached_len.is_contiguous()
+            and table_in.is_contiguous() and shared.is_contiguous() and ring.is_contiguous() and counters_in.is_contiguous()
+            and table_out.is_contiguous() and len_out.is_contiguous() and copy_src.is_contiguous() and copy_dst.is_contiguous()
+            and counters_out.is_contiguous()
+            and parent.numel() >= n_forks <= child.numel() and length.numel() >= n_forks <= copy_src.numel()
+            and copy_dst.numel() >= n_forks and cached_len.numel() >= n_seqs <= len_out.numel() and table_in.numel() >= cells <= table_out.numel()
+            and shared.numel() >= n_pages <= ring.numel() and counters_in.numel() >= 2 <= counters_out.numel() and short.numel()):
+        if _kv4_refuse("hs_kv_fork"):
+            return hs_kv_fork(parent, child, length, n_forks, cached_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared,
+                              ring, counters_in, table_out, len_out, copy_src, copy_dst, counters_out, short, stream)
+    st = (_lib or lib()).hs_kv_fork(
+        parent.data_ptr(), child.data_ptr(), length.data_ptr(), n_forks, cached_len.data_ptr(), n_seqs, page_tokens, n_pages,
+        table_in.data_ptr(), table_width, shared.data_ptr(), ring.data_ptr(), counters_in.data_ptr(), table_out.data_ptr(),
+        len_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), counters_out.data_ptr(), short.data_ptr(),
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv_fork", st)
 
@@ -536,11 +537,12 @@ def hs_kv_copy_pages(pools, page_bytes, n_pages, src, dst, n_copies, stream=None
     """pools: make_kv_pools of the layers' pools, or the tensors themselves."""
     if not isinstance(pools, make_kv_pools):
         pools = make_kv_pools(pools)
-    if pools.nbytes < n_pages * page_bytes:
-        raise HsError("hs_kv_copy_pages", HS_ERR_INVALID_ARG)
-    _kv_fits("hs_kv_copy_pages", ((src, n_copies), (dst, n_copies)), (), (0,))
-    st = lib().hs_kv_copy_pages(pools.c, len(pools.tensors), page_bytes, n_pages, src.data_ptr(), dst.data_ptr(), n_copies,
-                                _kv4_stream(stream))
+    if not (src.dtype is dst.dtype is _i32 and src.is_contiguous() and dst.is_contiguous() and src.numel() >= n_copies <= dst.numel()
+            and pools.nbytes >= n_pages * page_bytes):
+        if _kv4_refuse("hs_kv_copy_pages"):
+            return hs_kv_copy_pages(pools, page_bytes, n_pages, src, dst, n_copies, stream)
+    st = (_lib or lib()).hs_kv_copy_pages(pools.c, pools.n, page_bytes, n_pages, src.data_ptr(), dst.data_ptr(), n_copies,
+                                          _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv_copy_pages", st)
 
@@ -549,13 +551,25 @@ def hs_kv_release(cached_len, keep_len, n_seqs, page_tokens, n_pages, table_in, 
                   len_out, counters_out, workspace=None, workspace_bytes=None, stream=None):
     """Tensors of the header's types and sizes, each contiguous; table_out may be table_in."""
     cells = n_seqs * table_width
-    _kv_fits("hs_kv_release", ((cached_len, n_seqs), (keep_len, n_seqs), (table_in, cells), (shared, n_pages), (ring, n_pages),
-                               (table_out, cells), (len_out, n_seqs)), ((counters_in, 2), (counters_out, 2)),
-             (n_seqs, n_pages, table_width))
-    ws, nb = _kv_workspace(workspace, workspace_bytes)
-    st = lib().hs_kv_release(cached_len.data_ptr(), keep_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width,
-                             shared.data_ptr(), ring.data_ptr(), counters_in.data_ptr(), table_out.data_ptr(), len_out.data_ptr(),
-                             counters_out.data_ptr(), ws, nb, _kv4_stream(stream))
+    if not (cached_len.dtype is keep_len.dtype is table_in.dtype is shared.dtype is ring.dtype is table_out.dtype is len_out.dtype is _i32
+            and counters_in.dtype is counters_out.dtype is _i64
+            and cached_len.is_contiguous() and keep_len.is_contiguous() and table_in.is_contiguous() and shared.is_contiguous()
+            and ring.is_contiguous() and counters_in.is_contiguous() and table_out.is_contiguous() and len_out.is_contiguous()
+            and counters_out.is_contiguous()
+            and cached_len.numel() >= n_seqs <= keep_len.numel() and len_out.numel() >= n_seqs
+            and table_in.numel() >= cells <= table_out.numel() and shared.numel() >= n_pages <= ring.numel()
+            and counters_in.numel() >= 2 <= counters_out.numel()):
+        if _kv4_refuse("hs_kv_release"):
+            return hs_kv_release(cached_len, keep_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared, ring, counters_in,
+                                 table_out, len_out, counters_out, workspace, workspace_bytes, stream)
+    if workspace is None:
+        ws, nb = None, 0
+    else:
+        ws, nb = workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes
+    st = (_lib or lib()).hs_kv_release(
+        cached_len.data_ptr(), keep_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width, shared.data_ptr(),
+        ring.data_ptr(), counters_in.data_ptr(), table_out.data_ptr(), len_out.data_ptr(), counters_out.data_ptr(), ws, nb,
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv_release", st)
 
@@ -564,19 +578,25 @@ def hs_kv_compact(cached_len, n_seqs, page_tokens, n_pages, table_in, table_widt
                   shared_out, copy_src, copy_dst, counters_out, short, workspace=None, workspace_bytes=None, stream=None):
     """Tensors of the header's types and sizes, each contiguous; table_out and shared_out may be the inputs."""
     cells = n_seqs * table_width
-    _kv_fits("hs_kv_compact", ((cached_len, n_seqs), (table_in, cells), (shared_in, n_pages), (ring, n_pages), (table_out, cells),
-                               (shared_out, n_pages), (copy_src, max_copies), (copy_dst, max_copies), (short, 1)),
-             ((counters_in, 2), (counters_out, 2)), (n_seqs, n_pages, table_width, max_copies))
-    ws, nb = _kv_workspace(workspace, workspace_bytes)
-    st = lib().hs_kv_compact(cached_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width, shared_in.data_ptr(),
-                             ring.data_ptr(), counters_in.data_ptr(), max_copies, table_out.data_ptr(), shared_out.data_ptr(),
-                             copy_src.data_ptr(), copy_dst.data_ptr(), counters_out.data_ptr(), short.data_ptr(), ws, nb,
-                             _kv4_stream(stream))
+    if not (cached_len.dtype is table_in.dtype is shared_in.dtype is ring.dtype is table_out.dtype is shared_out.dtype is copy_src.dtype
+            is copy_dst.dtype is short.dtype is _i32 and counters_in.dtype is counters_out.dtype is _i64
+            and cached_len.is_contiguous() and table_in.is_contiguous() and shared_in.is_contiguous() and ring.is_contiguous()
+            and counters_in.is_contiguous() and table_out.is_contiguous() and shared_out.is_contiguous() and copy_src.is_contiguous()
+            and copy_dst.is_contiguous() and counters_out.is_contiguous()
+            and cached_len.numel() >= n_seqs and table_in.numel() >= cells <= table_out.numel()
+            and shared_in.numel() >= n_pages <= shared_out.numel() and ring.numel() >= n_pages
+            and copy_src.numel() >= max_copies <= copy_dst.numel() and counters_in.numel() >= 2 <= counters_out.numel() and short.numel()):
+        if _kv4_refuse("hs_kv_compact"):
+            return hs_kv_compact(cached_len, n_seqs, page_tokens, n_pages, table_in, table_width, shared_in, ring, counters_in, max_copies,
+                                 table_out, shared_out, copy_src, copy_dst, counters_out, short, workspace, workspace_bytes, stream)
+    if workspace is None:
+        ws, nb = None, 0
+    else:
+        ws, nb = workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes
+    st = (_lib or lib()).hs_kv_compact(
+        cached_len.data_ptr(), n_seqs, page_tokens, n_pages, table_in.data_ptr(), table_width, shared_in.data_ptr(), ring.data_ptr(),
+        counters_in.data_ptr(), max_copies, table_out.data_ptr(), shared_out.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(),
+        counters_out.data_ptr(), short.data_ptr(), ws, nb,
+        _current[1](_current[0]()) if stream is None and _current else _kv4_stream(stream))
     if st:
         raise HsError("hs_kv_compact", st)
-
-
-def _kv_workspace(workspace, workspace_bytes):
-    if workspace is None:
-        return None, 0
-    return workspace.data_ptr(), workspace.nbytes if workspace_bytes is None else workspace_bytes

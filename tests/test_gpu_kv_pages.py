@@ -152,7 +152,7 @@ def test_release_of_everything_and_of_nothing():
     again = _kv_pages.release(np.zeros(800, np.int32), keep, 16, r.n_pages, want["table"], want["shared"], want["ring"], want["counters"])
     assert again["counters"] == want["counters"]
     _same(_release(np.zeros(800, np.int32), keep, r, want["table"], want["shared"], want["ring"], want["counters"], ws=ws), again)
-    assert not ws[256:256 + r.n_pages // 8].any() and not ws[:4].any()
+    assert not ws[256:256 + r.n_pages].any() and not ws[:4].any()
 
 
 def test_release_passes_over_pages_outside_the_pool():

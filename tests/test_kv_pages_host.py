@@ -22,7 +22,7 @@ def lib():
 
 # Of 4 rows of 8 entries over 100 pages, 3 forks, 50 copies: every buffer's bytes.
 ROWS = dict(n=4, page=64, pages=100, width=8, stream=None)
-WS = 256 + 2 * 256 + 2 * 512
+WS = 256 + 256 + 256 + 2 * 512
 CALLS = {
     "hs_kv_fork": dict(
         names="parent child length forks cached n page pages table_in width shared ring counters_in table_out len_out copy_src copy_dst "
@@ -56,7 +56,7 @@ def _caller(lib, fn):
 
 def test_workspace_size(lib):
     assert hs.hs_kv_pages_workspace_size(100) == WS
-    assert hs.hs_kv_pages_workspace_size(1 << 20) == 256 + 2 * (1 << 17) + 2 * (1 << 22)
+    assert hs.hs_kv_pages_workspace_size(1 << 20) == 256 + (1 << 20) + (1 << 17) + 2 * (1 << 22)
     assert hs.hs_kv_pages_workspace_size(0) == hs.hs_kv_pages_workspace_size(-1) == hs.hs_kv_pages_workspace_size(1 << 30) == 0
 
 
