@@ -720,3 +720,94 @@ def test_step_in_a_captured_graph():
     free = int(cin[1] - cin[0])
     rows = table.cpu().numpy()
     assert free + int((rows >= 0).sum()) == n_pages
+
+
+def test_a_workspace_shared_with_the_4_bit_cache():
+    """Both kinds of attention on one workspace, in turn."""
+    a, b = _kv8.Requests(41, [900, 3000], [1, 2], 16, 2, 128, 64), _kv4.Requests(42, [2500, 70], [1, 60], 8, 2, 128, 32)
+    need = max(hs.hs_kv8_attention_workspace_size(hs.make_kv8_cache(None, 1, 64, 2, 128), 2, 16),
+               hs.hs_kv4_attention_workspace_size(hs.make_kv4_cache(None, 1, 32, 2, 128), 2, 8))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    first = a.run(hs, 0.09, ws=ws), b.run(hs, 0.09, ws=ws)
+    _close(first[0], a.expected(0.09), 0.09)
+    for _ in range(3):
+        assert torch.equal(a.run(hs, 0.09, ws=ws), first[0]) and torch.equal(b.run(hs, 0.09, ws=ws), first[1])
+
+
+def test_requests_that_fork_decode_are_cut_back_and_move():
+    """Samples of a prompt over the 8-bit cache, as a server runs them: plan, append, attention,
+    fork, release and compact, mirrored byte by byte; every attention against 64 bits."""
+    page, hkv, hq, dim, n_pages, width, rows = 32, 2, 8, 128, 40, 6, 6
+    rng = np.random.default_rng(43)
+    pool, c = _cache(n_pages, page, hkv, dim)
+    mirror = np.full(pool.shape, 0xFF, np.uint8)
+    dev = dict(device="cuda")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, **dev)  # noqa: E731
+    table, ring, shared = torch.full((rows, width), -1, dtype=torch.int32, **dev), torch.from_numpy(rng.permutation(n_pages)).int().cuda(), i32(n_pages)
+    length, out_len, seq, qs, short, src, dst = i32(rows), i32(rows), i32(rows), i32(rows + 1), i32(1), i32(n_pages), i32(n_pages)
+    counters, cout, slot = torch.tensor([0, n_pages], **dev), torch.zeros(2, dtype=torch.int64, **dev), torch.zeros(256, dtype=torch.int64, **dev)
+    ws = torch.zeros(hs.hs_kv8_attention_workspace_size(c, rows, hq), dtype=torch.uint8, **dev)
+    pages_ws = torch.zeros(hs.hs_kv_pages_workspace_size(n_pages), dtype=torch.uint8, **dev)
+    size = hkv * _kv8.record_bytes(page, dim)
+
+    def done(new_length):
+        assert int(short) == 0
+        length.copy_(new_length)
+        counters.copy_(cout)
+
+    def slots_of(i):
+        j = np.arange(int(length[i]))
+        return table[i].cpu().numpy().astype(np.int64)[j // page] * page + j % page
+
+    def step(new):
+        t = sum(new)
+        hs.hs_kv4_plan(length, torch.tensor(new, dtype=torch.int32, **dev), rows, page, n_pages, table, width, ring, counters, 256, table, seq,
+                       qs, slot, None, cout, short)
+        size = 2.0 ** int(rng.integers(-3, 4))
+        k, v, q = _kv4.bf16(rng, (t, hkv, dim), size), _kv4.bf16(rng, (t, hkv, dim)), _kv4.bf16(rng, (t, hq, dim), 1 / size)
+        hs.hs_kv8_append(c, k.cuda(), v.cuda(), slot, t)
+        out = torch.empty((t, hq, dim), dtype=torch.bfloat16, **dev)
+        hs.hs_kv8_attention(c, q.cuda(), qs, seq, table, rows, max(new), 0.09, 0, out, ws)
+        done(seq)
+        _kv8.append(mirror, page, dim, slot[:t].cpu().numpy(), k.float().numpy(), v.float().numpy())
+        at = 0
+        for i, m in enumerate(new):
+            if m:
+                kk, vv = _kv8.read(mirror, page, dim, slots_of(i))
+                _close(out[at:at + m], _kv4.attention(q[at:at + m].double().numpy(), kk, vv, m, len(kk), 0.09), 0.09)
+            at += m
+        _same_bytes(pool, mirror)
+
+    def copied():
+        hs.hs_kv_copy_pages([pool], size, n_pages, src, dst, n_pages)
+        for x, y in zip(src.tolist(), dst.tolist()):
+            if x >= 0:
+                mirror[y] = mirror[x]
+        _same_bytes(pool, mirror)
+
+    def fork(p, ch, m):
+        src.fill_(-1), dst.fill_(-1)
+        a = [torch.tensor(x, dtype=torch.int32, **dev) for x in (p, ch, m)]
+        hs.hs_kv_fork(*a, len(p), length, rows, page, n_pages, table, width, shared, ring, counters, table, out_len, src, dst, cout, short)
+        done(out_len)
+        copied()
+
+    def keep(m):
+        hs.hs_kv_release(length, torch.tensor(m, dtype=torch.int32, **dev), rows, page, n_pages, table, width, shared, ring, counters, table,
+                         out_len, cout, pages_ws)
+        done(out_len)
+    step([45, 0, 0, 70, 0, 0])
+    fork([0, 0, 3], [1, 2, 4], [45, 40, 64])
+    for _ in range(3):
+        step([1, 1, 1, 1, 1, 0])
+    step([3, 2, 0, 0, 40, 0])               # drafts and a chunk
+    keep([46, 1 << 30, 1 << 30, 1 << 30, 65, 0])   # drafts refused, a row cut back in a page of its own
+    step([1, 1, 2, 0, 3, 0])
+    keep([0, 1 << 30, 1 << 30, 0, 1 << 30, 0])     # the prompts end, what was forked off lives on
+    hs.hs_kv_compact(length, rows, page, n_pages, table, width, shared, ring, counters, n_pages, table, shared, src, dst, cout, short, pages_ws)
+    done(length)
+    copied()
+    fork([1], [0], [33])
+    step([1, 1, 1, 90, 1, 0])
+    keep([0] * rows)
+    assert not shared.any() and int(counters[1] - counters[0]) == n_pages and hs.hs_device_status() == hs.HS_OK
