@@ -32,6 +32,7 @@ struct KvAttnArgs {
     const int* table;
     int width, n_seqs, n_tokens, group, rows, tq, min_units, pad, tile_log2;
     uint32_t short_line, short_ctas;  // a line of at most so many units goes to at most so many CTAs (0: no such line)
+    int whole_tiles;     // items of at most so many tiles may go to a CTA each (kv_begin_whole)
     int back;            // a row at position p >= 0 sees the keys from p - back on: window - 1, or all of int
     uint32_t group_inv;  // ceil(2^16 / group)
     float scale_log2;    // scale * log2(e)
@@ -258,7 +259,10 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
 }
 
 // The same by one warp alone, for at most 128 requests: four a lane at most,
-// and neither the CTA's other warps nor shared memory are waited for.
+// and neither the CTA's other warps nor shared memory are waited for.  WHOLE: if no item
+// of at most 32 requests has more than whole_tiles tiles and there are no more items than CTAs, a
+// CTA takes one, and nothing is cut or joined.
+template <bool WHOLE = false>
 __device__ __forceinline__ KvWalk kv_begin_few(const KvAttnArgs& a, uint32_t& total) {
     const int lane = threadIdx.x & 31, per = (a.n_seqs + 31) >> 5;
     uint32_t mine = 0, units[4];
@@ -282,9 +286,28 @@ __device__ __forceinline__ KvWalk kv_begin_few(const KvAttnArgs& a, uint32_t& to
         }
         mine += units[j];
     }
+    KvWalk w;
+    if (WHOLE && per == 1) {
+        const unsigned some = __ballot_sync(~0u, units[0] != 0);
+        const bool tall = min(max(start[1], 0), a.n_tokens) - min(max(start[0], 0), a.n_tokens) > a.tq;  // several row tiles
+        if (warp_max_u32(tall && units[0] ? ~0u : units[0]) <= (uint32_t)(a.g.heads * (a.whole_tiles + a.pad)) &&
+            __popc(some) * a.g.heads <= (int)gridDim.x) {
+            total = 0;
+            w.left = 0;
+            const int nth = (int)blockIdx.x / a.g.heads;  // among the requests that have rows
+            const unsigned is = __ballot_sync(~0u, units[0] != 0 && __popc(some & ((1u << lane) - 1)) == nth);
+            if (!is) return w;
+            w.seq = __ffs(is) - 1, w.head = (int)blockIdx.x - nth * a.g.heads, w.r = 0, w.tile = 0, w.first = true;
+            w.row0 = min(max(__shfl_sync(~0u, start[0], w.seq), 0), a.n_tokens);
+            w.n = min(max(__shfl_sync(~0u, start[1], w.seq), 0), a.n_tokens) - w.row0;
+            w.len = min(max(__shfl_sync(~0u, len[0], w.seq), 0), a.width << a.g.page_log2);
+            kv_set_item(a, w);
+            w.left = (uint32_t)w.units;
+            return w;
+        }
+    }
     const uint32_t incl = warp_scan(mine);
     total = __shfl_sync(~0u, incl, 31);
-    KvWalk w;
     const KvCut cut = kv_cut(a, total);
     w.left = 0;
     if (!total || blockIdx.x >= cut.active) return w;

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
     uint32_t total;
     if (a.n_seqs <= kKvFew) {
         __syncthreads();  // the barriers are ready
-        w = kv_begin_few(a, total);
+        w = kv_begin_few<true>(a, total);
     } else {
         kv_schedule(a, qs, ls, cum);
         w = kv_begin(a, qs, ls, cum);
@@ -614,6 +614,9 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
         a.short_line = items * (uint32_t)(a.pad + 128);
         a.short_ctas = 12 * items;
     }
+    // A CTA for itself takes an item of 8 tiles in 7.1 us where cutting and joining it takes 8.0, one of
+    // 16 in 10.3 and 8.4; eight warps one of 16 in 10.0 and 10.7.
+    a.whole_tiles = KW == 8 ? 16 : 10;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
@@ -622,15 +625,19 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
     return HS_OK;
 }
 
-// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.  Sixteen rows
-// of few items are shared by eight warps along the keys, one CTA an SM in place of two: half
-// as many pieces to join, and room to join 16 of them in shared memory.  us, against four: one request of
-// 131,071 tokens (32 / 2 heads) 24.6 and 27.3, one of 4096 11.8 and 15.2, eight of 2000 11.0 and
-// 14.1; but 16 of 4000 17.8 and 16.1, and up to 128 keys, where nothing is cut, 6.3 and 6.0.
+// Row tiles of 8, 16, 32 or 64: the smallest that holds a request's rows.  Up to sixteen
+// rows of few or of short items are shared by eight warps along the keys, one CTA an SM in place of
+// two: half as many pieces to join, room to join 16 of them in shared memory, and a short item done in half the
+// steps.  us, against four (16 and 4 rows of a kv head): 2 items of 131,071 keys 24.6 and 27.3,
+// of 8000 13.2 and 16.6 (4 rows 10.5 and 11.3), of 500 7.7 and 10.0 (6.0 and 7.1); 128 items of up to 1000 11.1 and
+// 15.2 (9.2 and 12.2); but 32 items of up to 4000 17.4 and 16.6 (14.3 and 12.0), 128 of up to 2000 22.2
+// and 19.4 (17.8 and 15.4), and up to 128 keys 5.8 and 5.6.  The host knows the tables' width only, not the lengths.
 template <int D>
 int launch_rows8(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
+    const int items = a.n_seqs * a.g.heads, keys = a.width << a.g.page_log2;
+    if (rows <= 16 && keys > 128 && (items <= 16 || (items <= std::min(152, sms) && keys <= 1024)))
+        return rows <= 8 ? launch_decode8<D, 1, 1, 8>(a, sms, s) : launch_decode8<D, 2, 1, 8>(a, sms, s);
     if (rows <= 8) return launch_decode8<D, 1, 1, 4>(a, sms, s);
-    if (rows <= 16 && a.n_seqs * a.g.heads <= 16 && a.width << a.g.page_log2 > 128) return launch_decode8<D, 2, 1, 8>(a, sms, s);
     if (rows <= 16) return launch_decode8<D, 2, 1, 4>(a, sms, s);
     if (rows <= 32) return launch_decode8<D, 2, 2, 4>(a, sms, s);
     return launch_decode8<D, 2, 4, 2>(a, sms, s);

@@ -301,6 +301,24 @@ def test_prompts_and_single_tokens_in_one_call(hq, hkv, dim, bound):
     _close(r.run(hs, scale, max_new=bound), r.expected(scale), scale)
 
 
+@pytest.mark.parametrize("n,hkv,most", [(1, 1, 640), (1, 2, 1024), (1, 2, 1025), (5, 3, 600), (5, 3, 641), (31, 2, 300), (32, 4, 500), (32, 5, 200),
+                                        (32, 2, 1000), (33, 2, 500), (32, 10, 90)])
+@pytest.mark.parametrize("group,new,dim", [(4, 1, 128), (16, 1, 64), (3, 6, 128), (12, 2, 64)])
+def test_short_items_of_few_requests(n, hkv, most, group, new, dim):
+    """Items that a CTA takes whole and such that are cut, at the lengths, numbers and tables at which
+    one turns into the other; requests without rows, without keys and without pages among them."""
+    rng = np.random.default_rng(n * most + group)
+    cached = [int(x) for x in rng.integers(0, most, n)]
+    cached[n // 2] = most - new
+    fresh = [new if i == n // 2 or x > 0.2 else 0 for i, x in enumerate(rng.random(n))]
+    r = _kv8.Requests(n + most, cached, fresh, hkv * group, hkv, dim, 64)
+    out = r.run(hs, 0.1)
+    _close(out, r.expected(0.1), 0.1)
+    _close(r.run(hs, 0.1, max_new=1), r.expected(0.1), 0.1)   # (several row tiles a request)
+    wide = torch.cat((torch.from_numpy(r.table), torch.full((n, 40), -1, dtype=torch.int32)), 1).cuda()
+    _close(r.run(hs, 0.1, table=wide), r.expected(0.1), 0.1)
+
+
 @pytest.mark.parametrize("n", [32, 33, 64, 100, 127, 128, 129, 300])
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_of_many_requests(n, new):
