@@ -616,7 +616,7 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
     }
     // A CTA for itself takes an item of 8 tiles in 7.1 us where cutting and joining it takes 8.0, one of
     // 16 in 10.3 and 8.4; eight warps one of 16 in 10.0 and 10.7.
-    a.whole_tiles = KW == 8 ? 16 : 10;
+    a.whole_tiles = KW == 8 ? 17 : 10;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
@@ -631,12 +631,17 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
 // steps.  us, against four (16 and 4 rows of a kv head): 2 items of 131,071 keys 24.6 and 27.3,
 // of 8000 13.2 and 16.6 (4 rows 10.5 and 11.3), of 500 7.7 and 10.0 (6.0 and 7.1); 128 items of up to 1000 11.1 and
 // 15.2 (9.2 and 12.2); but 32 items of up to 4000 17.4 and 16.6 (14.3 and 12.0), 128 of up to 2000 22.2
-// and 19.4 (17.8 and 15.4), and up to 128 keys 5.8 and 5.6.  The host knows the tables' width only, not the lengths.
+// and 19.4 (17.8 and 15.4), and up to 128 keys 5.8 and 5.6.  At 64 channels registers hold 32 rows
+// a warp: 64 windowed items of 18 rows and 1000 keys 12.7 and 14.4 (of up to 4000 keys 21.5 and
+// 20.5).  The host knows the tables' width and the window only, not the lengths.
 template <int D>
-int launch_rows8(KvAttnArgs& a, long long rows, int sms, cudaStream_t s) {
-    const int items = a.n_seqs * a.g.heads, keys = a.width << a.g.page_log2;
-    if (rows <= 16 && keys > 128 && (items <= 16 || (items <= std::min(152, sms) && keys <= 1024)))
+int launch_rows8(KvAttnArgs& a, long long rows, int window, int sms, cudaStream_t s) {
+    const int items = a.n_seqs * a.g.heads, width = a.width << a.g.page_log2, keys = window ? std::min(width, window) : width;
+    const bool brief = items <= std::min(152, sms) && keys <= 1024;
+    if (rows <= 16 && keys > 128 && (items <= 16 || brief))
         return rows <= 8 ? launch_decode8<D, 1, 1, 8>(a, sms, s) : launch_decode8<D, 2, 1, 8>(a, sms, s);
+    if constexpr (D == 64)
+        if (rows > 16 && rows <= 32 && brief) return launch_decode8<D, 4, 1, 8>(a, sms, s);
     if (rows <= 8) return launch_decode8<D, 1, 1, 4>(a, sms, s);
     if (rows <= 16) return launch_decode8<D, 2, 1, 4>(a, sms, s);
     if (rows <= 32) return launch_decode8<D, 2, 2, 4>(a, sms, s);
@@ -707,7 +712,7 @@ extern "C" int hs_kv8_attention(const hs_kv8_cache* cache, const uint16_t* q, lo
     const long long need = std::max((long long)max_new, 1ll) * a.group;
     const long long items = (long long)n_seqs * a.g.heads, keys = items * ((long long)a.width << a.g.page_log2);
     if (need >= (items <= 16 && keys <= 1 << 17 ? 65 : kPrefillRows)) return hs_kv8_prefill(a, dim, sms, s);
-    const int r = dim == 64 ? hs::launch_rows8<64>(a, need, sms, s) : hs::launch_rows8<128>(a, need, sms, s);
+    const int r = dim == 64 ? hs::launch_rows8<64>(a, need, window, sms, s) : hs::launch_rows8<128>(a, need, window, sms, s);
     return r != HS_OK ? r : launch_err();
 }
 

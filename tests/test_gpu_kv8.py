@@ -422,7 +422,7 @@ def test_nan_in_hidden_places_does_not_spread(new):
         _close(torch.from_numpy(got[:-1]), ref[:-1], 0.1)
 
 
-@pytest.mark.parametrize("new,hq,dim", [(3, 4, 128), (3, 2, 64), (7, 8, 128), (20, 4, 64), (16, 8, 64), (70, 4, 128)])
+@pytest.mark.parametrize("new,hq,dim", [(3, 4, 128), (3, 2, 64), (7, 8, 128), (20, 4, 64), (10, 4, 64), (16, 8, 64), (70, 4, 128)])
 @pytest.mark.parametrize("window", [0, 90])
 def test_a_nan_value_that_some_rows_see_and_some_do_not(new, hq, dim, window):
     """NaN in the values of one new token (half of its channels where there are 128) and of one
