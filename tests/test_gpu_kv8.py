@@ -302,7 +302,7 @@ def test_prompts_and_single_tokens_in_one_call(hq, hkv, dim, bound):
 
 
 @pytest.mark.parametrize("n,hkv,most", [(1, 1, 640), (1, 2, 1024), (1, 2, 1025), (5, 3, 600), (5, 3, 641), (31, 2, 300), (32, 4, 500), (32, 5, 200),
-                                        (32, 2, 1000), (33, 2, 500), (32, 10, 90)])
+                                        (32, 2, 1000), (33, 2, 500), (32, 10, 90), (140, 1, 300)])
 @pytest.mark.parametrize("group,new,dim", [(4, 1, 128), (16, 1, 64), (3, 6, 128), (12, 2, 64)])
 def test_short_items_of_few_requests(n, hkv, most, group, new, dim):
     """Items that a CTA takes whole and such that are cut, at the lengths, numbers and tables at which
