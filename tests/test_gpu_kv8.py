@@ -829,3 +829,26 @@ def test_requests_that_fork_decode_are_cut_back_and_move():
     step([1, 1, 1, 90, 1, 0])
     keep([0] * rows)
     assert not shared.any() and int(counters[1] - counters[0]) == n_pages and hs.hs_device_status() == hs.HS_OK
+
+
+def test_two_calls_at_once():
+    """Appends, reads and attention on two streams, a workspace each: what each gives alone."""
+    a, b = _kv8.Requests(44, [4000] * 6, [1] * 6, 32, 2, 128, 64), _kv8.Requests(45, [300, 2000], [200, 90], 8, 2, 64, 16)
+    streams, ws = [torch.cuda.Stream() for _ in range(2)], []
+    made = []
+    for r in (a, b):
+        c = hs.make_kv8_cache(None, r.n_pages, r.page, r.hkv, r.dim)
+        ws.append(torch.zeros(hs.hs_kv8_attention_workspace_size(c, len(r.len), r.hq), dtype=torch.uint8, device="cuda"))
+        first = r.run(hs, 0.09, ws=ws[-1])
+        _close(first, r.expected(0.09), 0.09)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        made.append((hs.make_kv8_cache(r.pool, r.n_pages, r.page, r.hkv, r.dim), r.q.cuda(), i32(r.starts.tolist()), i32(r.len),
+                     torch.from_numpy(r.table).cuda(), len(r.len), max(r.new), torch.empty_like(first), first))
+    torch.cuda.synchronize()
+    for turn in range(10):
+        for s, w, (c, q, qs, ls, table, n, most, out, first) in zip(streams, ws, made):
+            hs.hs_kv8_attention(c, q, qs, ls, table, n, most, 0.09, 0, out, w, stream=s)
+    torch.cuda.synchronize()
+    assert hs.hs_device_status() == hs.HS_OK
+    for m in made:
+        assert torch.equal(m[-1], m[-2])

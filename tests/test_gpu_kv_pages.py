@@ -364,3 +364,37 @@ def test_calls_in_a_graph_and_two_graphs_that_share_a_workspace():
         graphs[0].replay()
     torch.cuda.synchronize()
     _same(_np(**a), _kv_pages.release(r.cached, keep, 16, r.n_pages, r.table, r.shared, r.ring, r.counters))
+
+
+def test_calls_on_other_streams_than_the_current_one():
+    """The stream given, as an object or as its handle; two at once with a workspace each."""
+    r = _kv_pages.Rows(14, 300, 16, 30, 400, share=0.5)
+    keep = (r.cached // 2).astype(np.int32)
+    rel = _kv_pages.release(r.cached, keep, 16, r.n_pages, r.table, r.shared, r.ring, r.counters)
+    com = _kv_pages.compact(r.cached, 16, r.n_pages, r.table, r.shared, r.ring, r.counters, r.n_pages)
+    p, c, m = r.forks(50)
+    frk = _kv_pages.fork(p, c, m, r.cached, 16, r.n_pages, r.table, r.shared, r.ring, r.counters)
+    assert frk["short"] == 0
+    cached, keep_d, table, counters, shared = _d(r.cached), _d(keep), _d(r.table), _d(r.counters, torch.int64), _d(r.shared)
+    i64 = lambda: _i(2, t=torch.int64)  # noqa: E731
+    a = dict(table=_i(300, 30), shared=_d(r.shared), ring=_d(r.ring), len=_i(300), counters=i64())
+    b = dict(table=_i(300, 30), shared=_i(r.n_pages), ring=_d(r.ring), copy_src=_i(r.n_pages), copy_dst=_i(r.n_pages), counters=i64(), short=_i(1))
+    f = dict(table=_i(300, 30), shared=_d(r.shared), len=_i(300), copy_src=_i(50), copy_dst=_i(50), counters=i64(), short=_i(1))
+    ring, fp, fc, fm = _d(r.ring), _d(p), _d(c), _d(m)
+    pool = torch.arange(r.n_pages, dtype=torch.int32, device="cuda").repeat_interleave(64).view(r.n_pages, 64)
+    ws, streams = [_workspace(r.n_pages) for _ in range(2)], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    hs.hs_kv_release(cached, keep_d, 300, 16, r.n_pages, table, 30, a["shared"], a["ring"], counters, a["table"], a["len"], a["counters"], ws[0],
+                     stream=streams[0])
+    hs.hs_kv_compact(cached, 300, 16, r.n_pages, table, 30, shared, b["ring"], counters, r.n_pages, b["table"], b["shared"], b["copy_src"],
+                     b["copy_dst"], b["counters"], b["short"], ws[1], stream=streams[1].cuda_stream)
+    hs.hs_kv_copy_pages([pool], 256, r.n_pages, b["copy_src"], b["copy_dst"], r.n_pages, stream=streams[1])
+    hs.hs_kv_fork(fp, fc, fm, 50, cached, 300, 16, r.n_pages, table, 30, f["shared"], ring, counters, f["table"], f["len"], f["copy_src"],
+                  f["copy_dst"], f["counters"], f["short"], stream=streams[2].cuda_stream)
+    torch.cuda.synchronize()
+    _same(_np(**a), rel)
+    _same(_np(**b), com)
+    _same(_np(**f), frk)
+    for x, y in zip(com["copy_src"], com["copy_dst"]):
+        if x >= 0:
+            assert int(pool[y, 63]) == x
