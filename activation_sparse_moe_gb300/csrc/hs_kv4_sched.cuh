@@ -32,6 +32,7 @@ struct KvAttnArgs {
     const int* table;
     int width, n_seqs, n_tokens, group, rows, tq, min_units, pad, tile_log2;
     uint32_t short_line, short_ctas;  // a line of at most so many units goes to at most so many CTAs (0: no such line)
+    float least_run;     // a CTA takes at least least_run * sqrt(units of the line): see the chunk kernel that sets it (0: min_units)
     int whole_tiles;     // items of at most so many tiles may go to a CTA each (kv_begin_whole)
     int back;            // a row at position p >= 0 sees the keys from p - back on: window - 1, or all of int
     uint32_t group_inv;  // ceil(2^16 / group)
@@ -170,6 +171,7 @@ struct KvCut {
 __device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, uint32_t total) {
     KvCut c;
     c.active = max(1u, min(gridDim.x, total / (uint32_t)a.min_units));
+    if (a.least_run > 0.f) c.active = min(c.active, max(1u, (uint32_t)((float)total / fmaxf(1.f, a.least_run * sqrtf((float)total)))));
     if (total <= a.short_line) c.active = min(c.active, a.short_ctas);
     c.q = total / c.active;
     c.more = total - c.q * c.active;

@@ -20,6 +20,8 @@
 // converting warps' instructions compete with the softmax's: places of the tiles by
 // immediate offsets and one look a chunk for NaN instead of four took a prompt of 4096 tokens (32 / 8 heads) from
 // 179 to 150 us, 913 TFLOP/s, 48% of the measured bf16 peak; without any conversion it takes 146.
+#include <cmath>
+
 #include "hs_kv4_join.cuh"
 #include "hs_kv8.cuh"
 #include "hs_tc.cuh"
@@ -169,6 +171,33 @@ __device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk
     }
 }
 
+// For at most 32 requests: puts w at the CTA's own item if no item has more than
+// whole_tiles tiles and there are no more items than CTAs; nothing is then cut or joined.
+// False (in every CTA alike) if not so.  Called by a whole warp.
+__device__ __forceinline__ bool begin_whole_items(const KvAttnArgs& a, KvWalk& w) {
+    const int lane = threadIdx.x & 31;
+    int n = 0, len = 0, row_tiles = 0, tiles = 0;
+    if (lane < a.n_seqs) kv_request(a, a.q_start, a.seq_len, lane, n, len);
+    if (n) {
+        row_tiles = (n + a.tq - 1) / a.tq;
+        // the last row tile sees the most; with a window one that begins elsewhere in a tile may see one more
+        tiles = kv_span_tiles(kv_span(a, n, len, row_tiles - 1));
+        if (row_tiles > 1 && a.back != INT32_MAX) tiles = max(tiles, kv_span_tiles(kv_span(a, n, len, 0))) + 1;
+    }
+    const uint32_t items = (uint32_t)(row_tiles * a.g.heads), upto = warp_scan(items);
+    if (warp_max_s32(tiles) > a.whole_tiles || __shfl_sync(~0u, upto, 31) > gridDim.x) return false;
+    w.left = 0;
+    const unsigned past = __ballot_sync(~0u, upto > blockIdx.x);
+    if (!past) return true;
+    w.seq = __ffs(past) - 1;
+    const int rest = (int)(blockIdx.x - __shfl_sync(~0u, upto - items, w.seq)), of = __shfl_sync(~0u, row_tiles, w.seq);
+    w.head = rest / of, w.r = rest - w.head * of, w.tile = 0, w.first = true;
+    w.n = __shfl_sync(~0u, n, w.seq), w.len = __shfl_sync(~0u, len, w.seq), w.row0 = kv_start(a, a.q_start, w.seq);
+    kv_set_item(a, w);
+    w.left = (uint32_t)w.units;
+    return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttnArgs a) {
     using C = Prefill8Cfg<D>;
@@ -204,14 +233,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
     pdl_wait();
     pdl_trigger();
     tc_fence_before();
-    kv_schedule(a, qs, ls, cum);
-    tc_fence_after();
-    const uint32_t tmem = warp_max_u32(sh.tmem);  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
     // A warp's place in the line, in shared memory: looked at once an item.
     __shared__ KvWalk walks[kPfThreads / 32], coming[8];
+    __shared__ bool whole_items;
     KvWalk& w = walks[warp];
-    if (warp == 0) walks[0] = kv_begin(a, qs, ls, cum);
+    if (warp == 0) {
+        KvWalk v;
+        const bool ok = a.n_seqs <= 32 && begin_whole_items(a, v);
+        if (ok) walks[0] = v;
+        whole_items = ok;
+    }
     __syncthreads();
+    if (!whole_items) {
+        kv_schedule(a, qs, ls, cum);
+        if (warp == 0) walks[0] = kv_begin(a, qs, ls, cum);
+        __syncthreads();
+    }
+    tc_fence_after();
+    const uint32_t tmem = warp_max_u32(sh.tmem);  // S and P of the row tiles at columns 0 and 128, O at 256 and 384
     if (warp) w = walks[0];
     __syncthreads();
     auto next_piece = [&]() {
@@ -807,7 +846,9 @@ int launch_prefill8(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tq = kPfRows / a.group;
     a.tile_log2 = 7;
     a.min_units = 1;
+    a.least_run = 1.4f / sqrtf((float)a.g.heads * (float)(((long long)a.n_tokens + (long long)a.n_seqs * (a.tq - 1)) / a.tq));
     a.pad = 4;
+    a.whole_tiles = 10;
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
     static_assert(Prefill8Cfg<D>::smem(kKvMaxSeqs) <= kPfMaxSmem, "shared memory");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;

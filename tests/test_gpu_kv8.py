@@ -643,7 +643,7 @@ def test_attention_strides_streams_and_reuse_of_the_workspace():
 
 
 @pytest.mark.parametrize("ctx,new,hq,hkv,dim", [([900] * 5, [200] * 5, 16, 4, 128), ([1500, 40, 700], [1, 130, 333], 8, 2, 64),
-                                                ([3000] * 40, [1] * 40, 32, 8, 128), ([2000] * 9, [3] * 9, 32, 2, 128),
+                                                ([1500] * 24, [1] * 24, 32, 8, 128), ([2000] * 9, [3] * 9, 32, 2, 128),
                                                 # one row tile: joins in shared memory (few pieces), from memory (many)
                                                 ([1500] * 14, [3] * 14, 32, 2, 128), ([3000] * 6, [40] * 6, 4, 4, 64),
                                                 ([700, 0, 65], [40, 128, 1], 8, 8, 128), ([20000], [9], 16, 4, 64),
