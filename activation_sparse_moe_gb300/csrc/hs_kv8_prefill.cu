@@ -54,7 +54,7 @@ struct PfShared {
     uint32_t nan_keys[kPfInfo][2][4];  // by group of channels: the keys whose values are
     uint32_t tmem;
     // (Behind what every tile reads: before it, with those words elsewhere, chunks took 1% more.)
-    uint64_t pieces_full, products_done;
+    uint64_t pieces_full[2], products_done;
     int join_last[2];   // by row tile
     int direct[2][2];   // by end of the run (0: its first piece) and row tile: the item's other piece is there
 };
@@ -96,78 +96,96 @@ __device__ __noinline__ void add_pieces_apart(const KvAttnArgs& a, const KvWalk&
     add_pieces<D, 4, 2>(a, w, warp, warps, row0, row1, c, first, step, count, final);
 }
 
-// The same by the 256 softmax threads of a CTA that has no work left: its
-// shared memory is free, and the pieces (at most kJoin of them) come in whole by
-// bulk copies.  A few loops of little code: that of add_pieces runs once a call, and
-// costs fetching it besides the rounds of loads (48 rows of five pieces: 9,400
-// cycles, here 5,800; 16 requests of three drafts gained 1.6 of 25.2 us).  The
-// operations and their order are those of add_pieces.
+// Rows row0 <= row < row1 of the item whose `count` pieces (at most kJoin) begin in CTA c,
+// added into out by the 256 softmax threads of a CTA that has no work left: its shared memory
+// is free, and the pieces come in by bulk copies, as many rows at a time as half of it
+// holds, the next ones under the addition.  The weights are worked out a thread a row.
+// (Loads into registers and shuffles, as add_pieces has them, took 33 us for nine pieces of 256 rows; this
+// a fifth.)  The operations and their order are those of add_pieces and weigh, so that
+// the result does not depend on which CTA comes last.
 template <int D>
-__device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk& w, int c, int count, int rows) {
-    constexpr int kL = D / 8, kR = 32 / kL, kP = kJoin / kL, kAtOnce = 4;
-    const int tid = threadIdx.x, lane = tid & 31, sub = lane / kL, i8 = lane % kL;
+__device__ __noinline__ void add_pieces_at_end(const KvAttnArgs& a, const KvWalk& w, int c, int count, int row0, int row1) {
+    constexpr int kLanes = D / 8, kV = D / 4, kHalf = (Prefill8Cfg<D>::kPiecesRoom - 1024) / 2 & ~15;
+    static_assert(kHalf >= kJoin * D * 4 && kJoin == 16 && 256 * kJoin * 4 <= 8 * 2048, "room");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* room = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* buffers = room + Prefill8Cfg<D>::kPiecesRoom;
-    float* weights = reinterpret_cast<float*>(buffers);  // [row][kJoin]
-    uint64_t* bar = &reinterpret_cast<PfShared*>(buffers + 8 * 2048)->pieces_full;
-    const uint32_t bytes = (uint32_t)(rows * D * 4);
-    float* inv = weights + 128 * kJoin;
-    if (tid == 224) {  // (of the idle row tile)
+    float* weights = reinterpret_cast<float*>(buffers);            // [kJoin][256]
+    float* inv = reinterpret_cast<float*>(buffers - 1024);         // [256]
+    uint64_t* bars = reinterpret_cast<PfShared*>(buffers + 8 * 2048)->pieces_full;
+    const int rows = row1 - row0, at_once = min(rows, kHalf / (count * D * 4)), rounds = (rows + at_once - 1) / at_once;
+    auto fetch = [&](int k) {  // by one warp, a piece a lane
+        const int r = k * at_once;
+        const uint32_t bytes = (uint32_t)(min(at_once, rows - r) * D * 4);
+        if (lane == 0) mbar_arrive_expect_tx(bars + (k & 1), bytes * (uint32_t)count);
+        __syncwarp();
+        if (lane < count)
+            bulk_g2s(room + (k & 1) * kHalf + lane * (at_once * D * 4), a.part_o + (piece_slot(c, lane) * a.rows + row0 + r) * D, bytes,
+                     bars + (k & 1), policy_evict_first());
+        __syncwarp();
+    };
+    if (warp == 7) {
         asm volatile("fence.proxy.async;" ::: "memory");  // the other CTAs' writes, seen by the arrival before
-        mbar_arrive_expect_tx(bar, bytes * (uint32_t)count);
-        for (int i = 0; i < count; ++i)
-            bulk_g2s(room + i * bytes, a.part_o + piece_slot(c, i) * a.rows * D, bytes, bar, policy_evict_first());
+        fetch(0);
+        if (rounds > 1) fetch(1);
     }
-    __syncwarp();
-#pragma unroll 1
-    for (int r0 = (tid >> 5) * kR; r0 < rows; r0 += kAtOnce * 8 * kR) {
-        float wt[kAtOnce][kP], part[kAtOnce][kP], m[kAtOnce], l;
+    if (tid < rows) {
+        float m[kJoin], l[kJoin], top = kNoMax;
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const int row = min(r0 + x * 8 * kR + sub, rows - 1);
-            m[x] = kNoMax;
-#pragma unroll
-            for (int y = 0; y < kP; ++y) {
-                float2 ml = make_float2(kNoMax, 0.f);
-                if (i8 + y * kL < count) ml = __ldcg(a.part_ml + (uint32_t)(piece_slot(c, i8 + y * kL) * a.rows + row));
-                wt[x][y] = ml.x, part[x][y] = ml.y;
-                m[x] = fmaxf(m[x], ml.x);
-            }
+        for (int i = 0; i < kJoin; ++i) {
+            float2 ml = make_float2(kNoMax, 0.f);
+            if (i < count) ml = __ldcg(a.part_ml + (uint32_t)(piece_slot(c, i) * a.rows + row0 + tid));
+            m[i] = ml.x, l[i] = ml.y;
+            top = fmaxf(top, ml.x);
         }
 #pragma unroll
-        for (int x = 0; x < kAtOnce; ++x) {
-            const int row = r0 + x * 8 * kR + sub;
-            if (r0 + x * 8 * kR >= rows) break;
-            weigh<kL, kP>(wt[x], part[x], i8, count, m[x], l);
-            if (row >= rows) continue;
-#pragma unroll
-            for (int y = 0; y < kP; ++y) weights[row * kJoin + i8 + y * kL] = wt[x][y];
-            if (i8 == 0) inv[row] = l != 0.f ? 1.f / l : 0.f;
+        for (int i = 0; i < kJoin; ++i) {
+            m[i] = i < count ? ex2(m[i] - top) : 0.f;
+            weights[i * 256 + tid] = m[i];
         }
+        // the sum as lanes i, i + kLanes, ... of a row make it: theirs in turn, then across them
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) {
+            float sum = 0.f;
+#pragma unroll
+            for (int y = i; y < kJoin; y += kLanes) sum = fmaf(m[y], l[y], sum);
+            l[i] = sum;
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) l[i] = __fadd_rn(l[i], l[i + o]);
+        inv[tid] = l[0] != 0.f ? 1.f / l[0] : 0.f;
     }
     asm volatile("bar.sync 3, 256;" ::: "memory");
-    if (!mbar_wait(bar, 0)) {
-        mbar_wait(bar, 0);  // once more: the copies under way write into this CTA's shared memory
-        return;
-    }
+    int given_up = -1;  // the round whose wait gave up: no copy is asked for after it
 #pragma unroll 1
-    for (int at = tid; at < rows * kL; at += 256) {
-        const int row = at / kL, d = at % kL * 8, tok = kv_row_token(a, row);
-        float acc[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int k = 0; k < rounds; ++k) {
+        const int r = k * at_once, n = min(at_once, rows - r);
+        if (given_up < 0 && !warp_wait(bars + (k & 1), k >> 1 & 1)) given_up = k;
+#pragma unroll 2
+        for (int at = tid; at < n * kV; at += 256) {  // four channels of a row
+            const int row = at / kV, d = at % kV * 4, in_item = row0 + r + row, tok = kv_row_token(a, in_item);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint8_t* src = room + (k & 1) * kHalf + (row * D + d) * 4;
 #pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float f = weights[row * kJoin + i];
-            const float4* v = reinterpret_cast<const float4*>(room + i * bytes + (row * D + d) * 4);
-            const float4 v0 = v[0], v1 = v[1];
-            const float from[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(f, from[e], acc[e]);
+            for (int i = 0; i < count; ++i) {
+                const float f = weights[i * 256 + r + row];
+                const float4 v = *reinterpret_cast<const float4*>(src + i * (at_once * D * 4));
+                acc[0] = fmaf(f, v.x, acc[0]), acc[1] = fmaf(f, v.y, acc[1]), acc[2] = fmaf(f, v.z, acc[2]), acc[3] = fmaf(f, v.w, acc[3]);
+            }
+            const float by = inv[r + row];
+            *reinterpret_cast<uint2*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
+                                      (long long)(w.head * a.group + in_item - tok * a.group) * a.o_sh + d) =
+                make_uint2((uint32_t)f32_to_bf16_bits(acc[0] * by) | (uint32_t)f32_to_bf16_bits(acc[1] * by) << 16,
+                           (uint32_t)f32_to_bf16_bits(acc[2] * by) | (uint32_t)f32_to_bf16_bits(acc[3] * by) << 16);
         }
-        *reinterpret_cast<uint4*>(a.out + (long long)(w.row0 + w.r * a.tq + tok) * a.o_st +
-                                  (long long)(w.head * a.group + row - tok * a.group) * a.o_sh + d) = pack_bf16x8(acc, inv[row]);
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        if (warp == 7 && k + 2 < rounds && given_up < 0) fetch(k + 2);
+    }
+    if (given_up >= 0) {  // once more: the copies under way write into this CTA's shared memory
+        for (int k = given_up; k < min(given_up + 2, rounds); ++k) mbar_wait(bars + (k & 1), k >> 1 & 1);
     }
 }
 
@@ -221,7 +239,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
         for (int i = 0; i < kPfSlots; ++i) mbar_init(sh.kv_full + i, kPfApart), mbar_init(sh.kv_empty + i, 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
-        mbar_init(&sh.pieces_full, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(sh.pieces_full + i, 1);
         mbar_init(&sh.products_done, 1);
         fence_mbar_init();
     }
@@ -490,7 +508,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
         uint8_t* q_lines = q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + ((warp & 3) * 32 + sub) * 128;
         auto fetch_q = [&](const KvWalk& v) {
             const int nr = rows_of(v);
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < kB; ++i) {
                 const int qr = x * 128 + (warp & 3) * 32 + i * kAt + sub, qt = kv_row_token(a, qr);
                 uint8_t* dst = q_lines + i * kAt * 128 + (c & 7) * 16;
@@ -817,13 +835,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                 direct = other_is_there();
             }
             tiles += cnt;
-            if (!whole && !direct) {
-                join_pieces(of, joined(), lead(), &sh.join_last[two ? x : 0], meet, [&](int first, int step, int count, bool final) {
-                    const bool at_end = !two && nx.left == 0 && of.count <= kJoin;  // (no copy or product is under way then)
-                    if (at_end && count * rows_of(w) * D * 4 <= C::kPiecesRoom) {
-                        add_pieces_at_end<D>(a, w, of.c, count, rows_of(w));
-                        return;
+            if (!whole && nx.left == 0 && of.count <= kJoin) {  // (no copy or product is under way then, but where a wait gave up)
+                if (!direct) {
+                    meet();  // as join_pieces
+                    if (lead()) {
+                        int before;
+                        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(joined() + of.c) : "memory");
+                        sh.join_last[two ? x : 0] = before == of.count - 1;
+                        if (before == of.count - 1) joined()[of.c] = 0;  // for the next call
                     }
+                } else if (lead()) {
+                    sh.join_last[two ? x : 0] = 0;
+                }
+                asm volatile("bar.sync 3, 256;" ::: "memory");
+                const bool first = *(volatile int*)&sh.join_last[0] != 0, second = two && *(volatile int*)&sh.join_last[1] != 0;
+                if (first || second) add_pieces_at_end<D>(a, w, of.c, of.count, first ? 0 : 128, second ? nrows : min(nrows, 128));
+            } else if (!whole && !direct) {
+                join_pieces(of, joined(), lead(), &sh.join_last[two ? x : 0], meet, [&](int first, int step, int count, bool final) {
                     add_pieces_apart<D>(a, w, two ? warp & 3 : warp, two ? 4 : 8, two ? x * 128 : 0, two && !x ? 128 : nrows, of.c, first, step,
                                         count, final);
                 });
@@ -846,9 +874,12 @@ int launch_prefill8(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tq = kPfRows / a.group;
     a.tile_log2 = 7;
     a.min_units = 1;
-    a.least_run = 1.4f / sqrtf((float)a.g.heads * (float)(((long long)a.n_tokens + (long long)a.n_seqs * (a.tq - 1)) / a.tq));
+    // An item in pieces takes the time of a piece and that of joining them, 1.9 us a tile and about as much a piece:
+    // least in all at pieces of about the square root of the item.  Without that bound, and with every item cut wherever the
+    // line's equal parts end, 64 tokens (16 heads of 4 kv heads) behind 1000 took 45 us, behind 5000 82; now 27 and 44.
+    a.least_run = 1.0f / sqrtf((float)a.g.heads * (float)(((long long)a.n_tokens + (long long)a.n_seqs * (a.tq - 1)) / a.tq));
     a.pad = 4;
-    a.whole_tiles = 10;
+    a.whole_tiles = 12;  // (300 tokens behind 1000, items of up to 11 tiles: 30.6 us whole, 34 cut)
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
     static_assert(Prefill8Cfg<D>::smem(kKvMaxSeqs) <= kPfMaxSmem, "shared memory");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
