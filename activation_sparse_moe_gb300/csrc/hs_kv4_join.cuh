@@ -136,8 +136,9 @@ __device__ __forceinline__ void add_pieces(const KvAttnArgs& a, const KvWalk& w,
 struct KvPieces {
     int c, count;
 };
+template <KvBound B = KvBound::kNone>
 __device__ __forceinline__ KvPieces kv_pieces(const KvAttnArgs& a, const KvWalk& w, uint32_t total) {
-    const KvCut cut = kv_cut(a, total);
+    const KvCut cut = kv_cut<B>(a, total);
     // the unit with which this piece began: of the run's first item the run's, else
     // what the run has left lies before the run's end
     const uint32_t begin = w.first ? cut.at(blockIdx.x) - w.tile : cut.at(blockIdx.x + 1) - w.left, end = begin + (uint32_t)w.tiles;

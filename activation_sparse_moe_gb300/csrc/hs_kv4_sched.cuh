@@ -31,15 +31,15 @@ struct KvAttnArgs {
     const int* seq_len;
     const int* table;
     int width, n_seqs, n_tokens, group, rows, tq, min_units, pad, tile_log2;
-    uint32_t short_line, short_ctas;  // a line of at most so many units goes to at most so many CTAs (0: no such line)
-    float least_run;     // a CTA takes at least least_run * sqrt(units of the line): see the chunk kernel that sets it (0: min_units)
-    int whole_tiles;     // items of at most so many tiles may go to a CTA each (kv_begin_whole)
     int back;            // a row at position p >= 0 sees the keys from p - back on: window - 1, or all of int
     uint32_t group_inv;  // ceil(2^16 / group)
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [2 * CTAs][rows][dim] partial sums
     float2* part_ml;     // [2 * CTAs][rows] (maximum, sum)
     int* joined;         // [3 * CTAs] arrivals of pieces, zero between calls
+    uint32_t short_line, short_ctas;  // a line of at most so many units goes to at most so many CTAs (0: no such line)
+    float least_run;     // a CTA takes at least r = least_run * sqrt(units of the line) where r <= 16: see the chunk kernel that sets it
+    int whole_tiles;     // items of at most so many tiles may go to a CTA each
 };
 
 // Token of a row of a row tile: row / group, for the at most 256 rows there are.
@@ -168,11 +168,18 @@ struct KvCut {
         return (int)(unit < wide ? unit / (q + 1) : more + (unit - wide) / q);
     }
 };
+// What else bounds the CTAs of a line: nothing, or short_line and short_ctas, or least_run.  A matter of compiling:
+// the tests, in kernels that set none of them, cost one long context of 131071 tokens 0.3 of 24.7 us.
+enum class KvBound { kNone, kShortLine, kLeastRun };
+template <KvBound B>
 __device__ __forceinline__ KvCut kv_cut(const KvAttnArgs& a, uint32_t total) {
     KvCut c;
     c.active = max(1u, min(gridDim.x, total / (uint32_t)a.min_units));
-    if (a.least_run > 0.f) c.active = min(c.active, max(1u, (uint32_t)((float)total / fmaxf(1.f, a.least_run * sqrtf((float)total)))));
-    if (total <= a.short_line) c.active = min(c.active, a.short_ctas);
+    if (B == KvBound::kLeastRun) {
+        const float r = fmaxf(1.f, a.least_run * sqrtf((float)total));
+        if (r <= 16.f) c.active = min(c.active, max(1u, (uint32_t)((float)total / r)));
+    }
+    if (B == KvBound::kShortLine && total <= a.short_line) c.active = min(c.active, a.short_ctas);
     c.q = total / c.active;
     c.more = total - c.q * c.active;
     return c;
@@ -242,10 +249,11 @@ __device__ __forceinline__ void kv_place_run(const KvAttnArgs& a, const int* qs,
 }
 
 // Start of this CTA's run (called by whole warps; every lane gets the same).
+template <KvBound B = KvBound::kNone>
 __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, const int* ls, const uint32_t* cum) {
     KvWalk w;
     const uint32_t total = cum[a.n_seqs];
-    const KvCut cut = kv_cut(a, total);
+    const KvCut cut = kv_cut<B>(a, total);
     w.left = 0;
     if (!total || blockIdx.x >= cut.active) return w;
     const uint32_t u0 = cut.at(blockIdx.x);
@@ -264,7 +272,7 @@ __device__ __forceinline__ KvWalk kv_begin(const KvAttnArgs& a, const int* qs, c
 // and neither the CTA's other warps nor shared memory are waited for.  WHOLE: if no item
 // of at most 32 requests has more than whole_tiles tiles and there are no more items than CTAs, a
 // CTA takes one, and nothing is cut or joined.
-template <bool WHOLE = false>
+template <KvBound B = KvBound::kNone, bool WHOLE = false>
 __device__ __forceinline__ KvWalk kv_begin_few(const KvAttnArgs& a, uint32_t& total) {
     const int lane = threadIdx.x & 31, per = (a.n_seqs + 31) >> 5;
     uint32_t mine = 0, units[4];
@@ -310,7 +318,7 @@ __device__ __forceinline__ KvWalk kv_begin_few(const KvAttnArgs& a, uint32_t& to
     }
     const uint32_t incl = warp_scan(mine);
     total = __shfl_sync(~0u, incl, 31);
-    const KvCut cut = kv_cut(a, total);
+    const KvCut cut = kv_cut<B>(a, total);
     w.left = 0;
     if (!total || blockIdx.x >= cut.active) return w;
     const uint32_t u0 = cut.at(blockIdx.x);

@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
     uint32_t total;
     if (a.n_seqs <= kKvFew) {
         __syncthreads();  // the barriers are ready
-        w = kv_begin_few<true>(a, total);
+        w = kv_begin_few<KvBound::kShortLine, true>(a, total);
     } else {
         kv_schedule(a, qs, ls, cum);
-        w = kv_begin(a, qs, ls, cum);
+        w = kv_begin<KvBound::kShortLine>(a, qs, ls, cum);
         total = cum[a.n_seqs];
     }
     ahead[warp] = w;
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory");
         if (!whole) {
-            const KvPieces of = kv_pieces(a, w, total);
+            const KvPieces of = kv_pieces<KvBound::kShortLine>(a, w, total);
             auto meet = []() { asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kWarps) : "memory"); };
             join_pieces_in_runs(of, a.joined, tid == 0, &join_last, meet, [&](int first, int step, int count, bool final) {
                 // (no copy is under way then, but where a wait gave up)

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
     __syncthreads();
     if (!whole_items) {
         kv_schedule(a, qs, ls, cum);
-        if (warp == 0) walks[0] = kv_begin(a, qs, ls, cum);
+        if (warp == 0) walks[0] = kv_begin<KvBound::kLeastRun>(a, qs, ls, cum);
         __syncthreads();
     }
     tc_fence_after();
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                 }
                 if (sc != own_sc) m = kv_whole_max(m, sc, own_sc);
                 if (!whole) {
-                    of = kv_pieces(a, w, cum[a.n_seqs]);
+                    of = kv_pieces<KvBound::kLeastRun>(a, w, cum[a.n_seqs]);
                     if (of.count == 2 && lead()) {
                         int there;
                         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(joined() + of.c) : "memory");
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                 }
                 sc = next_sc;
             } else if (!whole) {
-                of = kv_pieces(a, w, cum[a.n_seqs]);
+                of = kv_pieces<KvBound::kLeastRun>(a, w, cum[a.n_seqs]);
                 direct = other_is_there();
             }
             tiles += cnt;
@@ -875,8 +875,9 @@ int launch_prefill8(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.tile_log2 = 7;
     a.min_units = 1;
     // An item in pieces takes the time of a piece and that of joining them, 1.9 us a tile and about as much a piece:
-    // least in all at pieces of about the square root of the item.  Without that bound, and with every item cut wherever the
-    // line's equal parts end, 64 tokens (16 heads of 4 kv heads) behind 1000 took 45 us, behind 5000 82; now 27 and 44.
+    // least in all at pieces of about the square root of the item, as long as one round joins those (items of 256
+    // tiles; longer ones are cut as fine as there are CTAs: 20 tokens of 2 kv heads behind 131,000 71 us, else 97).  Without
+    // that bound 64 tokens (16 heads of 4 kv heads) behind 1000 took 45 us, behind 5000 82 us; now 27 and 44.
     a.least_run = 1.0f / sqrtf((float)a.g.heads * (float)(((long long)a.n_tokens + (long long)a.n_seqs * (a.tq - 1)) / a.tq));
     a.pad = 4;
     a.whole_tiles = 12;  // (300 tokens behind 1000, items of up to 11 tiles: 30.6 us whole, 34 cut)
