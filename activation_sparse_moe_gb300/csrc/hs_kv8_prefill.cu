@@ -15,11 +15,14 @@
 // scale, a power of two, is exact in fp16, so keys and values are not rounded here.
 //
 // Bounds, for 256 rows x 128 keys at head_dim 128 on one SM: the products 2048
-// cycles at the dense fp16 rate; a row tile's scores, softmax and output follow one another, so that a
-// tile takes about 3500 for both, and an item some 12,000 more for filling, draining and writing.  The
-// converting warps' instructions compete with the softmax's: places of the tiles by
-// immediate offsets and one look a chunk for NaN instead of four took a prompt of 4096 tokens (32 / 8 heads) from
-// 179 to 150 us, 913 TFLOP/s, 48% of the measured bf16 peak; without any conversion it takes 146.
+// cycles at the dense fp16 rate, but a tile takes about 3500, the chain of a row tile: scores into registers 470,
+// their maximum 540, probabilities 1370, the products 1200, commits and wake-ups 300; the
+// other's chain runs under it.  An item takes some 12,000 more for filling, draining and writing.  No one resource
+// is full: without any conversion a prompt of 4096 tokens (32 / 8 heads) takes 142.6 us for 146.5 (935 TFLOP/s, 49%
+// of the measured bf16 peak), without exponentials 139.8; five stages of packed codes for three, a fourth or fifth
+// tile, and products that begin at half of the probabilities change nothing.  The converting warps' instructions
+// compete with the softmax's all the same: places of the tiles by immediate offsets and one look a chunk for
+// NaN instead of four took that prompt from 179 to 150 us.
 #include <cmath>
 
 #include "hs_kv4_join.cuh"
