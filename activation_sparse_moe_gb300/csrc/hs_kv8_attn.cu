@@ -659,8 +659,12 @@ int launch_rows8(KvAttnArgs& a, long long rows, int window, int sms, cudaStream_
 
 using namespace hs_host;
 
-// Rows of a request (new tokens x query heads of a kv head) from which the chunk kernel is used.
-constexpr int kPrefillRows = 33;
+// Rows of a request (new tokens x query heads of a kv head) that the few-row kernel takes: 32, and 64
+// of short or few items, whose start is shorter here.  us, this kernel and the chunk kernel, 40 to 64 rows of 128
+// channels: 32 items of up to 300 keys 12.9 and 13.8, of 1000 18.5 and 22, of 2000 21.8 and 22.9, but of 4000 28 and 26.9;
+// 48 items of 1000 19.9 and 22.1, but 64 of 700 20.8 and 18.7; 4 items of 16,000 33.2 and 35.5.  More than 32 requests, where the chunk kernel
+// gives no item to a CTA whole: 128 items of 300 20 and 26, of 700 26 and 28.7, 512 items of 1000 77 and 72.
+constexpr int kFewRows = 32, kFewRowsShort = 64;
 
 // The tensor-core kernel for chunks (hs_kv8_prefill.cu), and its device error word.
 int hs_kv8_prefill(hs::KvAttnArgs a, int dim, int sms, cudaStream_t stream);
@@ -717,8 +721,10 @@ extern "C" int hs_kv8_attention(const hs_kv8_cache* cache, const uint16_t* q, lo
     a.part_o = reinterpret_cast<float*>(w + round_up(rows * 8, 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const long long need = std::max((long long)max_new, 1ll) * a.group;
-    const long long items = (long long)n_seqs * a.g.heads, keys = items * ((long long)a.width << a.g.page_log2);
-    if (need >= (items <= 16 && keys <= 1 << 17 ? 65 : kPrefillRows)) return hs_kv8_prefill(a, dim, sms, s);
+    const long long items = (long long)n_seqs * a.g.heads, width = (long long)a.width << a.g.page_log2;
+    const long long keys = window ? std::min<long long>(width, window) : width;  // that a row may see
+    const bool brief = keys <= (n_seqs > 32 ? 768 : 384) || (items <= 48 && keys <= 2048) || (items <= 16 && items * keys <= 1 << 17);
+    if (need > (brief ? kFewRowsShort : kFewRows)) return hs_kv8_prefill(a, dim, sms, s);
     const int r = dim == 64 ? hs::launch_rows8<64>(a, need, window, sms, s) : hs::launch_rows8<128>(a, need, window, sms, s);
     return r != HS_OK ? r : launch_err();
 }

@@ -319,6 +319,23 @@ def test_short_items_of_few_requests(n, hkv, most, group, new, dim):
     _close(r.run(hs, 0.1, table=wide), r.expected(0.1), 0.1)
 
 
+@pytest.mark.parametrize("n,hkv,most,window", [(32, 4, 384, 0), (32, 4, 385, 0), (33, 3, 768, 0), (33, 3, 769, 0), (24, 2, 2048, 0), (24, 2, 2049, 0),
+                                               (25, 2, 1000, 0), (24, 2, 3000, 500), (150, 1, 700, 0), (4, 2, 5000, 333)])
+@pytest.mark.parametrize("group,new,dim", [(4, 16, 128), (11, 3, 64), (13, 5, 128)])
+def test_rows_of_short_items(n, hkv, most, window, group, new, dim):
+    """33 to 65 rows a request, at the numbers, widths and windows at which they go from one kernel to the other;
+    requests without rows among them, and a wide table that holds the same."""
+    rng = np.random.default_rng(n * most + group)
+    cached = [int(x) for x in rng.integers(0, most - new + 1, n)]
+    cached[n // 2] = most - new
+    fresh = [new if i == n // 2 or x > 0.2 else 0 for i, x in enumerate(rng.random(n))]
+    r = _kv8.Requests(n + most, cached, fresh, hkv * group, hkv, dim, 16)
+    ref = r.expected(0.1, window)
+    _close(r.run(hs, 0.1, window), ref, 0.1)
+    wide = torch.cat((torch.from_numpy(r.table), torch.full((n, 300), -1, dtype=torch.int32)), 1).cuda()
+    _close(r.run(hs, 0.1, window, table=wide), ref, 0.1)
+
+
 @pytest.mark.parametrize("n", [32, 33, 64, 100, 127, 128, 129, 300])
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_of_many_requests(n, new):
