@@ -319,7 +319,7 @@ def hs_kv4_pool_bytes(cache: hs_kv4_cache) -> int:
 # sizes, the slots' type, rows that do not follow one another.
 _current = None   # torch's own lookups of the current device and its raw stream
 _i64 = None       # torch.int64
-_i32 = _b16 = None  # and its int32 and bfloat16
+_i32 = _b16 = _f32 = None  # and its int32, bfloat16 and float32
 
 
 def _kv4_stream(stream):
@@ -335,11 +335,11 @@ def _kv4_stream(stream):
 
 def _kv4_refuse(fn):
     """The first call of a process looks at the tensors' types before they are known: True to look again."""
-    global _i64, _i32, _b16
+    global _i64, _i32, _b16, _f32
     if _i64 is not None:
         raise HsError(fn, HS_ERR_INVALID_ARG)
     import torch
-    _i64, _i32, _b16 = torch.int64, torch.int32, torch.bfloat16
+    _i64, _i32, _b16, _f32 = torch.int64, torch.int32, torch.bfloat16, torch.float32
     return True
 
 
@@ -444,13 +444,13 @@ def hs_kv8_append(cache: hs_kv8_cache, k, v, slots, n_tokens, stream=None):
 
 
 def hs_kv8_read(cache: hs_kv8_cache, slots, n_tokens, k_bf16=None, v_bf16=None, k_f32=None, v_f32=None, stream=None):
-    """As hs_kv4_read."""
+    """As hs_kv4_read; outputs of the types that their names say."""
     n = n_tokens * cache.n_kv_heads * cache.head_dim
     if (slots.dtype is not _i64 or not slots.is_contiguous() or slots.numel() < n_tokens
-            or (k_bf16 is not None and (k_bf16.numel() < n or not k_bf16.is_contiguous()))
-            or (v_bf16 is not None and (v_bf16.numel() < n or not v_bf16.is_contiguous()))
-            or (k_f32 is not None and (k_f32.numel() < n or not k_f32.is_contiguous()))
-            or (v_f32 is not None and (v_f32.numel() < n or not v_f32.is_contiguous()))):
+            or (k_bf16 is not None and (k_bf16.numel() < n or k_bf16.dtype is not _b16 or not k_bf16.is_contiguous()))
+            or (v_bf16 is not None and (v_bf16.numel() < n or v_bf16.dtype is not _b16 or not v_bf16.is_contiguous()))
+            or (k_f32 is not None and (k_f32.numel() < n or k_f32.dtype is not _f32 or not k_f32.is_contiguous()))
+            or (v_f32 is not None and (v_f32.numel() < n or v_f32.dtype is not _f32 or not v_f32.is_contiguous()))):
         if _kv4_refuse("hs_kv8_read"):
             return hs_kv8_read(cache, slots, n_tokens, k_bf16, v_bf16, k_f32, v_f32, stream)
     st = (_lib or lib()).hs_kv8_read(
@@ -472,7 +472,8 @@ def hs_kv8_attention(cache: hs_kv8_cache, q, q_start, seq_len, table, n_seqs, ma
     (qt, qh, qc), (ot, oh, oc), shape, (rows, width) = q.stride(), out.stride(), q.shape, table.shape
     tokens, heads, dim = shape
     if (qc != 1 or oc != 1 or dim != cache.head_dim or out.shape != shape or rows < n_seqs or not table.is_contiguous()
-            or q_start.numel() <= n_seqs or seq_len.numel() < n_seqs or q.dtype is not _b16 or out.dtype is not _b16):
+            or q_start.numel() <= n_seqs or seq_len.numel() < n_seqs or q.dtype is not _b16 or out.dtype is not _b16
+            or not (q_start.dtype is seq_len.dtype is table.dtype is _i32 and q_start.is_contiguous() and seq_len.is_contiguous())):
         if _kv4_refuse("hs_kv8_attention"):
             return hs_kv8_attention(cache, q, q_start, seq_len, table, n_seqs, max_new, scale, window, out, workspace, workspace_bytes,
                                     stream)

@@ -124,6 +124,28 @@ def test_binding_refuses_tensors_that_do_not_fit(lib):
                  table=[z(3, 32, t=i32)[:, :16], z(2, 16, t=i32), z(16, 3, t=i32).T]))
 
 
+def test_binding_refuses_other_types(lib):
+    """What the library would write past the end of (floats into bf16 rows) or misread (64-bit offsets, every other word)."""
+    import torch
+    b16, i32, i64, f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+    c = _cache(pool=A, n_pages=8, page=64, heads=2, dim=128)
+    rows = lambda t: torch.zeros(4, 2, 128, dtype=t)  # noqa: E731
+    read = dict(cache=c, slots=torch.zeros(4, dtype=i64), n_tokens=4, stream=0)
+    for name, bad in (("k_bf16", f32), ("v_bf16", torch.float16), ("k_f32", b16), ("v_f32", b16), ("k_f32", torch.float64)):
+        with pytest.raises(hs.HsError) as e:
+            hs.hs_kv8_read(**read, **{name: rows(bad)})
+        assert e.value.status == hs.HS_ERR_INVALID_ARG
+    words = lambda n, t: torch.zeros(n, dtype=t)  # noqa: E731
+    base = dict(cache=c, q=torch.zeros(4, 8, 128, dtype=b16), q_start=words(4, i32), seq_len=words(3, i32), table=torch.zeros(3, 16, dtype=i32),
+                n_seqs=3, max_new=2, scale=0.1, window=0, out=torch.zeros(4, 8, 128, dtype=b16), workspace=words(1, torch.uint8),
+                workspace_bytes=1 << 30, stream=0)
+    for name, bad in (("q_start", words(4, i64)), ("q_start", words(8, i32)[::2]), ("seq_len", words(3, i64)), ("seq_len", words(6, i32)[::2]),
+                      ("table", torch.zeros(3, 16, dtype=i64)), ("table", torch.zeros(3, 16, dtype=torch.int16))):
+        with pytest.raises(hs.HsError) as e:
+            hs.hs_kv8_attention(**{**base, name: bad})
+        assert e.value.status == hs.HS_ERR_INVALID_ARG
+
+
 # ------------------------------------------------ pins of the restatement
 def test_codes_by_hand():
     t = _kv8.TABLE
