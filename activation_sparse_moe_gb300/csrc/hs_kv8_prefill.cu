@@ -18,8 +18,8 @@
 // cycles at the dense fp16 rate, but a tile takes about 3500, the chain of a row tile: scores into registers 470,
 // their maximum 540, probabilities 1370, the products 1200, commits and wake-ups 300; the
 // other's chain runs under it.  An item takes some 12,000 more for filling, draining and writing.  No one resource
-// is full: without any conversion a prompt of 4096 tokens (32 / 8 heads) takes 142.6 us for 146.5 (935 TFLOP/s, 49%
-// of the measured bf16 peak), without exponentials 139.8; five stages of packed codes for three, a fourth or fifth
+// is full: without any conversion a prompt of 4096 tokens (32 / 8 heads), 143.2 us (960 TFLOP/s, 50% of the measured
+// bf16 peak), takes 4 us less, without exponentials 7; five stages of packed codes for three, a fourth or fifth
 // tile, and products that begin at half of the probabilities change nothing.  The converting warps' instructions
 // compete with the softmax's all the same: places of the tiles by immediate offsets and one look a chunk for
 // NaN instead of four took that prompt from 179 to 150 us.
@@ -505,13 +505,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
         bool dead = false;
         // The warp's 32 rows of a piece's queries, a row by D / 8 lanes: fetched as they are
         // into the lines of the tile that they will fill (16-byte chunk c of a row at place c
-        // of its line), ...
+        // of its line), ...  (Loops of little code, here and below: it runs once an item, when every role fetches
+        // instructions that it has not had for long.  Eight and four turns unrolled for two: 144.4 us for 143.0.)
         constexpr int kL = D / 8, kAt = 32 / kL, kB = 32 / kAt;  // lanes a row, rows at a time
         const int sub = lane / kL, c = lane % kL;
         uint8_t* q_lines = q_s + x * C::kQBytes + (c >> 3) * (128 * 128) + ((warp & 3) * 32 + sub) * 128;
         auto fetch_q = [&](const KvWalk& v) {
             const int nr = rows_of(v);
-#pragma unroll 8
+#pragma unroll 2
             for (int i = 0; i < kB; ++i) {
                 const int qr = x * 128 + (warp & 3) * 32 + i * kAt + sub, qt = kv_row_token(a, qr);
                 uint8_t* dst = q_lines + i * kAt * 128 + (c & 7) * 16;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
             __syncwarp();
             const uint8_t* own = q_s + x * C::kQBytes + ((warp & 3) * 32 + lane) * 128;
             uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < D / 8; ++i) {
                 const uint4 v = *reinterpret_cast<const uint4*>(own + (i >> 3) * (128 * 128) + (((i ^ lane) & 7) << 4));
                 const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
             const bool none = e >= kNoQuery;
             e = e == 0 || none ? 0 : max(-110, e - 127);  // a row of zeros keeps 2^8
             const float row_f = none ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 + 8 - e) << 23);
-#pragma unroll 4
+#pragma unroll 2
             for (int i = 0; i < kB; ++i) {
                 const float f = __shfl_sync(~0u, row_f, i * kAt + sub);
                 uint8_t* line = q_lines + i * kAt * 128;
@@ -633,11 +634,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
 #pragma unroll
                     for (int c = 0; c < kPfKeys / 32; ++c) tmem_ld32_async(tl + x * 128 + c * 32, v + c * 32);
                     tmem_ld_wait(v);
-                    if (masked) {
+                    if (masked) {  // (by bits: comparisons of each key, four instructions a score, took a prompt of 4096 from 144.4 to 146.8 us)
 #pragma unroll
-                        for (int i = 0; i < kPfKeys; ++i) {
-                            const int key = key0 + i;
-                            if (key > lim || key < low || ((gone >> (i >> 4)) & 1u)) v[i] = -INFINITY;
+                        for (int c = 0; c < kPfKeys / 32; ++c) {
+                            const int at = key0 + c * 32;
+                            uint32_t seen = lim < at ? 0u : ~0u >> (31 - min(lim - at, 31));
+                            if (low > at) seen &= low - at > 31 ? 0u : ~0u << (low - at);
+                            if ((gone >> (2 * c)) & 1u) seen &= 0xffff0000u;
+                            if ((gone >> (2 * c)) & 2u) seen &= 0x0000ffffu;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((seen >> i) & 1u)) v[c * 32 + i] = -INFINITY;
                         }
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -880,7 +887,7 @@ int launch_prefill8(KvAttnArgs& a, int sms, cudaStream_t s) {
     // An item in pieces takes the time of a piece and that of joining them, 1.9 us a tile and about as much a piece:
     // least in all at pieces of about the square root of the item, as long as one round joins those (items of 256
     // tiles; longer ones are cut as fine as there are CTAs: 20 tokens of 2 kv heads behind 131,000 71 us, else 97).  Without
-    // that bound 64 tokens (16 heads of 4 kv heads) behind 1000 took 45 us, behind 5000 82 us; now 27 and 44.
+    // that bound 64 tokens (16 heads of 4 kv heads) behind 1000 took 45 us, behind 5000 82 us; now 25 and 41.
     a.least_run = 1.0f / sqrtf((float)a.g.heads * (float)(((long long)a.n_tokens + (long long)a.n_seqs * (a.tq - 1)) / a.tq));
     a.pad = 4;
     a.whole_tiles = 12;  // (300 tokens behind 1000, items of up to 11 tiles: 30.6 us whole, 34 cut)
