@@ -55,6 +55,7 @@ struct PfShared {
     uint32_t tmem;
     // (Behind what every tile reads: before it, with those words elsewhere, chunks took 1% more.)
     uint64_t pieces_full, products_done;
+    uint64_t nan_read;  // row tile 1 has looked for NaN in the last tile of a piece
     int join_last[2];   // by row tile
     int direct[2][2];   // by end of the run (0: its first piece) and row tile: the item's other piece is there
 };
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             mbar_init(sh.q_full + i, 4), mbar_init(sh.s_full + i, 1), mbar_init(sh.p_full + i, 4), mbar_init(sh.o_full + i, 1);
         mbar_init(&sh.pieces_full, 1);
         mbar_init(&sh.products_done, 1);
+        mbar_init(&sh.nan_read, 4);
         fence_mbar_init();
     }
     if (tid < kPfInfo) {
@@ -298,7 +300,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | (1u << 16);  // V: rows along K
         const uint32_t q_at = smem_u32(q_s), kv_at = smem_u32(kv_s);
         uint32_t slot = 0, phase = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};  // slot: of the next K tile
-        bool dead = false;
+        uint32_t nan_phase = 0;
+        bool dead = false, two_before = false;  // the piece before had two row tiles
         auto wait = [&](uint64_t* bar, uint32_t parity) { dead |= !warp_wait(bar, parity); };
         while (w.left > 0 && !dead) {
             const int cnt = (int)warp_max_u32((uint32_t)kv_piece_tiles(w));
@@ -307,6 +310,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
             for (int k = 0; k <= cnt && !dead; ++k) {
                 // tile k's scores and tile k - 1's outputs, a row tile at a time
                 if (k) wait(sh.kv_full + v_slot, v_phase);
+                // What is known of NaN in the last tile of the piece before is cleared four tiles on, by warps
+                // that need this tile of V free.  Row tile 0 has looked by then (its probabilities
+                // are here), row tile 1, where this piece has none, need not have.
+                if (k == 1 && two_before) {
+                    wait(&sh.nan_read, nan_phase);
+                    nan_phase ^= 1;
+                }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if ((x && !two) || dead) continue;
@@ -356,6 +366,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                     slot = next;
                 }
             }
+            two_before = two;
             next_piece();
         }
         // The products read shared memory and write tensor memory, which is given back below.
@@ -653,6 +664,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                 if (!dead) {
                     tc_fence_after();
                     see_nan(cnt - 1);
+                    if (x) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.nan_read);
+                    }
                     const uint32_t at = (2 * blockIdx.x + (w.tile == 0 ? 1 : 0)) * (uint32_t)a.rows + r;
                     // The other piece's row, and the weights of both: the operations of add_pieces,
                     // so that the result is the same whoever comes last.

@@ -19,7 +19,7 @@ def _lib():
     hs.lib()
 
 
-@pytest.mark.parametrize("bits", [8])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_nan_of_items_of_two_row_tiles_before_items_of_one(bits, dim):
     """Requests of 160 rows whose last tile of keys holds a NaN value that some rows see, and longer ones of 80

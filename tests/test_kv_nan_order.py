@@ -120,7 +120,7 @@ def test_without_the_wait_a_late_row_tile_loses_what_was_known():
     assert not any(run(r, 0, False) for r in RUNS)
 
 
-@pytest.mark.parametrize("kernel", ["hs_kv8_prefill.cu"])
+@pytest.mark.parametrize("kernel", ["hs_kv4_prefill.cu", "hs_kv8_prefill.cu"])
 @pytest.mark.parametrize("late", [None, 0, 1])
 def test_a_late_row_tile_finds_what_is_known_of_nan(kernel, late):
     src = drains._squeeze(kernel)
