@@ -27,6 +27,31 @@ __device__ __forceinline__ uint8_t* kv_record(const KvGeom& g, int page, int hea
     return g.pool + ((size_t)page * g.heads + head) * (size_t)g.rec;  // past 4 GB in a long cache: 64 bits
 }
 
+// A power of two for each of a lane's query rows (n, e) in the few-row kernels; more than four, for
+// which registers do not suffice, by their exponent fields, a byte each.
+template <int NQ>
+struct RowPowers {
+    float v[NQ][2];
+    __device__ __forceinline__ explicit RowPowers(uint32_t field) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) v[n][0] = v[n][1] = __uint_as_float(field << 23);
+    }
+    __device__ __forceinline__ float operator()(int n, int e) const { return v[n][e]; }
+    __device__ __forceinline__ uint32_t field(int n, int e) const { return __float_as_uint(v[n][e]) >> 23; }
+    __device__ __forceinline__ void set(int n, int e, uint32_t field) { v[n][e] = __uint_as_float(field << 23); }
+};
+template <>
+struct RowPowers<4> {
+    uint32_t v[2];
+    __device__ __forceinline__ explicit RowPowers(uint32_t field) { v[0] = v[1] = field * 0x01010101u; }
+    __device__ __forceinline__ float operator()(int n, int e) const {
+        const int at = (2 * n + e) % 4;
+        return __uint_as_float((at == 3 ? v[n / 2] >> 1 : v[n / 2] << (23 - 8 * at)) & 0x7f800000u);
+    }
+    __device__ __forceinline__ uint32_t field(int n, int e) const { return (v[n / 2] >> ((2 * n + e) % 4 * 8)) & 255u; }
+    __device__ __forceinline__ void set(int n, int e, uint32_t now) { v[n / 2] += (now - field(n, e)) << ((2 * n + e) % 4 * 8); }
+};
+
 // bulk_g2s with shared-memory addresses of the 32-bit window.
 __device__ __forceinline__ void bulk_g2s_to(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
     asm volatile(

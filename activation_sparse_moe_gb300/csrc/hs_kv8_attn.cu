@@ -257,9 +257,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
         constexpr int kV = D / 8;  // channels of a lane
         float O[kV / 2][NQ][4];
         float m[NQ][2], l[NQ][2];
-        // The largest exponent of a value scale so far (its field in fp32): probability *
-        // scale * 2^(6 + 127 - eb) is at most 2^14.
-        uint32_t eb = 127 + kKv8Low;
+        // A row's largest value scale so far 2^e, of the blocks that it sees (others say nothing
+        // about it): probability * scale * 2^(6 - e) is at most 2^14.  up: 2^(6 - e); low: the
+        // smallest e of the lane's rows, as the field of 2^e in fp32.
+        RowPowers<NQ> up(127 + 6 - kKv8Low);
+        uint32_t low = 127 + kKv8Low;
         // Some row goes by another factor than its scores' own (kv_score_factor).  Those
         // then stand in the second words of merge_ml, which are the warp's until the piece ends.
         bool far = false;
@@ -302,8 +304,8 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
                     }
                 }
                 const float2 scale = *reinterpret_cast<const float2*>(scales + 16 * h);
-                // what lies behind the last key, or in a page that is not there, may be anything
-                vs[h] = !MASKED || (key0 + 16 * h < w.len && !((none >> h) & 1u)) ? scale.y : 0.f;
+                // what no row sees may be anything: behind the last key, before the window, in a page that is not there
+                vs[h] = !MASKED || (key0 + 16 * h <= max_lim && key0 + 16 * h + 15 >= back_min && !((none >> h) & 1u)) ? scale.y : 0.f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -325,11 +327,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) grow |= fmaf(largest(n, e), sc[n][e], -m[n][e]) > kLazy;
-            if (__any_sync(~0u, grow || top > eb)) {  // rare: a maximum passed the lag, or a scale the exponent
-                const uint32_t neb = min(max(eb, top), 127u + kKv8High);
-                const float down = __uint_as_float((127u + eb - neb) << 23);
-                eb = neb;
+            if (__any_sync(~0u, grow || top > low)) {  // rare: a maximum passed the lag, or a scale a row's exponent
                 bool over = far;
+                low = 255;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -339,6 +339,18 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
                         const float y = x * sc[n][e], nm = fmaxf(m[n][e], y), f = ex2(m[n][e] - nm);
                         m[n][e] = nm;
+                        uint32_t see = top;  // of the blocks of which the row sees a key
+                        if (MASKED) {
+                            const int row = row0 + n * 8 + 2 * t + e, lim = ctx + w.r * a.tq + kv_row_token(a, row), from = max(lim, 0) - back_keys;
+                            see = 0;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (key0 + 16 * h <= lim && key0 + 16 * h + 15 >= from) see = max(see, __float_as_uint(vs[h]) >> 23);
+                        }
+                        const uint32_t was = up.field(n, e), now = min(was, 254u + 6u - min(see, 127u + kKv8High));
+                        const float down = __uint_as_float((127u + now - was) << 23);
+                        up.set(n, e, now);
+                        low = min(low, 254u + 6u - now);
                         over |= fabsf(y) >= kFarScore && y > kNoMax;  // (-infinity: the row sees no key of these)
                         l[n][e] *= f;
 #pragma unroll
@@ -364,20 +376,21 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float ke = vs[h] * __uint_as_float((127u + 6u + 127u - eb) << 23);
                 uint32_t B[NQ][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int n = 0; n < NQ; ++n) {
+                    const float ke[2] = {vs[h] * up(n, 0), vs[h] * up(n, 1)};
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
+                    for (int j = 0; j < 2; ++j) {
                         float x[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             x[e] = ex2(fmaf(s[h][j][n][e], sc[n][e], -m[n][e]));
                             l[n][e] += x[e];
                         }
-                        B[n][j] = transpose_8x8(pack_half2(x[0] * ke, x[1] * ke));
+                        B[n][j] = transpose_8x8(pack_half2(x[0] * ke[0], x[1] * ke[1]));
                     }
+                }
                 // the codes of keys t, t + 4, t + 8 and t + 12: kV channels from kV g on
                 constexpr int kW = kV / 4;
                 uint32_t c[4][kW];
@@ -502,13 +515,14 @@ __global__ void __launch_bounds__(32 * RT * KW, (Decode8Cfg<D, NQ, RT, KW>::kCta
                 for (int e = 0; e < 2; ++e) m[n][e] = kv_whole_max(m[n][e], sc[n][e], own_sc[n * 8 + e].y);
             __syncwarp();
         }
-        const float back_to = __uint_as_float((eb - 6u) << 23);
 #pragma unroll
-        for (int u = 0; u < kV / 2; ++u)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int e = 0; e < 2; ++e) {
+                const float back_to = __uint_as_float((254u << 23) - __float_as_uint(up(n, e)));  // 2^(e - 6)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) O[u][n][e] *= back_to;
+                for (int u = 0; u < kV / 2; ++u) O[u][n][e] *= back_to, O[u][n][2 + e] *= back_to;
+            }
         // The key warps' sums meet in shared memory; then a warp takes a row at a time,
         // adds them in the order of the warps and writes the row, as output or as a piece.
 #pragma unroll

@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                 // tile k's scores and tile k - 1's outputs, a row tile at a time
                 if (k) wait(sh.kv_full + v_slot, v_phase);
                 // What is known of NaN in the last tile of the piece before is cleared four tiles on, by warps
-                // that need this tile of V free.  Row tile 0 has looked by then (its probabilities
-                // are here), row tile 1, where this piece has none, need not have.
+                // that need this tile of V free.  Row tile 0 has looked before its probabilities
+                // come; row tile 1, where this piece has none, need not have.
                 if (k == 1 && two_before) {
                     wait(&sh.nan_read, nan_phase);
                     nan_phase ^= 1;
