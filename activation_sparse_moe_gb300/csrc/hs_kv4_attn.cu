@@ -275,9 +275,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
         // Lane: outputs of channels 64 i + 8 g + 2 u + (e / 2), rows 2t + e % 2.
         float O[NG][4][NQ][4];
         float m[NQ][2], l[NQ][2], bs[NG][NQ][2];
-        // Exponent field of the largest value scale so far: probability * scale *
-        // 2^(21 - eb) stays below 2^15.
-        uint32_t eb = 0;
+        // A row's largest value scale so far, of the keys that it sees (others say nothing about
+        // it), by its exponent field eb: probability * scale * 2^(21 - eb) stays below 2^15.
+        // up: 2^(21 - eb); low: the smallest eb of the lane's rows.
+        RowPowers<NQ> up(148);
+        uint32_t low = 0;
         // Some row goes by another factor than its scores' own (kv_score_factor).  Those
         // then stand in the second words of merge_ml, which are the warp's until the piece ends.
         bool far = false;
@@ -313,8 +315,9 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint8_t* pk = rec + (16 * h + 8 * j + kr) * (NG * 4);
-                    // what lies behind the last key may be anything
-                    const bool there = !MASKED || (key0 + 16 * h + 8 * j + kr < w.len && !((none >> h) & 1u));
+                    // what no row sees may be anything: behind the last key, before the window, in a page that is not there
+                    const int key = key0 + 16 * h + 8 * j + kr;
+                    const bool there = !MASKED || (key <= max_lim && key >= back_min && !((none >> h) & 1u));
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
                         kp[h][j][i] = there ? reinterpret_cast<const uint32_t*>(pk + kKp)[i] : 0;
@@ -376,11 +379,10 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) grow |= fmaf(largest(n, e), sc[n][e], -m[n][e]) > kLazy;
-            if (__any_sync(~0u, grow || top > eb << 10)) {  // rare: a maximum passed the lag, or a scale the exponent
-                const uint32_t neb = max(eb, warp_max_u32(top) >> 10);
-                const float down = __uint_as_float((127u + eb - neb) << 23);
-                eb = neb;
+            if (__any_sync(~0u, grow || top > low << 10)) {  // rare: a maximum passed the lag, or a scale a row's exponent
                 bool over = far;
+                const uint32_t all = warp_max_u32(top) >> 10;
+                low = 31;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -388,8 +390,25 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                         float x = largest(n, e);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+                        uint32_t see = all;  // the largest exponent of the scales of keys that the row sees
+                        if (MASKED) {
+                            see = 0;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                    for (int i = 0; i < NG; ++i)
+                                        if (s[h][j][n][e] != -INFINITY) see = max(see, (vp[h][j][i] >> 10) & 31u);
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) see = max(see, __shfl_xor_sync(~0u, see, o));
+                        }
                         const float y = x * sc[n][e], nm = fmaxf(m[n][e], y), f = ex2(m[n][e] - nm);
                         m[n][e] = nm;
+                        const uint32_t was = up.field(n, e), now = min(was, 148u - see);
+                        const float down = __uint_as_float((127u + now - was) << 23);
+                        up.set(n, e, now);
+                        low = min(low, 148u - now);
                         over |= fabsf(y) >= kFarScore && y > kNoMax;  // (-infinity: the row sees no key of these)
                         l[n][e] *= f;
 #pragma unroll
@@ -419,16 +438,12 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float ke = __uint_as_float((148u - eb) << 23);
                 uint32_t B[NG][NQ][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float2 p[NG];
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) {
-                        p[i] = half2_to_float2(vp[h][j][i]);
-                        p[i].x *= ke;
-                    }
+                    for (int i = 0; i < NG; ++i) p[i] = half2_to_float2(vp[h][j][i]);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         float x[2];
@@ -444,7 +459,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                             for (int e = 0; e < 2; ++e) {
                                 const bool hide = MASKED && s[h][j][n][e] == -INFINITY;  // a key that the row does not see may hold a NaN
                                 bs[i][n][e] = hide ? bs[i][n][e] : fmaf(x[e], p[i].y, bs[i][n][e]);
-                                y[e] = hide ? 0.f : x[e] * p[i].x;
+                                y[e] = hide ? 0.f : x[e] * up(n, e) * p[i].x;
                             }
                             B[i][n][j] = transpose_8x8(pack_half2(y[0], y[1]));
                         }
@@ -514,7 +529,11 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                 for (int e = 0; e < 2; ++e) m[n][e] = kv_whole_max(m[n][e], sc[n][e], own_sc[n * 8 + e].y);
             __syncwarp();
         }
-        const float even = __uint_as_float((uint32_t)(127 + 24 - 21 + (int)eb) << 23);  // 2^24 / 2^(21 - eb)
+        float even[NQ][2];  // 2^24 / 2^(21 - eb)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) even[n][e] = __uint_as_float((278u << 23) - __float_as_uint(up(n, e)));
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(32 * RT * KW, (DecodeCfg<D, NQ, RT, KW>::kCtas
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        O[i][u][n][e] = fmaf(O[i][u][n][e], e < 2 ? even : even * 0.0625f, bs[i][n][e & 1]);
+                        O[i][u][n][e] = fmaf(O[i][u][n][e], e < 2 ? even[n][e & 1] : even[n][e & 1] * 0.0625f, bs[i][n][e & 1]);
         // The key warps' sums meet in shared memory; then a warp takes a row at a time,
         // adds them in the order of the warps and writes the row, as output or as a piece.
 #pragma unroll

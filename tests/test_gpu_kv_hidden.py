@@ -60,7 +60,7 @@ def _sizes(big):
     return edit
 
 
-@pytest.mark.parametrize("bits", [8])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("new,hq,dim", [(1, 2, 64), (1, 16, 128), (3, 8, 128), (4, 16, 64), (8, 8, 64), (8, 8, 128), (12, 8, 128), (16, 8, 128)])
 @pytest.mark.parametrize("page", [16, 64])
 def test_large_values_before_the_window(bits, new, hq, dim, page):
@@ -73,7 +73,7 @@ def test_large_values_before_the_window(bits, new, hq, dim, page):
     _bounded(r, bits, r.run(hs, 0.1, window), 0.1, window)
 
 
-@pytest.mark.parametrize("bits", [8])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("hq,dim", [(2, 64), (4, 128), (8, 64), (8, 128), (16, 128)])
 @pytest.mark.parametrize("window", [0, 60])
 def test_large_values_behind_a_rows_border(bits, hq, dim, window):
@@ -83,7 +83,7 @@ def test_large_values_behind_a_rows_border(bits, hq, dim, window):
     _bounded(r, bits, r.run(hs, 0.1, window), 0.1, window)
 
 
-@pytest.mark.parametrize("bits", [8])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("hq,dim", [(2, 64), (4, 128), (8, 64), (8, 128), (16, 128)])
 def test_large_values_that_only_the_first_rows_windows_reach(bits, hq, dim):
     """The window's border passes key 112 between the fourth row and the fifth; key 111 is large."""
@@ -92,7 +92,7 @@ def test_large_values_that_only_the_first_rows_windows_reach(bits, hq, dim):
 
 
 @pytest.mark.parametrize("kind", ["ones", "infinite", "largest", "negative"])
-@pytest.mark.parametrize("bits", [8])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("new,hq,dim", [(1, 4, 128), (3, 8, 64), (8, 8, 128)])
 def test_memory_before_every_window_that_was_never_written(kind, bits, new, hq, dim):
     """Tokens before the window that were not appended (slots of -1): their blocks hold codes and
