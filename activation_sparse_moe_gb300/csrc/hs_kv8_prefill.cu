@@ -433,6 +433,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
         bool dead = false;
         for (; w.left > 0 && !dead; next_piece()) {
             const int cnt = kv_piece_tiles(w), len = w.len;
+            const int begin = max(len - w.n + w.r * a.tq, 0) - a.back;  // the item's rows see no key before it
             int key0 = (w.lo + w.tile) * kPfKeys;
             for (int k = 0; k < cnt && !dead; ++k, ++tiles, key0 += kPfKeys) {
                 const int info = tiles % kPfInfo;
@@ -459,11 +460,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv8_prefill_kernel(const KvAttn
                         if (idx == 8) sh.nan_any[on] = 0;
                         else sh.nan_keys[on][idx >> 2][idx & 3] = 0;
                     }
-                    if (gone || key0 + kPfKeys > len) {  // what lies behind the last key, or in a page that is not there, may be anything
+                    // what lies behind the last key, before every row's window, or in a page that is not there, may be anything
+                    if (gone || key0 + kPfKeys > len || key0 < begin) {
 #pragma unroll
                         for (int i = 0; i < kMine; ++i) {
                             const int in_tile = half * kPfHalf + first + i * kApart;
-                            if (key0 + in_tile >= len || (gone >> (in_tile >> 4 & 7)) & 1u) q[i] = make_uint4(0, 0, 0, 0), scale[i] = 1.f;
+                            if (key0 + in_tile >= len || key0 + in_tile < begin || (gone >> (in_tile >> 4 & 7)) & 1u) q[i] = make_uint4(0, 0, 0, 0), scale[i] = 1.f;
                         }
                     }
                     if (v) {  // a NaN value must not meet the zero probability of a row that does not see it

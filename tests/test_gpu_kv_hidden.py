@@ -93,10 +93,12 @@ def test_large_values_that_only_the_first_rows_windows_reach(bits, hq, dim):
 
 @pytest.mark.parametrize("kind", ["ones", "infinite", "largest", "negative"])
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("new,hq,dim", [(1, 4, 128), (3, 8, 64), (8, 8, 128)])
+@pytest.mark.parametrize("new,hq,dim", [(1, 4, 128), (3, 8, 64), (8, 8, 128), (40, 8, 128), (70, 4, 64), (300, 2, 128)])
 def test_memory_before_every_window_that_was_never_written(kind, bits, new, hq, dim):
     """Tokens before the window that were not appended (slots of -1): their blocks hold codes and
     scales that no append writes."""
+    if bits == 4 and new * hq // 2 > 64:
+        pytest.skip("chunks")
     length = 300 + new
     window = 93
     first = length - new - window + 1               # the first key that some row sees: 208, in the middle of a step of 32
