@@ -380,6 +380,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
         bool dead = false;
         for (; w.left > 0 && !dead; next_piece()) {
             const int cnt = kv_piece_tiles(w);
+            // the item's rows see `span` keys from `begin` on, or fewer
+            const int begin = max(max(w.len - w.n + w.r * a.tq, 0) - a.back, 0);
+            const uint32_t span = (uint32_t)(w.len - begin);
             for (int k = 0; k < cnt && !dead; ++k, ++tiles) {
                 const int key0 = (w.lo + w.tile + k) * kPfKeys, info = tiles % kPfInfo;
                 for (int v = 0; v < 2; ++v, ++f) {
@@ -404,7 +407,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) kv4_prefill_kernel(const KvAttn
                         if (kItems % (32 * kPfApart) == 0 || id < kItems) {
                             q[i] = *reinterpret_cast<const uint4*>(from + key * (D / 2) + c * 16);
                             sb[i] = *reinterpret_cast<const uint32_t*>(from + kPfKeys * (D / 2) + (key * NG + (c >> 1)) * 4);
-                            if (key0 + key >= w.len || (gone >> (key >> 4)) & 1u) sb[i] = 0;
+                            // what lies behind the last key, before every row's window, or in a page that is not there, may be anything
+                            if ((uint32_t)(key0 + key - begin) >= span || (gone >> (key >> 4)) & 1u) sb[i] = 0;
                             nan |= (sb[i] & 0x7c000000u) == 0x7c000000u;
                         }
                     }
