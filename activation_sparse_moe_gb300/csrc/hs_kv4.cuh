@@ -9,7 +9,8 @@ namespace hs {
 
 constexpr int kKvMaxSeqs = 4096;
 constexpr int kKvMaxTokens = 1 << 20;   // tokens of one append or read
-constexpr long long kKvMaxKeys = (1ll << 31) - (1 << 13);  // of a table's row: the loads look some 4000 keys ahead in 32 bits
+constexpr int kKvAhead = 1 << 13;       // keys by which a position may be passed in 32 bits (each kernel asserts what it does)
+constexpr long long kKvMaxKeys = (1ll << 31) - kKvAhead;  // of a table's row
 
 struct KvGeom {
     uint8_t* pool;

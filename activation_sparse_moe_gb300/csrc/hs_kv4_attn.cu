@@ -649,6 +649,7 @@ int launch_decode(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.pad = RT == 1 ? 6 : 4;
     const int ctas = std::min(152, sms) * C::kCtas;
     static_assert(2 * 152 * C::kCtas * C::kRows <= kKvWsRows && 152 * C::kCtas <= kKvMaxCtas, "workspace");
+    static_assert(kKvTile + 31 * KW * kKvStep + 16 <= kKvAhead, "32 table entries of a warp's steps, from any key of a row's last tile");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
     if (hs_host::launch_pdl(kv4_decode_kernel<D, NQ, RT, KW>, dim3(ctas), dim3(C::kThreads), smem, s, a) != cudaSuccess)
         return HS_ERR_CUDA;

@@ -842,6 +842,7 @@ int launch_prefill(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.min_units = 1;
     a.pad = 4;
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
+    static_assert(2 * kPfKeys <= kKvAhead, "keys of a tile");
     static_assert(PrefillCfg<D>::smem(kKvMaxSeqs) <= kPfMaxSmem, "shared memory");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
     if (hs_host::launch_pdl(kv4_prefill_kernel<D>, dim3(std::min(152, sms)), dim3(kPfThreads), PrefillCfg<D>::smem(a.n_seqs), s, a) !=

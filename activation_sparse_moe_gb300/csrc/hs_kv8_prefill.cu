@@ -909,6 +909,7 @@ int launch_prefill8(KvAttnArgs& a, int sms, cudaStream_t s) {
     a.pad = 4;
     a.whole_tiles = 12;  // (300 tokens behind 1000, items of up to 11 tiles: 30.6 us whole, 34 cut)
     static_assert(2 * 152 * kPfRows <= kKvWsRows, "workspace");
+    static_assert(2 * kPfKeys <= kKvAhead, "keys of a tile");
     static_assert(Prefill8Cfg<D>::smem(kKvMaxSeqs) <= kPfMaxSmem, "shared memory");
     if (!kv_line_ok(a)) return HS_ERR_UNSUPPORTED_SHAPE;
     if (hs_host::launch_pdl(kv8_prefill_kernel<D>, dim3(std::min(152, sms)), dim3(kPfThreads), Prefill8Cfg<D>::smem(a.n_seqs), s, a) !=
