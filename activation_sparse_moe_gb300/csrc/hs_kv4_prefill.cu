@@ -21,7 +21,7 @@
 // other arithmetic about 1000 issue cycles, taking codes apart about 500.  A
 // row tile's scores, softmax and output follow one another (tensor memory holds
 // no second set of scores beside 2 x 128 columns of scores and outputs at head_dim 128), so
-// that a tile takes 3500 cycles for both; an item costs some 12,000 more: filling,
+// that a tile takes 3800 cycles for both; an item costs some 12,000 more: filling,
 // draining, writing.  A prompt of 4096 tokens (32 / 8 heads of 128 channels):
 // 148 us, 926 TFLOP/s, 48% of the measured bf16 peak; within long items 1340 TFLOP/s.
 #include "hs_kv4_join.cuh"

@@ -1,5 +1,5 @@
 // Division of the attention's work among the CTAs of one launch, shared by
-// the kernels of hs_kv4_attention.
+// the kernels of hs_kv4_attention and hs_kv8_attention.
 //
 // An item is (request, kv head, row tile): the row tile holds TQ of the
 // request's new tokens for all G query heads of the kv head.  Its work is the

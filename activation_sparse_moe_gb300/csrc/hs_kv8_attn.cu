@@ -5,7 +5,10 @@
 // Mathematics.  With k_j = 2^e c_j, e the exponent of the key's block of 16,
 //   q . k_j = 2^e (q . c_j),
 // so the matrix product runs on the codes, and a block's scale acts on 16 rows of one
-// product.  The values' scales fold into the probabilities, o = sum_j (p_j 2^e) c_j.
+// product.  The values' scales fold into the probabilities, o = sum_j (p_j 2^e) c_j, which go to fp16 under
+// a power of two of each row's own, that of the largest scale among the blocks that the row sees: what it does not
+// see leaves its roundings alone.  (Powers a row cost 0.7 of 13.4 us in 16 x 3 windowed drafts, 2% in other short calls
+// and nothing in long ones.)
 // e4m3 is exact in fp16, by one conversion for two codes.  Each query row is scaled by the power
 // of two that brings its largest channel to [2^8, 2^9), whatever stands in the others:
 // bf16 values down to 2^-25 of it then lose nothing as fp16, smaller ones move a
@@ -654,7 +657,7 @@ int launch_decode8(KvAttnArgs& a, int sms, cudaStream_t s) {
 // of 8000 13.2 and 16.6 (4 rows 10.5 and 11.3), of 500 7.7 and 10.0 (6.0 and 7.1); 128 items of up to 1000 11.1 and
 // 15.2 (9.2 and 12.2); but 32 items of up to 4000 17.4 and 16.6 (14.3 and 12.0), 128 of up to 2000 22.2
 // and 19.4 (17.8 and 15.4), and up to 128 keys 5.8 and 5.6.  At 64 channels registers hold 32 rows
-// a warp: 64 windowed items of 18 rows and 1000 keys 12.7 and 14.4 (of up to 4000 keys 21.5 and
+// a warp: 64 windowed items of 18 rows and 1000 keys 13.3 and 14.6 (of up to 4000 keys 21.5 and
 // 20.5).  The host knows the tables' width and the window only, not the lengths.
 template <int D>
 int launch_rows8(KvAttnArgs& a, long long rows, int window, int sms, cudaStream_t s) {

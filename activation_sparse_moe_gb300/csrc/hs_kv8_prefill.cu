@@ -15,10 +15,10 @@
 // scale, a power of two, is exact in fp16, so keys and values are not rounded here.
 //
 // Bounds, for 256 rows x 128 keys at head_dim 128 on one SM: the products 2048
-// cycles at the dense fp16 rate, but a tile takes about 3500, the chain of a row tile: scores into registers 470,
-// their maximum 540, probabilities 1370, the products 1200, commits and wake-ups 300; the
-// other's chain runs under it.  An item takes some 12,000 more for filling, draining and writing.  No one resource
-// is full: without any conversion a prompt of 4096 tokens (32 / 8 heads), 143.2 us (960 TFLOP/s, 50% of the measured
+// cycles at the dense fp16 rate, but a tile takes 3760 (1.82 us), the chain of a row tile, in a trace
+// that slows it by some 3%: scores into registers 470, their maximum 540, probabilities 1370, the
+// products 1200, commits and wake-ups 300; the other's chain runs under it.  An item takes some 12,000 more for filling, draining and writing.  No one resource
+// is full: without any conversion a prompt of 4096 tokens (32 / 8 heads), 143.9 us (955 TFLOP/s, 50% of the measured
 // bf16 peak), takes 4 us less, without exponentials 7; five stages of packed codes for three, a fourth or fifth
 // tile, and products that begin at half of the probabilities change nothing.  The converting warps' instructions
 // compete with the softmax's all the same: places of the tiles by immediate offsets and one look a chunk for

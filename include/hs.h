@@ -397,6 +397,8 @@ size_t hs_kv4_pool_bytes(const hs_kv4_cache* cache);
  *                  refused as a whole: no request gets a page or a token
  *                  (q_start all 0, slots -1, seq_len = cached_len); ended
  *                  requests still give their pages back.
+ * An ended request's pages go to the ring whoever else lists them: where rows
+ * share pages (hs_kv_fork), a request ends by hs_kv_release instead.
  * Of what the call writes (the ring among it) nothing may overlap anything else
  * (HS_ERR_INVALID_ARG), table_out_dev as table_in_dev apart: the next step's
  * lengths and counters are other buffers than this one's, or copies.
@@ -444,8 +446,9 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  *   q_bf16_dev, out_bf16_dev  bf16, n_tokens rows, strides as in hs_kv4_append
  *   q_start_dev [n_seqs + 1] ascending, seq_len_dev [n_seqs]
  *   table_dev   [n_seqs][table_width]; a length past table_width pages is cut
- *   max_new     the largest number of new tokens of a request, or more: it
- *               chooses the kernel, and with it the roundings, not the result
+ *   max_new     the largest number of new tokens of a request, or more: with
+ *               n_seqs, the heads, the table's width and the window it chooses
+ *               the kernel, and with it the roundings, not the result
  *   scale       > 0, at most 10^30 (scores past the fp32 range say nothing);
  *   window      >= 0 (0: none)
  * n_seqs 1..4096; n_q_heads a multiple of n_kv_heads, at most 64 times it;
@@ -455,7 +458,8 @@ int hs_kv4_read(const hs_kv4_cache* cache, const long long* slot_dev, int n_toke
  * values (chunks) with fp16 queries, each row scaled by a power of two of its
  * own, fp32 sums, probabilities rounded to fp16 for the second product.  A
  * query row that holds a NaN or an infinity gives NaN where it sees a key, and
- * no other row.
+ * no other row.  What a row does not see does not touch it, whatever stands
+ * there; what no row of a request sees need not have been written.
  * Scores are held to fp32 at any size; past 2^21 (of their base-2 logarithms) a
  * row's are levelled to 2^-20 of the largest.
  * Deterministic.  Calls sharing one workspace must not overlap on the GPU.
@@ -505,7 +509,8 @@ size_t hs_kv8_pool_bytes(const hs_kv8_cache* cache);
  * are the ones in front of the first new one; where the scale grows, they are rounded
  * again at the new one (their codes move towards zero by powers of two: what was not
  * below 2^-6 of the new scale stays exact).  A block whose first token is new begins
- * anew, whatever stood there.
+ * anew, whatever stood there; one whose first tokens were skipped goes by the scale that
+ * stands there (the smallest, where the pool was zero-filled).
  *   code = e4m3(x / 2^e), round to nearest, ties to even
  * A group of 64 channels of a token that holds a NaN or a magnitude past 57344
  * (448 * 2^7) reads back as NaN and says nothing about the scale.  A slot outside the
@@ -607,7 +612,8 @@ int hs_kv_copy_pages(void* const* pools, int n_pools, long long page_bytes, int 
 /* Cuts each row back to its first keep_len tokens (0: the request ends; as many as
  * it holds or more: nothing happens).  A page that a row gives up loses an owner; one
  * that had none beyond the row goes to the end of the ring.  The pages of one call
- * go there in ascending order.
+ * go there in ascending order.  (A look at a mark for each of n_pages is part of it: one
+ * short request ends in 4.6 us in a pool of 2000 pages, in 24 us in one of 300,000.)
  *   cached_len_dev, keep_len_dev [n_seqs];  table_in_dev [n_seqs][table_width]
  *   shared_dev, ring_dev [n_pages], in and out
  *   table_out_dev  -1 past a row's pages; it may be table_in_dev, whose entries past
